@@ -492,6 +492,159 @@ int paro_mxfp4_linear_prepared(const paro_w4_layer *layer, const void *hl, const
                                paro_dtype y_dt, void *workspace, size_t workspace_bytes, void *stream);
 size_t paro_mxfp4_linear_prepared_workspace_bytes(const paro_w4_layer *layer, int64_t tokens);
 
+/*
+ * Between a decoder layer's q/k/v projections and its output projection:
+ * attention over packed prompts, attention of one new token over a paged
+ * key-value cache, and the cache itself (pages granted, written, shared
+ * between sequences, freed and compacted on the device, so that a whole
+ * serving step can be captured into a graph).
+ *
+ * For query row i of a sequence with n_q query rows and n_k keys, head h
+ * reading key-value head h / (q_heads / kv_heads):
+ *   s_j = scale * (q_i . k_j)      for j <= i + n_k - n_q  (all j if !causal)
+ *   y_i = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),     m = max_j s_j
+ * so the last query row sees every key.  A row that may see no key
+ * (i + n_k < n_q, or n_k = 0) gives zeros; what stands in keys and values a
+ * row may not see, infinities and NaN included, does not reach it.  Scores,
+ * maxima, sums and outputs are held in fp32; the weights exp(s - m) are
+ * rounded to the activation dtype (at most 1, relative error half a step)
+ * for the matrix cores, and the sum is taken over the rounded weights, so
+ * they add up to one; y is rounded once.
+ * GPU limits: head_dim 64 or 128, q_heads a multiple of kv_heads and at most
+ * 256, strides non-negative multiples of 8 elements below 2^40, tensors
+ * 16-byte aligned.
+ */
+typedef struct {
+  int32_t q_heads, kv_heads, head_dim;
+  int32_t causal;                 /* 0: every row sees every key of its sequence */
+  float scale;                    /* finite; usually 1 / sqrt(head_dim)          */
+  int64_t q_token, q_head;        /* strides in elements: row r, head h of q     */
+  int64_t k_token, k_head;        /*   starts at q + r * q_token + h * q_head    */
+  int64_t v_token, v_head;        /* k and v strides: packed prompts only        */
+  int64_t y_token, y_head;
+} paro_attention_shape;
+
+/*
+ * A paged key-value cache: host struct of sizes and DEVICE pointers.  Pages
+ * hold page_size (16, 32, 64, 128 or 256) positions of one sequence, for all
+ * kv_heads and all layers of a model; the same page index serves K, V and
+ * every layer.  Position p of the sequence in slot s lies in page
+ * table[s][p / page_size], row p % page_size.
+ *   A slot is empty when lengths[s] == 0.  In a valid state the first
+ *   ceil(lengths[s] / page_size) entries of table[s] are pages, the others
+ *   are -1, and refs[p] counts the entries that hold page p (0: free).
+ *   paro_kv_fork, _reserve, _free and _compact keep a valid state valid.
+ *   Start: lengths 0, refs 0, table -1 everywhere.
+ * Table entries and lengths are not read on the host; kernels clamp them, so
+ * an invalid state yields wrong numbers, never an out-of-bounds access.
+ * GPU limits: slots <= 4096, num_pages <= 2^22, max_pages <= 2^20 and
+ * max_pages * page_size <= 2^30, layers <= 1024, kv_heads <= 256; k and v
+ * 16-byte aligned, refs, table and lengths 4-byte aligned.
+ */
+typedef struct {
+  int32_t layers, kv_heads, head_dim, page_size;
+  int64_t num_pages;
+  int32_t slots, max_pages;
+  paro_dtype dt;        /* PARO_F16 or PARO_BF16                              */
+  void *k, *v;          /* [layers][num_pages][kv_heads][page_size][head_dim] */
+  int32_t *refs;        /* [num_pages]                                        */
+  int32_t *table;       /* [slots][max_pages]                                 */
+  int32_t *lengths;     /* [slots] positions held                             */
+} paro_kv_cache;
+
+/*
+ * Attention over prompts packed one after another.
+ *   q [q_tokens][q_heads][head_dim], k, v [k_tokens][kv_heads][head_dim],
+ *   y like q: dt in {F16, BF16}, with the strides of `shape` (views into a
+ *   fused q/k/v buffer are fine).  y's rows and heads must not overlap each
+ *   other, q, k or v.
+ *   cu_q, cu_k : DEVICE int64 [sequences + 1], 8-byte aligned: sequence s
+ *   has query rows cu_q[s]..cu_q[s+1] and keys cu_k[s]..cu_k[s+1].  Expected
+ *   nondecreasing from 0 to q_tokens (k_tokens); entries are clamped into
+ *   that range and a sequence that would end before it starts is empty.
+ *   Rows of y outside every sequence are not written.
+ * sequences in 0..65536, q_tokens and k_tokens <= 2^21.
+ */
+int paro_attention_prompt(const paro_attention_shape *shape, const void *q, const void *k, const void *v,
+                          paro_dtype dt, const int64_t *cu_q, const int64_t *cu_k, int64_t sequences,
+                          int64_t q_tokens, int64_t k_tokens, void *y, void *stream);
+/*
+ * The same over the cache: the keys and values of sequence i are all
+ * lengths[slots[i]] positions of its slot in layer `layer`, its query rows
+ * cu_q[i]..cu_q[i+1] the newest of them (so a chunk of a prompt sees the
+ * cached prefix before it; call paro_kv_reserve and paro_kv_append for the
+ * chunk first).  slots: DEVICE int32 [sequences]; a slot outside the cache
+ * counts as empty.  shape's heads and head_dim must be the cache's; k and v
+ * strides are not used.  q and y must not overlap the cache.
+ */
+int paro_attention_prompt_cached(const paro_kv_cache *cache, int layer, const paro_attention_shape *shape,
+                                 const void *q, const int32_t *slots, const int64_t *cu_q, int64_t sequences,
+                                 int64_t q_tokens, void *y, void *stream);
+/*
+ * One new token per sequence: row r of q [rows][q_heads][head_dim] attends
+ * to all lengths[slots[r]] positions of its slot (its own among them, see
+ * paro_kv_append).  A slot may appear in several rows.  An empty slot or one
+ * outside the cache gives zeros.
+ *   workspace: paro_attention_decode_workspace_bytes bytes, 16-byte aligned,
+ *   zero-filled before its first use with this library; each completed call
+ *   leaves its counters zero.  Calls that overlap in time need separate
+ *   ones.  The split of the length depends on rows, q_heads and the cache's
+ *   sizes and on each length alone, and parts are joined in order: a
+ *   repeated call gives identical bits.
+ * rows <= 65536.
+ */
+int paro_attention_decode(const paro_kv_cache *cache, int layer, const paro_attention_shape *shape, const void *q,
+                          const int32_t *slots, int64_t rows, void *y, void *workspace, size_t workspace_bytes,
+                          void *stream);
+size_t paro_attention_decode_workspace_bytes(const paro_kv_cache *cache, int64_t rows, int q_heads);
+
+/*
+ * New K and V rows into the pages of one layer: rows cu[i]..cu[i+1] of k and
+ * v [tokens][kv_heads][head_dim] (cache dtype, strides in elements as in
+ * paro_attention_shape) become the newest positions of slot slots[i], i.e.
+ * lengths[slots[i]] - (cu[i+1] - cu[i]) and up, which paro_kv_reserve has
+ * granted before.  cu: DEVICE int64 [n + 1], or NULL for one row per entry
+ * (tokens == n).  n <= 65536.  Rows whose position or page does not exist
+ * are skipped; of entries that name the same slot the first one counts and
+ * the others are skipped.  Nothing else of the cache is written.
+ */
+int paro_kv_append(const paro_kv_cache *cache, int layer, const void *k, int64_t k_token, int64_t k_head,
+                   const void *v, int64_t v_token, int64_t v_head, const int32_t *slots, const int64_t *cu,
+                   int64_t n, int64_t tokens, void *stream);
+/*
+ * Room for grow[i] >= 0 new positions in slot slots[i], i < n <= 4096
+ * (DEVICE int32 arrays): lengths grow, missing pages are taken from the free
+ * ones in ascending order, and a last page that is shared and not full is
+ * replaced by a copy of it in all layers (copy on write).
+ * granted[i] (DEVICE int32 [n], written): 1, or 0 with the slot left as it
+ * was: its slot or growth is out of range, it would exceed max_pages, an
+ * earlier entry names the same slot, or the pages that it and the entries
+ * before it need are more than are free.
+ * workspace: paro_kv_workspace_bytes(cache) bytes, 16-byte aligned; needs no
+ * clearing; the same holds for paro_kv_fork and paro_kv_compact.
+ */
+int paro_kv_reserve(const paro_kv_cache *cache, const int32_t *slots, const int32_t *grow, int64_t n,
+                    int32_t *granted, void *workspace, size_t workspace_bytes, void *stream);
+/*
+ * The empty slot children[i] becomes a copy of slot parents[i] that shares
+ * its pages (no page is copied), i < n <= 4096.  granted[i]: 1, or 0
+ * with nothing done: a slot is out of range, the child is not empty, is its
+ * own parent, or is named by an earlier entry.  Parents are taken as they
+ * were before the call.
+ */
+int paro_kv_fork(const paro_kv_cache *cache, const int32_t *parents, const int32_t *children, int64_t n,
+                 int32_t *granted, void *workspace, size_t workspace_bytes, void *stream);
+/* Empties the slots slots[i], i < n <= 4096; their pages are given up
+ * (and are free once no other slot holds them).  Slots out of range and
+ * repeated entries are ignored. */
+int paro_kv_free(const paro_kv_cache *cache, const int32_t *slots, int64_t n, void *stream);
+/* Moves the pages in use to the lowest indices, in all layers, with `used`
+ * (DEVICE int32 [1]) set to their number: the i-th used page at or above
+ * that number goes, in ascending order, to the i-th free page below it. */
+int paro_kv_compact(const paro_kv_cache *cache, int32_t *used, void *workspace, size_t workspace_bytes,
+                    void *stream);
+size_t paro_kv_workspace_bytes(const paro_kv_cache *cache);
+
 /* Bytes of workspace the linear needs for this shape and path (0 allowed). */
 size_t paro_w4a16_linear_workspace_bytes(const paro_w4_layer *layer, int64_t tokens,
                                          paro_dtype x_dt, paro_path path);

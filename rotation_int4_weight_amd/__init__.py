@@ -20,7 +20,10 @@ from ._lib import (BF16, EXPORTS, F16, F32, PATH_AUTO, PATH_DECODE_FUSED, PATH_D
                    paro_w4a16_moe_linear_workspace_bytes, paro_mxfp4_quantize_weight,
                    paro_mxfp4_quantize_activations, paro_mxfp4_gemm, paro_mxfp4_linear,
                    paro_mxfp4_linear_workspace_bytes, paro_mxfp4_activation_workspace_bytes,
-                   paro_mxfp4_linear_prepared, paro_mxfp4_linear_prepared_workspace_bytes)
+                   paro_mxfp4_linear_prepared, paro_mxfp4_linear_prepared_workspace_bytes,
+                   KVCache, paro_attention_prompt, paro_attention_prompt_cached, paro_attention_decode,
+                   paro_attention_decode_workspace_bytes, paro_kv_append, paro_kv_reserve, paro_kv_fork,
+                   paro_kv_free, paro_kv_compact, paro_kv_workspace_bytes)
 
 __all__ = ["BF16", "EXPORTS", "F16", "F32", "PATH_AUTO", "PATH_DECODE_FUSED", "PATH_DECODE_SPLIT",
            "PATH_PREFILL", "DeviceLayer", "ParoError", "load", "make_workspace", "paro_abi_version",
@@ -36,4 +39,7 @@ __all__ = ["BF16", "EXPORTS", "F16", "F32", "PATH_AUTO", "PATH_DECODE_FUSED", "P
            "paro_w4a16_moe_linear_workspace_bytes", "paro_mxfp4_quantize_weight",
            "paro_mxfp4_quantize_activations", "paro_mxfp4_gemm", "paro_mxfp4_linear",
            "paro_mxfp4_linear_workspace_bytes", "paro_mxfp4_activation_workspace_bytes",
-           "paro_mxfp4_linear_prepared", "paro_mxfp4_linear_prepared_workspace_bytes"]
+           "paro_mxfp4_linear_prepared", "paro_mxfp4_linear_prepared_workspace_bytes",
+           "KVCache", "paro_attention_prompt", "paro_attention_prompt_cached", "paro_attention_decode",
+           "paro_attention_decode_workspace_bytes", "paro_kv_append", "paro_kv_reserve", "paro_kv_fork",
+           "paro_kv_free", "paro_kv_compact", "paro_kv_workspace_bytes"]

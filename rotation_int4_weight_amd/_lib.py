@@ -36,7 +36,10 @@ EXPORTS = ("paro_scale_rotate", "paro_w4_unpack_dequant", "paro_w4a16_linear",
            "paro_scale_rotate_tiled", "paro_w4a16_linear_tiled",
            "paro_w4a16_linear_workspace_bytes",
            "paro_w4a16_linear_choose_path", "paro_validate_layer", "paro_last_error",
-           "paro_abi_version")
+           "paro_abi_version", "paro_attention_prompt", "paro_attention_prompt_cached",
+           "paro_attention_decode", "paro_attention_decode_workspace_bytes", "paro_kv_append",
+           "paro_kv_reserve", "paro_kv_fork", "paro_kv_free", "paro_kv_compact",
+           "paro_kv_workspace_bytes")
 
 
 class ParoError(RuntimeError):
@@ -52,6 +55,23 @@ class ParoLayerC(ctypes.Structure):
                 ("channel_scales", ctypes.c_void_p), ("qweight", ctypes.c_void_p),
                 ("qzeros", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("bias", ctypes.c_void_p)]
+
+
+class ParoAttentionShapeC(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64),
+                ("y_token", ctypes.c_int64), ("y_head", ctypes.c_int64)]
+
+
+class ParoKvCacheC(ctypes.Structure):
+    _fields_ = [("layers", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int64), ("slots", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("dt", ctypes.c_int), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p)]
 
 
 _lib = None
@@ -109,6 +129,18 @@ def load(path: str | None = None):
     lib.paro_w4a16_linear_workspace_bytes.restype = SZ
     lib.paro_w4a16_linear_choose_path.argtypes = [P, I64]
     lib.paro_validate_layer.argtypes = [P]
+    lib.paro_attention_prompt.argtypes = [P, P, P, P, I32, P, P, I64, I64, I64, P, P]
+    lib.paro_attention_prompt_cached.argtypes = [P, I32, P, P, P, P, I64, I64, P, P]
+    lib.paro_attention_decode.argtypes = [P, I32, P, P, P, I64, P, P, SZ, P]
+    lib.paro_attention_decode_workspace_bytes.argtypes = [P, I64, I32]
+    lib.paro_attention_decode_workspace_bytes.restype = SZ
+    lib.paro_kv_append.argtypes = [P, I32, P, I64, I64, P, I64, I64, P, P, I64, I64, P]
+    lib.paro_kv_reserve.argtypes = [P, P, P, I64, P, P, SZ, P]
+    lib.paro_kv_fork.argtypes = [P, P, P, I64, P, P, SZ, P]
+    lib.paro_kv_free.argtypes = [P, P, I64, P]
+    lib.paro_kv_compact.argtypes = [P, P, P, SZ, P]
+    lib.paro_kv_workspace_bytes.argtypes = [P]
+    lib.paro_kv_workspace_bytes.restype = SZ
     lib.paro_last_error.argtypes = []
     lib.paro_last_error.restype = ctypes.c_char_p
     lib.paro_abi_version.argtypes = []
@@ -120,7 +152,9 @@ def load(path: str | None = None):
                  "paro_mxfp4_linear",
                  "paro_rotation_matrix", "paro_scale_rotate_tiled", "paro_w4a16_linear_tiled",
                  "paro_w4a16_linear_choose_path",
-                 "paro_validate_layer", "paro_abi_version"):
+                 "paro_validate_layer", "paro_abi_version", "paro_attention_prompt",
+                 "paro_attention_prompt_cached", "paro_attention_decode", "paro_kv_append", "paro_kv_reserve",
+                 "paro_kv_fork", "paro_kv_free", "paro_kv_compact"):
         getattr(lib, name).restype = I32
     if path == LIB_PATH:
         _lib = lib
@@ -418,3 +452,201 @@ def paro_w4a16_linear_tiled(layer: DeviceLayer, x_t, x_dt: int, tokens: int, y, 
     """The prefill contraction over X_r in the tiled layout; y: (tokens, O) x dtype or fp32."""
     _check(load().paro_w4a16_linear_tiled(layer.ref, _ptr(x_t), x_dt, tokens, _ptr(y), _dt(y),
                                           _stream_handle(stream)), "paro_w4a16_linear_tiled")
+
+
+# ---- attention and the key-value cache ----
+
+class KVCache:
+    """A paged key-value cache: its tensors and the C descriptor (paro_kv_cache).
+
+    k, v: (layers, pages, kv_heads, page_size, head_dim) fp16/bf16; refs: (pages,), table: (slots, max_pages),
+    lengths: (slots,), int32; contiguous, on one device.  KVCache.empty() makes them.
+    """
+
+    def __init__(self, k, v, refs, table, lengths):
+        import torch
+        what = "KVCache"
+        _need(k.dim() == 5 and v.shape == k.shape, 2, what, "k and v: (layers, pages, kv_heads, page_size, head_dim)")
+        _need(k.dtype in (torch.float16, torch.bfloat16) and v.dtype == k.dtype, 3, what, "k and v: fp16 or bf16")
+        _need(refs.shape == (k.shape[1],) and table.dim() == 2 and lengths.shape == (table.shape[0],), 2, what,
+              "refs (pages,), table (slots, max_pages), lengths (slots,)")
+        _need(all(t.dtype == torch.int32 for t in (refs, table, lengths)), 3, what, "refs, table and lengths: int32")
+        _need(all(t.is_contiguous() and t.device == k.device for t in (k, v, refs, table, lengths)), 2, what,
+              "contiguous tensors on one device")
+        self.k, self.v, self.refs, self.table, self.lengths = k, v, refs, table, lengths
+        layers, pages, kv_heads, page_size, head_dim = k.shape
+        self.c = ParoKvCacheC(layers, kv_heads, head_dim, page_size, pages, table.shape[0], table.shape[1], _dt(k),
+                              k.data_ptr(), v.data_ptr(), refs.data_ptr(), table.data_ptr(), lengths.data_ptr())
+
+    @classmethod
+    def empty(cls, layers, pages, kv_heads, page_size, head_dim, slots, max_pages, dtype, device="cuda"):
+        """A cache with all slots empty and all pages free."""
+        import torch
+        shape = (layers, pages, kv_heads, page_size, head_dim)
+        return cls(torch.zeros(shape, dtype=dtype, device=device), torch.zeros(shape, dtype=dtype, device=device),
+                   torch.zeros(pages, dtype=torch.int32, device=device),
+                   torch.full((slots, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(slots, dtype=torch.int32, device=device))
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.c)
+
+
+def _need(good, status: int, what: str, msg: str):
+    if not good:
+        raise ParoError(status, what, msg)
+
+
+def _scratch(workspace, device, what):
+    """Bytes of a workspace tensor (0 for None, which the library refuses)."""
+    if workspace is None:
+        return 0
+    _need(workspace.is_contiguous() and workspace.device == device, 7, what, f"workspace: a contiguous tensor on {device}")
+    return workspace.numel() * workspace.element_size()
+
+
+def _index(t, dtype, n, device, what, name):
+    _need(t.dtype == dtype and t.dim() == 1 and t.is_contiguous() and t.device == device, 3, what,
+          f"{name}: a contiguous 1-d {dtype} tensor on {device}")
+    if n is not None:
+        _need(t.numel() == n, 2, what, f"{name} has {t.numel()} entries, {n} expected")
+
+
+def _rows(t, like, what, name):
+    """A (tokens, heads, head_dim) view with channels together, of like's dtype and device."""
+    _need(t.dim() == 3 and (t.stride(2) == 1 or t.numel() == 0), 2, what,
+          f"{name}: (tokens, heads, head_dim) with contiguous channels")
+    _need(t.dtype == like.dtype and t.device == like.device, 3, what, f"{name}: {like.dtype} on {like.device}")
+
+
+def _launch(fn, device, stream, *args):
+    """Calls fn(*args, stream) with `device` current; the stream defaults to that device's current one."""
+    import torch
+    _need(device.type == "cuda", 1, fn.__name__, f"tensors in device memory are required, not on {device}")
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream_handle(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream_handle(stream))
+
+
+def _shape_of(q, y, kv_heads, scale, causal, k=None, v=None):
+    d = q.shape[2]
+    s = ParoAttentionShapeC(q.shape[1], kv_heads, d, int(bool(causal)), d ** -0.5 if scale is None else scale,
+                            q.stride(0), q.stride(1), 0, 0, 0, 0, y.stride(0), y.stride(1))
+    if k is not None:
+        s.k_token, s.k_head, s.v_token, s.v_head = k.stride(0), k.stride(1), v.stride(0), v.stride(1)
+    return s
+
+
+def paro_attention_prompt(q, k, v, cu_q, cu_k, y, scale=None, causal=True, stream=None) -> None:
+    """q, y: (tokens, q_heads, head_dim); k, v: (keys, kv_heads, head_dim), fp16/bf16 views; cu_q, cu_k: int64
+    (sequences + 1,) device tensors; scale: 1 / sqrt(head_dim) if None."""
+    import torch
+    what = "paro_attention_prompt"
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (y, "y")):
+        _rows(t, q, what, name)
+    _need(y.shape == q.shape and k.shape == v.shape and k.shape[2] == q.shape[2], 2, what,
+          "y like q, v like k, one head_dim")
+    _index(cu_q, torch.int64, None, q.device, what, "cu_q")
+    _index(cu_k, torch.int64, cu_q.numel(), q.device, what, "cu_k")
+    _need(cu_q.numel() > 0, 2, what, "cu_q has sequences + 1 entries")
+    s = _shape_of(q, y, k.shape[1], scale, causal, k, v)
+    _check(_launch(load().paro_attention_prompt, q.device, stream, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _dt(q),
+                   _ptr(cu_q), _ptr(cu_k), cu_q.numel() - 1, q.shape[0], k.shape[0], _ptr(y)), what)
+
+
+def paro_attention_prompt_cached(cache: KVCache, layer: int, q, slots, cu_q, y, scale=None, causal=True,
+                                 stream=None) -> None:
+    """q, y: (tokens, q_heads, head_dim) of the cache's dtype: the newest rows of the slots; slots: int32
+    (sequences,); cu_q: int64 (sequences + 1,)."""
+    import torch
+    what = "paro_attention_prompt_cached"
+    for t, name in ((q, "q"), (y, "y")):
+        _rows(t, cache.k, what, name)
+    _need(y.shape == q.shape, 2, what, "y like q")
+    _index(slots, torch.int32, None, cache.k.device, what, "slots")
+    _index(cu_q, torch.int64, slots.numel() + 1, cache.k.device, what, "cu_q")
+    s = _shape_of(q, y, cache.c.kv_heads, scale, causal)
+    _check(_launch(load().paro_attention_prompt_cached, q.device, stream, cache.ref, layer, ctypes.byref(s), _ptr(q),
+                   _ptr(slots), _ptr(cu_q), slots.numel(), q.shape[0], _ptr(y)), what)
+
+
+def paro_attention_decode_workspace_bytes(cache: KVCache, rows: int, q_heads: int) -> int:
+    return int(load().paro_attention_decode_workspace_bytes(cache.ref, rows, q_heads))
+
+
+def paro_attention_decode(cache: KVCache, layer: int, q, slots, y, workspace, scale=None, stream=None) -> None:
+    """q, y: (rows, q_heads, head_dim), one new token per row; slots: int32 (rows,); workspace: zero-filled before
+    its first use, of paro_attention_decode_workspace_bytes() bytes."""
+    import torch
+    what = "paro_attention_decode"
+    for t, name in ((q, "q"), (y, "y")):
+        _rows(t, cache.k, what, name)
+    _need(y.shape == q.shape, 2, what, "y like q")
+    _index(slots, torch.int32, q.shape[0], cache.k.device, what, "slots")
+    ws_bytes = _scratch(workspace, cache.k.device, what)
+    s = _shape_of(q, y, cache.c.kv_heads, scale, True)
+    _check(_launch(load().paro_attention_decode, q.device, stream, cache.ref, layer, ctypes.byref(s), _ptr(q),
+                   _ptr(slots), q.shape[0], _ptr(y), _ptr(workspace), ws_bytes), what)
+
+
+def paro_kv_append(cache: KVCache, layer: int, k, v, slots, cu=None, stream=None) -> None:
+    """k, v: (tokens, kv_heads, head_dim) of the cache's dtype become the newest positions of the slots: rows
+    cu[i]..cu[i + 1] of slot slots[i] (int32), one row per slot if cu (int64) is None."""
+    import torch
+    what = "paro_kv_append"
+    for t, name in ((k, "k"), (v, "v")):
+        _rows(t, cache.k, what, name)
+    _need(k.shape == v.shape and tuple(k.shape[1:]) == (cache.c.kv_heads, cache.c.head_dim), 2, what,
+          f"k and v: (tokens, {cache.c.kv_heads}, {cache.c.head_dim})")
+    _index(slots, torch.int32, None, cache.k.device, what, "slots")
+    if cu is not None:
+        _index(cu, torch.int64, slots.numel() + 1, cache.k.device, what, "cu")
+    _check(_launch(load().paro_kv_append, k.device, stream, cache.ref, layer, _ptr(k), k.stride(0), k.stride(1),
+                   _ptr(v), v.stride(0), v.stride(1), _ptr(slots), _ptr(cu), slots.numel(), k.shape[0]), what)
+
+
+def paro_kv_workspace_bytes(cache: KVCache) -> int:
+    """Workspace bytes of paro_kv_reserve, paro_kv_fork and paro_kv_compact."""
+    return int(load().paro_kv_workspace_bytes(cache.ref))
+
+
+def _plan_call(fn, what, cache, lists, workspace, stream):
+    import torch
+    n = lists[0][1].numel()
+    for name, t in lists:
+        _index(t, torch.int32, n, cache.k.device, what, name)
+    ws_bytes = _scratch(workspace, cache.k.device, what)
+    ptrs = [_ptr(t) for _, t in lists]
+    _check(_launch(fn, cache.k.device, stream, cache.ref, ptrs[0], ptrs[1], n, ptrs[2], _ptr(workspace), ws_bytes),
+           what)
+
+
+def paro_kv_reserve(cache: KVCache, slots, grow, granted, workspace, stream=None) -> None:
+    """Room for grow[i] new positions in slot slots[i]; granted[i] is set to 1 or 0 (int32 tensors)."""
+    _plan_call(load().paro_kv_reserve, "paro_kv_reserve", cache,
+               [("slots", slots), ("grow", grow), ("granted", granted)], workspace, stream)
+
+
+def paro_kv_fork(cache: KVCache, parents, children, granted, workspace, stream=None) -> None:
+    """The empty slot children[i] shares the pages of slot parents[i]; granted[i] is set to 1 or 0."""
+    _plan_call(load().paro_kv_fork, "paro_kv_fork", cache,
+               [("parents", parents), ("children", children), ("granted", granted)], workspace, stream)
+
+
+def paro_kv_free(cache: KVCache, slots, stream=None) -> None:
+    """Empties the slots (int32 tensor) and gives up their pages."""
+    import torch
+    _index(slots, torch.int32, None, cache.k.device, "paro_kv_free", "slots")
+    _check(_launch(load().paro_kv_free, cache.k.device, stream, cache.ref, _ptr(slots), slots.numel()),
+           "paro_kv_free")
+
+
+def paro_kv_compact(cache: KVCache, used, workspace, stream=None) -> None:
+    """Moves the pages in use to the lowest indices; used: int32 (1,), set to their number."""
+    import torch
+    _index(used, torch.int32, 1, cache.k.device, "paro_kv_compact", "used")
+    ws_bytes = _scratch(workspace, cache.k.device, "paro_kv_compact")
+    _check(_launch(load().paro_kv_compact, cache.k.device, stream, cache.ref, _ptr(used), _ptr(workspace), ws_bytes),
+           "paro_kv_compact")

@@ -1,0 +1,71 @@
+// attention.hpp - internal host launchers of the attention and key-value
+// cache kernels.  attention_abi.cpp validates every argument before calling
+// these; all pointers are device pointers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "paro.h"
+
+namespace paro {
+
+constexpr int kMaxSlots = 4096;      // the planning kernels keep per-slot tables in LDS
+constexpr int kMaxSequences = 65536;
+
+// One layer of a paged cache as the kernels see it.
+struct KvLayer {
+  uint16_t *k, *v;         // the layer's pages [num_pages][kv_heads][page_size][head_dim]
+  const int32_t *table;    // [slots][max_pages]
+  const int32_t *lengths;  // [slots]
+  int64_t page_stride;     // elements per page: kv_heads * page_size * head_dim
+  int num_pages, max_pages, slots;
+  int page_shift;          // log2(page_size)
+};
+
+struct AttentionArgs {
+  const uint16_t *q, *k, *v;  // k, v: packed prompts only
+  uint16_t *y;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, y_token, y_head;  // elements
+  int q_heads, kv_heads, group;  // group = q_heads / kv_heads
+  int head_dim, dt, causal;
+  float scale;
+  int64_t q_tokens, k_tokens;
+  const int64_t *cu_q, *cu_k;
+  const int32_t *slots;  // cache forms
+  int sequences;         // prompts: sequences; decode: rows
+  KvLayer kv;            // cache forms
+};
+
+// Prompts: K and V packed (cached = false) or in the cache's pages.
+hipError_t launch_attention_prompt(const AttentionArgs &a, bool cached, hipStream_t st);
+
+// One token per row over the cache.  The length of a row is split over
+// `splits` workgroups where there are few (row, key-value head, head tile)
+// items; with more than kDecodeCounters of them the chip is full and
+// splits == 1, so a fixed counter area at the start of every workspace serves
+// all shapes and stays zero between calls.
+constexpr int kDecodeCounters = 16384;
+struct DecodeAttentionPlan {
+  int splits;
+  int head_tiles;  // workgroups per key-value head: its query heads in tiles of 16
+};
+DecodeAttentionPlan plan_attention_decode(int64_t rows, int q_heads, int kv_heads, int64_t max_len);
+size_t attention_decode_partial_bytes(const DecodeAttentionPlan &p, int64_t rows, int kv_heads, int head_dim);
+hipError_t launch_attention_decode(const AttentionArgs &a, const DecodeAttentionPlan &p, uint32_t *counters,
+                                   float *partials, hipStream_t st);
+
+hipError_t launch_kv_append(const KvLayer &kv, int kv_heads, int head_dim, const uint16_t *k, int64_t k_token,
+                            int64_t k_head, const uint16_t *v, int64_t v_token, int64_t v_head, const int32_t *slots,
+                            const int64_t *cu, int n, int64_t tokens, hipStream_t st);
+
+// Page bookkeeping.  work: kv_work_ints(c) int32.
+size_t kv_work_ints(const paro_kv_cache &c);
+hipError_t launch_kv_reserve(const paro_kv_cache &c, const int32_t *slots, const int32_t *grow, int n,
+                             int32_t *granted, int32_t *work, hipStream_t st);
+hipError_t launch_kv_fork(const paro_kv_cache &c, const int32_t *parents, const int32_t *children, int n,
+                          int32_t *granted, int32_t *work, hipStream_t st);
+hipError_t launch_kv_free(const paro_kv_cache &c, const int32_t *slots, int n, hipStream_t st);
+hipError_t launch_kv_compact(const paro_kv_cache &c, int32_t *used, int32_t *work, hipStream_t st);
+
+}  // namespace paro

@@ -11,12 +11,15 @@
 #include <string>
 #include <vector>
 
+#include "abi.hpp"
 #include "launch.hpp"
 #include "paro.h"
 
-namespace {
+namespace paro {
 
+namespace {
 thread_local std::string g_last_error;
+}
 
 int fail(int code, const char *fmt, ...) {
   char buf[512];
@@ -33,7 +36,21 @@ int ok() {
   return PARO_OK;
 }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+int hip_fail(hipError_t e, const char *what) {
+  return fail(PARO_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+}  // namespace paro
+
+namespace {
+
+using paro::act_dtype;
+using paro::align_up;
+using paro::aligned;
+using paro::fail;
+using paro::hip_fail;
+using paro::ok;
+using paro::overlap;
 
 constexpr int64_t kMaxTokens = int64_t(1) << 21;  // keeps every grid dimension < 65536
 constexpr int kMaxKrot = 64;
@@ -124,19 +141,6 @@ int check_tokens(int64_t tokens) {
   return PARO_OK;
 }
 
-bool act_dtype(int dt) { return dt == PARO_F16 || dt == PARO_BF16; }
-
-int hip_fail(hipError_t e, const char *what) {
-  return fail(PARO_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-bool overlap(const void *a, size_t an, const void *b, size_t bn) {
-  const char *pa = (const char *)a, *pb = (const char *)b;
-  return an && bn && pa < pb + bn && pb < pa + an;
-}
-
 paro::LinearArgs linear_args(const paro_w4_layer *L, int64_t tokens, const void *x, paro_dtype x_dt, void *y,
                              paro_dtype y_dt) {
   paro::LinearArgs a;
@@ -194,7 +198,7 @@ extern "C" {
 
 int paro_abi_version(void) { return PARO_ABI_VERSION; }
 
-const char *paro_last_error(void) { return g_last_error.c_str(); }
+const char *paro_last_error(void) { return paro::g_last_error.c_str(); }
 
 int paro_validate_layer(const paro_w4_layer *L) {
   int rc = check_method_shape(L);

@@ -1,0 +1,307 @@
+"""Prompt and decode attention through the C-ABI against the definition in 64
+bits: head layouts, ragged and empty sequences, rows that see no key, strides,
+masked NaN, streams, and refusals that only the binding can make."""
+import pytest
+
+from _attention import cached_rows, check_rows, default_scale, filled_cache, offsets, randn
+
+torch = pytest.importorskip("torch")
+paro = pytest.importorskip("rotation_int4_weight_amd")
+
+pytestmark = pytest.mark.gpu
+
+HEADS = [(1, 1), (4, 1), (7, 1), (32, 8), (6, 2), (40, 2)]
+TYPES = [torch.float16, torch.bfloat16]
+NAN = float("nan")
+
+
+def run_prompt(q_counts, k_counts, heads, kv_heads, dim, dtype, causal=True, scale=None, seed=0, qs=1.5):
+    q = randn((sum(q_counts), heads, dim), dtype, seed, qs)
+    k = randn((sum(k_counts), kv_heads, dim), dtype, seed + 1)
+    v = randn((sum(k_counts), kv_heads, dim), dtype, seed + 2)
+    y = torch.full_like(q, NAN)
+    paro.paro_attention_prompt(q, k, v, offsets(q_counts), offsets(k_counts), y, scale=scale, causal=causal)
+    torch.cuda.synchronize()
+    q0 = k0 = 0
+    for a, b in zip(q_counts, k_counts):
+        check_rows(y[q0:q0 + a], q[q0:q0 + a], k[k0:k0 + b], v[k0:k0 + b],
+                   default_scale(dim) if scale is None else scale, causal)
+        q0, k0 = q0 + a, k0 + b
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads", HEADS)
+def test_prompt_heads(heads, dim, dtype):
+    run_prompt([33, 1, 70], [33, 1, 70], *heads, dim, dtype)
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, torch.bfloat16), (128, torch.float16)])
+@pytest.mark.parametrize("counts", [[1], [2], [31], [32], [33], [63, 64, 65], [127, 128, 129], [0, 5, 0, 0, 1, 0],
+                                    [257, 1, 3, 300], [1] * 70, [700]])
+def test_prompt_lengths(counts, dim, dtype):
+    run_prompt(counts, counts, 4, 1, dim, dtype, seed=len(counts))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q_counts,k_counts", [([5, 3, 0, 7, 70], [2, 3, 4, 0, 300]), ([65], [64]), ([300], [10]),
+                                               ([1, 1, 1], [129, 64, 0]), ([40], [1000]), ([0, 0], [5, 0])])
+def test_prompt_fewer_and_more_keys_than_rows(q_counts, k_counts, causal):
+    for dim, dtype, heads in ((128, torch.bfloat16, (8, 2)), (64, torch.float16, (3, 3))):
+        run_prompt(q_counts, k_counts, *heads, dim, dtype, causal=causal, seed=3)
+
+
+def test_prompt_scales_and_large_scores():
+    for scale in (0.0, -0.3, 1.0):  # 1.0: scores to about +-100, weights concentrate on one key
+        run_prompt([90], [90], 4, 2, 128, torch.bfloat16, scale=scale, qs=1.0, seed=5)
+    run_prompt([90], [90], 4, 2, 64, torch.float16, scale=3.0, qs=1.0, seed=6)
+
+
+@pytest.mark.parametrize("layout", ["fused", "heads_first", "broadcast"])
+def test_prompt_strides(layout):
+    n, heads, kv_heads, dim, dtype = 75, 6, 2, 64, torch.float16
+    if layout == "fused":  # q, k, v are slices of one projection's rows
+        rows = randn((n, heads + 2 * kv_heads, dim), dtype, 1)
+        q, k, v = rows[:, :heads], rows[:, heads:heads + kv_heads], rows[:, heads + kv_heads:]
+        y = torch.full((n, heads, dim + 8), NAN, dtype=dtype, device="cuda")[..., :dim]
+    elif layout == "heads_first":
+        q, k, v = (randn((h, n, dim), dtype, i).transpose(0, 1) for i, h in enumerate((heads, kv_heads, kv_heads)))
+        y = torch.full((heads, n, dim), NAN, dtype=dtype, device="cuda").transpose(0, 1)
+    else:  # one key-value head seen as two, one query row seen as all
+        q = randn((1, heads, dim), dtype, 0).expand(n, heads, dim)
+        k, v = (randn((n, 1, dim), dtype, i).expand(n, kv_heads, dim) for i in (1, 2))
+        y = torch.full((n, heads, dim), NAN, dtype=dtype, device="cuda")
+    cu = offsets([40, 35])
+    paro.paro_attention_prompt(q, k, v, cu, cu, y)
+    for a, b in ((0, 40), (40, 75)):
+        check_rows(y[a:b], q[a:b], k[a:b], v[a:b], default_scale(dim))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("bad", [NAN, float("inf"), float("-inf"), "lowest"])
+def test_prompt_masked_places_do_not_reach_a_row(bad, dim):
+    """Keys and values that only later rows see hold NaN, infinities or the type's lowest value."""
+    dtype, counts, heads = torch.bfloat16, [100, 70], 4
+    bad = torch.finfo(dtype).min if bad == "lowest" else bad
+    q, k, v = randn((170, heads, dim), dtype, 0), randn((170, 1, dim), dtype, 1), randn((170, 1, dim), dtype, 2)
+    cut = [60, 100 + 33]  # first bad row of each sequence
+    for lo, hi in ((cut[0], 100), (cut[1], 170)):
+        k[lo:hi] = bad
+        v[lo:hi] = bad
+    y = torch.full_like(q, 7.0)
+    paro.paro_attention_prompt(q, k, v, offsets(counts), offsets(counts), y)
+    for lo, hi in ((0, cut[0]), (100, cut[1])):
+        check_rows(y[lo:hi], q[lo:hi], k[lo:hi], v[lo:hi], default_scale(dim))
+
+
+def test_prompt_bad_values_reach_the_rows_that_see_them():
+    dtype, n, dim = torch.float16, 50, 64
+    q, k, v = randn((n, 2, dim), dtype, 0), randn((n, 1, dim), dtype, 1), randn((n, 1, dim), dtype, 2)
+    v[20, 0, 5] = float("inf")
+    v[30, 0, 9] = NAN
+    y = torch.empty_like(q)
+    paro.paro_attention_prompt(q, k, v, offsets([n]), offsets([n]), y)
+    inf, nan = torch.isinf(y), torch.isnan(y)
+    assert not inf[:20].any() and not nan[:30].any()
+    assert bool((inf[20:, :, 5] | nan[20:, :, 5]).all()) and bool(nan[30:, :, 9].all())
+    inf[20:, :, 5] = nan[20:, :, 5] = nan[30:, :, 9] = False
+    assert not inf.any() and not nan.any()
+
+
+def test_prompt_rows_outside_the_sequences_stay():
+    q, k, v = randn((60, 4, 64), torch.float16, 0), randn((60, 2, 64), torch.float16, 1), randn((60, 2, 64),
+                                                                                               torch.float16, 2)
+    y = torch.full_like(q, 3.0)
+    cu = torch.tensor([10, 25, 25, 40], dtype=torch.int64, device="cuda")
+    paro.paro_attention_prompt(q, k, v, cu, cu, y)
+    assert bool((y[:10] == 3).all()) and bool((y[40:] == 3).all())
+    for a, b in ((10, 25), (25, 40)):
+        check_rows(y[a:b], q[a:b], k[a:b], v[a:b], default_scale(64))
+
+
+@pytest.mark.parametrize("cu", [[-5, 30, 20, 400], [0, 200, 100], [50, 0], [-9, -3], [10 ** 12, 10 ** 13]])
+def test_prompt_malformed_offsets_stay_in_bounds(cu):
+    """Wrong numbers are allowed; what is not covered by a sequence is not written, and nothing else is touched."""
+    big = torch.full((3, 120, 4, 64), 3.0, dtype=torch.float16, device="cuda")
+    q, k, v = randn((120, 4, 64), torch.float16, 0), randn((120, 2, 64), torch.float16, 1), randn((120, 2, 64),
+                                                                                                 torch.float16, 2)
+    cu = torch.tensor(cu, dtype=torch.int64, device="cuda")
+    paro.paro_attention_prompt(q, k, v, cu, cu, big[1])
+    torch.cuda.synchronize()
+    assert bool((big[0] == 3).all()) and bool((big[2] == 3).all())
+
+
+def test_prompt_no_rows_and_no_sequences():
+    q = torch.empty((0, 4, 64), dtype=torch.float16, device="cuda")
+    k = torch.empty((0, 2, 64), dtype=torch.float16, device="cuda")
+    paro.paro_attention_prompt(q, k, k, offsets([0]), offsets([0]), q)
+    y = torch.full((5, 4, 64), 2.0, dtype=torch.float16, device="cuda")
+    paro.paro_attention_prompt(torch.zeros_like(y), k, k, offsets([]), offsets([]), y)
+    assert bool((y == 2).all())
+    # rows but no key at all
+    paro.paro_attention_prompt(torch.zeros_like(y), k, k, offsets([5]), offsets([0]), y)
+    assert bool((y == 0).all())
+
+
+def test_prompt_repeats_to_the_bit_and_on_another_stream():
+    q, k, v = randn((333, 8, 128), torch.bfloat16, 0), randn((333, 2, 128), torch.bfloat16, 1), randn(
+        (333, 2, 128), torch.bfloat16, 2)
+    cu = offsets([200, 133])
+    first = torch.empty_like(q)
+    paro.paro_attention_prompt(q, k, v, cu, cu, first)
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for _ in range(3):
+        y = torch.full_like(q, NAN)
+        torch.cuda.synchronize()
+        paro.paro_attention_prompt(q, k, v, cu, cu, y, stream=other)
+        torch.cuda.synchronize()
+        assert torch.equal(y, first)
+
+
+# ---- over the cache ----
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+def test_chunk_pages(page, dtype):
+    lengths, new = [1, 40, 0, 130, 300, 64, 517], [1, 7, 0, 130, 65, 64, 100]
+    heads, kv_heads, dim = (7, 1, 64) if page % 3 else (8, 2, 128)
+    c = filled_cache(paro, lengths, page, kv_heads, dim, dtype, page)
+    order = [3, 0, 6, 2, 5, 1, 4]
+    counts = [new[s] for s in order]
+    q = randn((sum(counts), heads, dim), dtype, 1, 1.5)
+    y = torch.full_like(q, NAN)
+    slots = torch.tensor(order, dtype=torch.int32, device="cuda")
+    paro.paro_attention_prompt_cached(c, 0, q, slots, offsets(counts), y)
+    at = 0
+    for s, n in zip(order, counts):
+        k, v = cached_rows(c, 0, s)
+        check_rows(y[at:at + n], q[at:at + n], k, v, default_scale(dim))
+        at += n
+
+
+def test_chunk_layers_empty_and_foreign_slots():
+    c = filled_cache(paro, [20, 90, 0], 16, 2, 128, torch.float16, 1, layers=3)
+    q = randn((3 + 90 + 4 + 2, 4, 128), torch.float16, 0)
+    y = torch.full_like(q, NAN)
+    slots = torch.tensor([0, 1, 2, 99], dtype=torch.int32, device="cuda")
+    paro.paro_attention_prompt_cached(c, 2, q, slots, offsets([3, 90, 4, 2]), y)
+    for s, (a, b) in ((0, (0, 3)), (1, (3, 93))):
+        k, v = cached_rows(c, 2, s)
+        check_rows(y[a:b], q[a:b], k, v, default_scale(128))
+    assert bool((y[93:] == 0).all())  # no keys
+
+
+def run_decode(lengths, heads, kv_heads, dim, page, dtype, seed=0, order=None, extra=2, layers=1, layer=0):
+    c = filled_cache(paro, lengths, page, kv_heads, dim, dtype, seed, extra=extra, layers=layers)
+    order = list(range(len(lengths))) if order is None else order
+    q = randn((len(order), heads, dim), dtype, seed + 9, 1.5)
+    y = torch.full_like(q, NAN)
+    slots = torch.tensor(order, dtype=torch.int32, device="cuda")
+    ws = paro.make_workspace(paro.paro_attention_decode_workspace_bytes(c, len(order), heads))
+    first = None
+    for _ in range(3):  # the workspace serves again, and the bits repeat
+        paro.paro_attention_decode(c, layer, q, slots, y, ws)
+        torch.cuda.synchronize()
+        first = y.clone() if first is None else first
+        assert torch.equal(y, first)
+    for r, s in enumerate(order):
+        k, v = cached_rows(c, layer, s)
+        check_rows(y[r:r + 1], q[r:r + 1], k, v, default_scale(dim))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads", HEADS + [(16, 1), (17, 1), (48, 2)])
+def test_decode_heads(heads, dim, dtype):
+    run_decode([1, 33, 0, 200], *heads, dim, 16, dtype)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+def test_decode_pages_and_lengths(page):
+    run_decode([1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 0, 127, 128, 129, 255, 256, 257, 500], 4, 1, 128, page,
+               torch.bfloat16, page)
+    run_decode([3000, 1], 8, 2, 64, page, torch.float16, page, order=[1, 0, 0, 1])
+
+
+@pytest.mark.parametrize("extra", [2, 700])
+def test_decode_long_and_spare_table(extra):
+    """Few rows: the length is split over workgroups; a table far longer than the sequences splits more."""
+    run_decode([5000], 4, 1, 128, 64, torch.float16, 1, extra=extra)
+    run_decode([9001, 17, 4096], 2, 2, 64, 16, torch.bfloat16, 2, extra=extra, layers=2, layer=1)
+
+
+def test_decode_workspace_serves_several_shapes():
+    dtype, dim = torch.float16, 128
+    caches = [filled_cache(paro, ln, 16, 2, dim, dtype, i, extra=300) for i, ln in
+              enumerate(([2000], [700, 3, 900], [40] * 60))]
+    need = max(paro.paro_attention_decode_workspace_bytes(c, c.table.shape[0], 8) for c in caches)
+    ws = paro.make_workspace(need)
+    for _ in range(2):
+        for i, c in enumerate(caches):
+            n = c.table.shape[0]
+            q, y = randn((n, 8, dim), dtype, i), torch.full((n, 8, dim), NAN, dtype=dtype, device="cuda")
+            paro.paro_attention_decode(c, 0, q, torch.arange(n, dtype=torch.int32, device="cuda"), y, ws)
+            for r in range(n):
+                k, v = cached_rows(c, 0, r)
+                check_rows(y[r:r + 1], q[r:r + 1], k, v, default_scale(dim))
+
+
+def test_decode_empty_foreign_and_clamped():
+    c = filled_cache(paro, [20, 0], 16, 1, 64, torch.float16, 1, extra=0)
+    q = randn((4, 2, 64), torch.float16, 0)
+    y = torch.full_like(q, NAN)
+    ws = paro.make_workspace(paro.paro_attention_decode_workspace_bytes(c, 4, 2))
+    slots = torch.tensor([1, -1, 2, 0], dtype=torch.int32, device="cuda")
+    paro.paro_attention_decode(c, 0, q, slots, y, ws)
+    assert bool((y[:3] == 0).all())
+    k, v = cached_rows(c, 0, 0)
+    check_rows(y[3:], q[3:], k, v, default_scale(64))
+    # lengths and pages out of range: wrong numbers, no fault, and y alone is written
+    c.lengths.copy_(torch.tensor([10 ** 9, -4]))
+    c.table[0, 1] = 10 ** 9
+    before = c.k.clone()
+    paro.paro_attention_decode(c, 0, q, slots, y, ws)
+    torch.cuda.synchronize()
+    assert bool((y[:3] == 0).all()) and torch.equal(c.k.view(torch.int16), before.view(torch.int16))
+
+
+def test_decode_and_chunk_strides():
+    dtype, dim, lengths = torch.bfloat16, 128, [50, 300]
+    c = filled_cache(paro, lengths, 32, 2, dim, dtype, 3)
+    rows = randn((2, 8, dim), dtype, 4)
+    q = rows[:, 2:6]
+    y = torch.full((4, 2, dim), NAN, dtype=dtype, device="cuda").transpose(0, 1)
+    ws = paro.make_workspace(paro.paro_attention_decode_workspace_bytes(c, 2, 4))
+    slots = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    paro.paro_attention_decode(c, 0, q, slots, y, ws, scale=0.2)
+    z = torch.full((2, 4, dim + 16), NAN, dtype=dtype, device="cuda")[..., 8:dim + 8]
+    paro.paro_attention_prompt_cached(c, 0, q, slots, offsets([1, 1]), z, scale=0.2)
+    for r, s in enumerate((1, 0)):
+        k, v = cached_rows(c, 0, s)
+        check_rows(y[r:r + 1], q[r:r + 1], k, v, 0.2)
+        check_rows(z[r:r + 1], q[r:r + 1], k, v, 0.2)
+
+
+def test_binding_refuses():
+    f = torch.float16
+    q, k = torch.zeros((4, 4, 64), dtype=f, device="cuda"), torch.zeros((4, 2, 64), dtype=f, device="cuda")
+    cu, y = offsets([4]), torch.zeros((4, 4, 64), dtype=f, device="cuda")
+    bad = [
+        (q, k, k.bfloat16(), cu, cu, y), (q, k, k[:3], cu, cu, y), (q, k, k, cu.int(), cu, y),
+        (q, k, k, cu, cu[:1], y), (q, k, k, cu, cu, q), (q, k, k, cu, cu, y[:3]),
+        (q.transpose(1, 2), k, k, cu, cu, y), (q[:, :3], k, k, cu, cu, y[:, :3]), (q, k.cpu(), k, cu, cu, y),
+        (q[..., :32], k[..., :32], k[..., :32], cu, cu, y[..., :32]), (q, k, k, cu, cu, y[:1].expand(4, 4, 64)),
+    ]
+    for args in bad:
+        with pytest.raises(paro.ParoError):
+            paro.paro_attention_prompt(*args)
+    with pytest.raises(paro.ParoError):
+        paro.paro_attention_prompt(q, k, k, cu, cu, y, scale=float("inf"))
+    c = paro.KVCache.empty(1, 4, 2, 16, 64, 2, 2, f)
+    s = torch.zeros(4, dtype=torch.int32, device="cuda")
+    ws = paro.make_workspace(paro.paro_attention_decode_workspace_bytes(c, 4, 4))
+    for args in [(c, 1, q, s, y, ws), (c, 0, q, s[:3], y, ws), (c, 0, q, s, y, ws[:64]), (c, 0, q, s, y, None),
+                 (c, 0, q[:, :3], s, y[:, :3], ws), (c, 0, q.bfloat16(), s, y, ws), (c, 0, q, s.long(), y, ws)]:
+        with pytest.raises(paro.ParoError):
+            paro.paro_attention_decode(*args)
