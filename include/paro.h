@@ -591,7 +591,7 @@ int paro_attention_prompt_cached(const paro_kv_cache *cache, int layer, const pa
  *   ones.  The split of the length depends on rows, q_heads and the cache's
  *   sizes and on each length alone, and parts are joined in order: a
  *   repeated call gives identical bits.
- * rows <= 65536.
+ * rows <= 32768.
  */
 int paro_attention_decode(const paro_kv_cache *cache, int layer, const paro_attention_shape *shape, const void *q,
                           const int32_t *slots, int64_t rows, void *y, void *workspace, size_t workspace_bytes,

@@ -477,6 +477,8 @@ class KVCache:
         layers, pages, kv_heads, page_size, head_dim = k.shape
         self.c = ParoKvCacheC(layers, kv_heads, head_dim, page_size, pages, table.shape[0], table.shape[1], _dt(k),
                               k.data_ptr(), v.data_ptr(), refs.data_ptr(), table.data_ptr(), lengths.data_ptr())
+        self.ref = ctypes.byref(self.c)
+        self.dtype, self.device = k.dtype, k.device
 
     @classmethod
     def empty(cls, layers, pages, kv_heads, page_size, head_dim, slots, max_pages, dtype, device="cuda"):
@@ -488,10 +490,6 @@ class KVCache:
                    torch.full((slots, max_pages), -1, dtype=torch.int32, device=device),
                    torch.zeros(slots, dtype=torch.int32, device=device))
 
-    @property
-    def ref(self):
-        return ctypes.byref(self.c)
-
 
 def _need(good, status: int, what: str, msg: str):
     if not good:
@@ -502,58 +500,62 @@ def _scratch(workspace, device, what):
     """Bytes of a workspace tensor (0 for None, which the library refuses)."""
     if workspace is None:
         return 0
-    _need(workspace.is_contiguous() and workspace.device == device, 7, what, f"workspace: a contiguous tensor on {device}")
-    return workspace.numel() * workspace.element_size()
+    _need(workspace.is_contiguous() and workspace.device == device, 7, what, "workspace: a contiguous tensor on q's device")
+    return workspace.nbytes
 
 
 def _index(t, dtype, n, device, what, name):
-    _need(t.dtype == dtype and t.dim() == 1 and t.is_contiguous() and t.device == device, 3, what,
-          f"{name}: a contiguous 1-d {dtype} tensor on {device}")
-    if n is not None:
-        _need(t.numel() == n, 2, what, f"{name} has {t.numel()} entries, {n} expected")
+    """t: a contiguous 1-d tensor of n entries (None: any)."""
+    if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() or t.device != device:
+        raise ParoError(3, what, f"{name}: a contiguous 1-d {dtype} tensor on {device}")
+    if n is not None and t.shape[0] != n:
+        raise ParoError(2, what, f"{name} has {t.shape[0]} entries, {n} expected")
 
 
-def _rows(t, like, what, name):
-    """A (tokens, heads, head_dim) view with channels together, of like's dtype and device."""
-    _need(t.dim() == 3 and (t.stride(2) == 1 or t.numel() == 0), 2, what,
-          f"{name}: (tokens, heads, head_dim) with contiguous channels")
-    _need(t.dtype == like.dtype and t.device == like.device, 3, what, f"{name}: {like.dtype} on {like.device}")
+def _rows(t, dtype, device, what, name):
+    """t: a (tokens, heads, head_dim) view with channels together; returns its token and head strides."""
+    stride = t.stride()
+    if len(stride) != 3 or (stride[2] != 1 and t.numel()):
+        raise ParoError(2, what, f"{name}: (tokens, heads, head_dim) with contiguous channels")
+    if t.dtype != dtype or t.device != device:
+        raise ParoError(3, what, f"{name}: {dtype} on {device}")
+    return stride
 
 
 def _launch(fn, device, stream, *args):
     """Calls fn(*args, stream) with `device` current; the stream defaults to that device's current one."""
     import torch
-    _need(device.type == "cuda", 1, fn.__name__, f"tensors in device memory are required, not on {device}")
+    if device.type != "cuda":
+        raise ParoError(1, fn.__name__, f"tensors in device memory are required, not on {device}")
     if device.index == torch.cuda.current_device():
         return fn(*args, _stream_handle(stream))
     with torch.cuda.device(device):
         return fn(*args, _stream_handle(stream))
 
 
-def _shape_of(q, y, kv_heads, scale, causal, k=None, v=None):
-    d = q.shape[2]
-    s = ParoAttentionShapeC(q.shape[1], kv_heads, d, int(bool(causal)), d ** -0.5 if scale is None else scale,
-                            q.stride(0), q.stride(1), 0, 0, 0, 0, y.stride(0), y.stride(1))
-    if k is not None:
-        s.k_token, s.k_head, s.v_token, s.v_head = k.stride(0), k.stride(1), v.stride(0), v.stride(1)
-    return s
+def _shape_of(q, kv_heads, scale, causal, qs, ys, ks=(0, 0), vs=(0, 0)):
+    _, heads, d = q.shape
+    return ParoAttentionShapeC(heads, kv_heads, d, bool(causal), d ** -0.5 if scale is None else scale, qs[0], qs[1],
+                               ks[0], ks[1], vs[0], vs[1], ys[0], ys[1])
 
 
 def paro_attention_prompt(q, k, v, cu_q, cu_k, y, scale=None, causal=True, stream=None) -> None:
     """q, y: (tokens, q_heads, head_dim); k, v: (keys, kv_heads, head_dim), fp16/bf16 views; cu_q, cu_k: int64
     (sequences + 1,) device tensors; scale: 1 / sqrt(head_dim) if None."""
     import torch
-    what = "paro_attention_prompt"
-    for t, name in ((q, "q"), (k, "k"), (v, "v"), (y, "y")):
-        _rows(t, q, what, name)
+    what, dt, dev = "paro_attention_prompt", q.dtype, q.device
+    qs, ks, vs, ys = (_rows(t, dt, dev, what, name) for t, name in ((q, "q"), (k, "k"), (v, "v"), (y, "y")))
+    _need(dt in (torch.float16, torch.bfloat16), 3, what, "fp16 or bf16")
     _need(y.shape == q.shape and k.shape == v.shape and k.shape[2] == q.shape[2], 2, what,
           "y like q, v like k, one head_dim")
-    _index(cu_q, torch.int64, None, q.device, what, "cu_q")
-    _index(cu_k, torch.int64, cu_q.numel(), q.device, what, "cu_k")
-    _need(cu_q.numel() > 0, 2, what, "cu_q has sequences + 1 entries")
-    s = _shape_of(q, y, k.shape[1], scale, causal, k, v)
-    _check(_launch(load().paro_attention_prompt, q.device, stream, ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _dt(q),
-                   _ptr(cu_q), _ptr(cu_k), cu_q.numel() - 1, q.shape[0], k.shape[0], _ptr(y)), what)
+    n = cu_q.shape[0] if cu_q.dim() else 0
+    _need(n > 0, 2, what, "cu_q has sequences + 1 entries")
+    _index(cu_q, torch.int64, None, dev, what, "cu_q")
+    _index(cu_k, torch.int64, n, dev, what, "cu_k")
+    s = _shape_of(q, k.shape[1], scale, causal, qs, ys, ks, vs)
+    _check(_launch(load().paro_attention_prompt, dev, stream, ctypes.byref(s), q.data_ptr(), k.data_ptr(),
+                   v.data_ptr(), _dt(q), cu_q.data_ptr(), cu_k.data_ptr(), n - 1, q.shape[0], k.shape[0],
+                   y.data_ptr()), what)
 
 
 def paro_attention_prompt_cached(cache: KVCache, layer: int, q, slots, cu_q, y, scale=None, causal=True,
@@ -561,15 +563,15 @@ def paro_attention_prompt_cached(cache: KVCache, layer: int, q, slots, cu_q, y, 
     """q, y: (tokens, q_heads, head_dim) of the cache's dtype: the newest rows of the slots; slots: int32
     (sequences,); cu_q: int64 (sequences + 1,)."""
     import torch
-    what = "paro_attention_prompt_cached"
-    for t, name in ((q, "q"), (y, "y")):
-        _rows(t, cache.k, what, name)
+    what, dt, dev = "paro_attention_prompt_cached", cache.dtype, cache.device
+    qs, ys = _rows(q, dt, dev, what, "q"), _rows(y, dt, dev, what, "y")
     _need(y.shape == q.shape, 2, what, "y like q")
-    _index(slots, torch.int32, None, cache.k.device, what, "slots")
-    _index(cu_q, torch.int64, slots.numel() + 1, cache.k.device, what, "cu_q")
-    s = _shape_of(q, y, cache.c.kv_heads, scale, causal)
-    _check(_launch(load().paro_attention_prompt_cached, q.device, stream, cache.ref, layer, ctypes.byref(s), _ptr(q),
-                   _ptr(slots), _ptr(cu_q), slots.numel(), q.shape[0], _ptr(y)), what)
+    _index(slots, torch.int32, None, dev, what, "slots")
+    n = slots.shape[0]
+    _index(cu_q, torch.int64, n + 1, dev, what, "cu_q")
+    s = _shape_of(q, cache.c.kv_heads, scale, causal, qs, ys)
+    _check(_launch(load().paro_attention_prompt_cached, dev, stream, cache.ref, layer, ctypes.byref(s), q.data_ptr(),
+                   slots.data_ptr(), cu_q.data_ptr(), n, q.shape[0], y.data_ptr()), what)
 
 
 def paro_attention_decode_workspace_bytes(cache: KVCache, rows: int, q_heads: int) -> int:
@@ -580,31 +582,32 @@ def paro_attention_decode(cache: KVCache, layer: int, q, slots, y, workspace, sc
     """q, y: (rows, q_heads, head_dim), one new token per row; slots: int32 (rows,); workspace: zero-filled before
     its first use, of paro_attention_decode_workspace_bytes() bytes."""
     import torch
-    what = "paro_attention_decode"
-    for t, name in ((q, "q"), (y, "y")):
-        _rows(t, cache.k, what, name)
+    what, dt, dev = "paro_attention_decode", cache.dtype, cache.device
+    qs, ys = _rows(q, dt, dev, what, "q"), _rows(y, dt, dev, what, "y")
     _need(y.shape == q.shape, 2, what, "y like q")
-    _index(slots, torch.int32, q.shape[0], cache.k.device, what, "slots")
-    ws_bytes = _scratch(workspace, cache.k.device, what)
-    s = _shape_of(q, y, cache.c.kv_heads, scale, True)
-    _check(_launch(load().paro_attention_decode, q.device, stream, cache.ref, layer, ctypes.byref(s), _ptr(q),
-                   _ptr(slots), q.shape[0], _ptr(y), _ptr(workspace), ws_bytes), what)
+    n = q.shape[0]
+    _index(slots, torch.int32, n, dev, what, "slots")
+    ws_bytes = _scratch(workspace, dev, what)
+    s = _shape_of(q, cache.c.kv_heads, scale, True, qs, ys)
+    _check(_launch(load().paro_attention_decode, dev, stream, cache.ref, layer, ctypes.byref(s), q.data_ptr(),
+                   slots.data_ptr(), n, y.data_ptr(), _ptr(workspace), ws_bytes), what)
 
 
 def paro_kv_append(cache: KVCache, layer: int, k, v, slots, cu=None, stream=None) -> None:
     """k, v: (tokens, kv_heads, head_dim) of the cache's dtype become the newest positions of the slots: rows
     cu[i]..cu[i + 1] of slot slots[i] (int32), one row per slot if cu (int64) is None."""
     import torch
-    what = "paro_kv_append"
-    for t, name in ((k, "k"), (v, "v")):
-        _rows(t, cache.k, what, name)
-    _need(k.shape == v.shape and tuple(k.shape[1:]) == (cache.c.kv_heads, cache.c.head_dim), 2, what,
-          f"k and v: (tokens, {cache.c.kv_heads}, {cache.c.head_dim})")
-    _index(slots, torch.int32, None, cache.k.device, what, "slots")
+    what, dt, dev = "paro_kv_append", cache.dtype, cache.device
+    ks, vs = _rows(k, dt, dev, what, "k"), _rows(v, dt, dev, what, "v")
+    rows, heads, d = k.shape
+    if v.shape != k.shape or heads != cache.c.kv_heads or d != cache.c.head_dim:
+        raise ParoError(2, what, f"k and v: (tokens, {cache.c.kv_heads}, {cache.c.head_dim})")
+    _index(slots, torch.int32, None, dev, what, "slots")
+    n = slots.shape[0]
     if cu is not None:
-        _index(cu, torch.int64, slots.numel() + 1, cache.k.device, what, "cu")
-    _check(_launch(load().paro_kv_append, k.device, stream, cache.ref, layer, _ptr(k), k.stride(0), k.stride(1),
-                   _ptr(v), v.stride(0), v.stride(1), _ptr(slots), _ptr(cu), slots.numel(), k.shape[0]), what)
+        _index(cu, torch.int64, n + 1, dev, what, "cu")
+    _check(_launch(load().paro_kv_append, dev, stream, cache.ref, layer, k.data_ptr(), ks[0], ks[1], v.data_ptr(),
+                   vs[0], vs[1], slots.data_ptr(), _ptr(cu), n, rows), what)
 
 
 def paro_kv_workspace_bytes(cache: KVCache) -> int:
@@ -612,41 +615,40 @@ def paro_kv_workspace_bytes(cache: KVCache) -> int:
     return int(load().paro_kv_workspace_bytes(cache.ref))
 
 
-def _plan_call(fn, what, cache, lists, workspace, stream):
+def _plan_call(fn, what, cache, names, a, b, out, workspace, stream):
     import torch
-    n = lists[0][1].numel()
-    for name, t in lists:
-        _index(t, torch.int32, n, cache.k.device, what, name)
-    ws_bytes = _scratch(workspace, cache.k.device, what)
-    ptrs = [_ptr(t) for _, t in lists]
-    _check(_launch(fn, cache.k.device, stream, cache.ref, ptrs[0], ptrs[1], n, ptrs[2], _ptr(workspace), ws_bytes),
-           what)
+    dev = cache.device
+    n = a.shape[0] if a.dim() else 0
+    for t, name in zip((a, b, out), names):
+        _index(t, torch.int32, n, dev, what, name)
+    _check(_launch(fn, dev, stream, cache.ref, a.data_ptr(), b.data_ptr(), n, out.data_ptr(), _ptr(workspace),
+                   _scratch(workspace, dev, what)), what)
 
 
 def paro_kv_reserve(cache: KVCache, slots, grow, granted, workspace, stream=None) -> None:
     """Room for grow[i] new positions in slot slots[i]; granted[i] is set to 1 or 0 (int32 tensors)."""
-    _plan_call(load().paro_kv_reserve, "paro_kv_reserve", cache,
-               [("slots", slots), ("grow", grow), ("granted", granted)], workspace, stream)
+    _plan_call(load().paro_kv_reserve, "paro_kv_reserve", cache, ("slots", "grow", "granted"), slots, grow, granted,
+               workspace, stream)
 
 
 def paro_kv_fork(cache: KVCache, parents, children, granted, workspace, stream=None) -> None:
     """The empty slot children[i] shares the pages of slot parents[i]; granted[i] is set to 1 or 0."""
-    _plan_call(load().paro_kv_fork, "paro_kv_fork", cache,
-               [("parents", parents), ("children", children), ("granted", granted)], workspace, stream)
+    _plan_call(load().paro_kv_fork, "paro_kv_fork", cache, ("parents", "children", "granted"), parents, children,
+               granted, workspace, stream)
 
 
 def paro_kv_free(cache: KVCache, slots, stream=None) -> None:
     """Empties the slots (int32 tensor) and gives up their pages."""
     import torch
-    _index(slots, torch.int32, None, cache.k.device, "paro_kv_free", "slots")
-    _check(_launch(load().paro_kv_free, cache.k.device, stream, cache.ref, _ptr(slots), slots.numel()),
+    _index(slots, torch.int32, None, cache.device, "paro_kv_free", "slots")
+    _check(_launch(load().paro_kv_free, cache.device, stream, cache.ref, slots.data_ptr(), slots.shape[0]),
            "paro_kv_free")
 
 
 def paro_kv_compact(cache: KVCache, used, workspace, stream=None) -> None:
     """Moves the pages in use to the lowest indices; used: int32 (1,), set to their number."""
     import torch
-    _index(used, torch.int32, 1, cache.k.device, "paro_kv_compact", "used")
-    ws_bytes = _scratch(workspace, cache.k.device, "paro_kv_compact")
-    _check(_launch(load().paro_kv_compact, cache.k.device, stream, cache.ref, _ptr(used), _ptr(workspace), ws_bytes),
-           "paro_kv_compact")
+    what, dev = "paro_kv_compact", cache.device
+    _index(used, torch.int32, 1, dev, what, "used")
+    _check(_launch(load().paro_kv_compact, dev, stream, cache.ref, used.data_ptr(), _ptr(workspace),
+                   _scratch(workspace, dev, what)), what)

@@ -118,13 +118,4 @@ hipError_t launch_attention_prompt(const AttentionArgs &a, bool cached, hipStrea
   return cached ? launch_rows<true>(a, st) : launch_rows<false>(a, st);
 }
 
-DecodeAttentionPlan plan_attention_decode(int64_t, int q_heads, int kv_heads, int64_t) {
-  return DecodeAttentionPlan{1, (q_heads / kv_heads + 15) / 16};
-}
-size_t attention_decode_partial_bytes(const DecodeAttentionPlan &, int64_t, int, int) { return 0; }
-hipError_t launch_attention_decode(const AttentionArgs &a, const DecodeAttentionPlan &, uint32_t *, float *,
-                                   hipStream_t st) {
-  return launch_rows<true>(a, st);
-}
-
 }  // namespace paro

@@ -12,6 +12,7 @@ namespace paro {
 
 constexpr int kMaxSlots = 4096;      // the planning kernels keep per-slot tables in LDS
 constexpr int kMaxSequences = 65536;
+constexpr int kMaxDecodeRows = 32768;  // a grid dimension
 
 // One layer of a paged cache as the kernels see it.
 struct KvLayer {

@@ -296,7 +296,7 @@ int paro_attention_prompt_cached(const paro_kv_cache *c, int layer, const paro_a
 }
 
 size_t paro_attention_decode_workspace_bytes(const paro_kv_cache *c, int64_t rows, int q_heads) {
-  if (check_cache(c, false) || rows <= 0 || rows > paro::kMaxSequences || q_heads < 1 || q_heads > kMaxHeads ||
+  if (check_cache(c, false) || rows <= 0 || rows > paro::kMaxDecodeRows || q_heads < 1 || q_heads > kMaxHeads ||
       q_heads % c->kv_heads)
     return 0;
   const paro::DecodeAttentionPlan p =
@@ -308,7 +308,7 @@ int paro_attention_decode(const paro_kv_cache *c, int layer, const paro_attentio
                           const int32_t *slots, int64_t rows, void *y, void *workspace, size_t workspace_bytes,
                           void *stream) {
   int rc = check_cache_and_shape(c, layer, s);
-  if (!rc) rc = check_rows(rows, "rows", paro::kMaxSequences);
+  if (!rc) rc = check_rows(rows, "rows", paro::kMaxDecodeRows);
   if (rc) return rc;
   if (rows == 0) return ok();
   if ((rc = check_qy(s, q, y, rows)) || (rc = check_apart_from_cache(c, s, y, rows))) return rc;
