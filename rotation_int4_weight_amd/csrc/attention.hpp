@@ -42,11 +42,10 @@ struct AttentionArgs {
 hipError_t launch_attention_prompt(const AttentionArgs &a, bool cached, hipStream_t st);
 
 // One token per row over the cache.  The length of a row is split over
-// `splits` workgroups where there are few (row, key-value head, head tile)
-// items; with more than kDecodeCounters of them the chip is full and
-// splits == 1, so a fixed counter area at the start of every workspace serves
-// all shapes and stays zero between calls.
-constexpr int kDecodeCounters = 16384;
+// `splits` workgroups where there are fewer than kDecodeCounters (row,
+// key-value head, head tile) items, so a fixed counter area at the start of
+// every workspace serves all shapes and stays zero between calls.
+constexpr int kDecodeCounters = 512;
 struct DecodeAttentionPlan {
   int splits;
   int head_tiles;  // workgroups per key-value head: its query heads in tiles of 16

@@ -33,7 +33,12 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kStep = 32;           // keys per wave and step
 constexpr int kCoherent = 16;       // SC1: device-scope loads and stores of the parts
-constexpr int kMinPart = kStep * kWaves * 2;
+constexpr int kUnit = kStep * kWaves;  // keys per workgroup and step
+// Rows up to this length are not cut: joining parts costs about 3 us (stores,
+// a counter and loads through the coherent levels), one step about 1.2 us (16
+// rows of 300: 6.8 us whole, 9.0 in parts; one row of 777: 11.0 and 7.3).
+constexpr int kWhole = 3 * kUnit;
+constexpr int64_t kCus = 256;
 
 template <int DIM>
 struct Tile {
@@ -162,6 +167,15 @@ __device__ __forceinline__ void step(State<DIM> &st, Tile<DIM> &t, const u32x4 (
   }
 }
 
+// (o, m, sum) joined with another part's, both relative to their maxima
+__device__ __forceinline__ void add_part(f32x4 &o, float &m, float &sum, const f32x4 &po, float pm, float psum) {
+  const float mn = fmaxf(m, pm), ref = mn == -INFINITY ? 0.f : mn;
+  const float ka = __builtin_amdgcn_exp2f(m - ref), kb = __builtin_amdgcn_exp2f(pm - ref);
+  o = o * ka + po * kb;
+  sum = sum * ka + psum * kb;
+  m = mn;
+}
+
 template <int DT, int DIM>
 __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs a, DecodeAttentionPlan plan,
                                                                   uint32_t *__restrict__ counters,
@@ -170,6 +184,7 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
   constexpr int RS = DIM + 4;  // LDS row: the four words over keep rows on different banks
   __shared__ __align__(16) float so[kWaves][16][RS];
   __shared__ float sm[kWaves][16], sl[kWaves][16];
+  __shared__ float jm[16], jl[16];
   __shared__ int s_last;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
   const int split = blockIdx.x;
@@ -178,15 +193,6 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
   const int heads = min(16, a.group - 16 * tile);  // query heads of this workgroup
   const int head0 = kvh * a.group + 16 * tile;
   const int slot = a.slots[row];
-  int len = 0;
-  if (slot >= 0 && slot < a.kv.slots) len = min(max(a.kv.lengths[slot], 0), a.kv.max_pages << a.kv.page_shift);
-  // equal parts of whole steps, at least kMinPart keys
-  const int part = max(kMinPart, (int)((((int64_t)len + plan.splits - 1) / plan.splits + kStep * kWaves - 1) /
-                                       (kStep * kWaves) * (kStep * kWaves)));
-  const int parts = max(1, (len + part - 1) / part);
-  if (split >= parts) return;
-  const int begin = split * part, end = min(len, begin + part);
-
   // Q^T fragments: lane: head lane%16, channels 32 s + 8 g..; unused heads zero
   u32x4 q[DIM / 32];
   {
@@ -198,6 +204,15 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
       if (h >= heads) q[s] = u32x4{0, 0, 0, 0};
     }
   }
+  int len = 0;
+  if (slot >= 0 && slot < a.kv.slots) len = min(max(a.kv.lengths[slot], 0), a.kv.max_pages << a.kv.page_shift);
+  // equal parts of whole steps
+  const int part = len <= kWhole ? kWhole
+                                 : (int)((((int64_t)len + plan.splits - 1) / plan.splits + kUnit - 1) / kUnit * kUnit);
+  const int parts = max(1, (len + part - 1) / part);
+  if (split >= parts) return;
+  const int begin = split * part, end = min(len, begin + part);
+
   State<DIM> st;
 #pragma unroll
   for (int j = 0; j < E; ++j) st.o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -213,26 +228,24 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
     pg.num_pages = a.kv.num_pages;
     pg.shift = a.kv.page_shift;
     pg.dim = DIM;
-    constexpr int kStride = kStep * kWaves;
     int pos = begin + wave * kStep;
     // two tiles in turn: one is worked on while the other is loaded; the
-    // addresses of the one after are looked up meanwhile.  Past the end the
-    // last page is read again and not used.
+    // addresses of the one after are looked up meanwhile
     Tile<DIM> t0, t1;
     load_tile<DIM>(t0, a.kv.k, a.kv.v, pg.at(pos), pg.at(pos + 16), lane);
-    int64_t n0 = pg.at(pos + kStride), n1 = pg.at(pos + kStride + 16);
+    int64_t n0 = pg.at(pos + kUnit), n1 = pg.at(pos + kUnit + 16);
     while (true) {
-      load_tile<DIM>(t1, a.kv.k, a.kv.v, n0, n1, lane);
-      n0 = pg.at(pos + 2 * kStride);
-      n1 = pg.at(pos + 2 * kStride + 16);
+      if (pos + kUnit < end) load_tile<DIM>(t1, a.kv.k, a.kv.v, n0, n1, lane);
+      n0 = pg.at(pos + 2 * kUnit);
+      n1 = pg.at(pos + 2 * kUnit + 16);
       step<DT, DIM>(st, t0, q, scale2, end - pos, lane);
-      pos += kStride;
+      pos += kUnit;
       if (pos >= end) break;
-      load_tile<DIM>(t0, a.kv.k, a.kv.v, n0, n1, lane);
-      n0 = pg.at(pos + 2 * kStride);
-      n1 = pg.at(pos + 2 * kStride + 16);
+      if (pos + kUnit < end) load_tile<DIM>(t0, a.kv.k, a.kv.v, n0, n1, lane);
+      n0 = pg.at(pos + 2 * kUnit);
+      n1 = pg.at(pos + 2 * kUnit + 16);
       step<DT, DIM>(st, t1, q, scale2, end - pos, lane);
-      pos += kStride;
+      pos += kUnit;
       if (pos >= end) break;
     }
   }
@@ -301,31 +314,46 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
   }
   __syncthreads();
   if (!s_last) return;
-  for (int h = (int)threadIdx.x / kPerHead; h < heads; h += kHeadsPerPass) {
+  // DIM / 4 threads per head leave room for `lanes` of them per output: each
+  // takes every lanes-th part, eight loads in flight together
+  const int lanes = max(1, kHeadsPerPass / heads);
+  const int sub = (int)threadIdx.x / kPerHead;
+  float *const jo = &so[0][0][0];  // [sub][RS], after the waves' use of so
+  for (int h0 = 0; h0 < heads; h0 += kHeadsPerPass) {
+    const int h = lanes > 1 ? sub / lanes : h0 + sub, first = lanes > 1 ? sub % lanes : 0;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, sum = 0.f;
-    constexpr int kBatch = 8;  // loads of eight parts in flight together
-    for (int p0 = 0; p0 < parts; p0 += kBatch) {
-      f32x4 x[kBatch];
-      u32x2 ml[kBatch];
+    if (h < heads) {
+      constexpr int kBatch = 8;
+      for (int p0 = first; p0 < parts; p0 += kBatch * lanes) {
+        f32x4 x[kBatch];
+        u32x2 ml[kBatch];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const uint32_t at = (uint32_t)(min(p0 + u, parts - 1) * slot_floats + h * (DIM + 4)) * 4u;
-        x[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at + ch * 4, 0, kCoherent));
-        ml[u] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, at + DIM * 4, 0, kCoherent));
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (p0 + u < parts) {
-          const float pm = __uint_as_float(ml[u][0]);
-          const float mn = fmaxf(m, pm), ref = mn == -INFINITY ? 0.f : mn;
-          const float ka = __builtin_amdgcn_exp2f(m - ref), kb = __builtin_amdgcn_exp2f(pm - ref);
-          o = o * ka + x[u] * kb;
-          sum = sum * ka + __uint_as_float(ml[u][1]) * kb;
-          m = mn;
+        for (int u = 0; u < kBatch; ++u) {
+          const uint32_t at = (uint32_t)(min(p0 + u * lanes, parts - 1) * slot_floats + h * (DIM + 4)) * 4u;
+          x[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at + ch * 4, 0, kCoherent));
+          ml[u] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, at + DIM * 4, 0, kCoherent));
         }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (p0 + u * lanes < parts) add_part(o, m, sum, x[u], __uint_as_float(ml[u][0]), __uint_as_float(ml[u][1]));
       }
     }
+    if (lanes > 1) {  // then heads <= kHeadsPerPass / 2: this loop runs once
+      __syncthreads();
+      if (h < heads) {
+        *reinterpret_cast<f32x4 *>(jo + sub * RS + ch) = o;
+        if (ch == 0) {
+          jm[sub] = m;
+          jl[sub] = sum;
+        }
+      }
+      __syncthreads();
+      if (first != 0) continue;
+      for (int u = 1; u < lanes && h < heads; ++u)
+        add_part(o, m, sum, *reinterpret_cast<const f32x4 *>(jo + (sub + u) * RS + ch), jm[sub + u], jl[sub + u]);
+    }
+    if (h >= heads) continue;
     const float inv = 1.f / sum;
     const u32x2 y = {pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
     *reinterpret_cast<u32x2 *>(a.y + row * a.y_token + (int64_t)(head0 + h) * a.y_head + ch) = y;
@@ -335,12 +363,17 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
 
 }  // namespace
 
+// One workgroup per CU streams the cache fastest: a second one adds only its
+// own start and end (8 rows of 8192: 43.5 us with 256 workgroups, 45.1 with
+// 512; one row of 32768: 27.2 and 30.4), so the parts fill the 256 CUs once.
+// Between one and two workgroups per CU two parts even out the second round
+// (40 rows of 4096: 124.6 us against 140.3); from two on, whole rows.
 DecodeAttentionPlan plan_attention_decode(int64_t rows, int q_heads, int kv_heads, int64_t max_len) {
   DecodeAttentionPlan p;
   p.head_tiles = (q_heads / kv_heads + 15) / 16;
   const int64_t items = rows * kv_heads * p.head_tiles;
-  const int64_t most = std::max<int64_t>(1, (max_len + kMinPart - 1) / kMinPart);
-  p.splits = items > kDecodeCounters ? 1 : (int)std::max<int64_t>(1, std::min({most, 4096 / items, int64_t(64)}));
+  const int64_t most = std::max<int64_t>(1, (max_len + kUnit - 1) / kUnit);
+  p.splits = (int)std::min(most, items <= kCus ? kCus / items : items < 2 * kCus ? int64_t(2) : int64_t(1));
   return p;
 }
 
