@@ -507,9 +507,8 @@ size_t paro_mxfp4_linear_prepared_workspace_bytes(const paro_w4_layer *layer, in
  * (i + n_k < n_q, or n_k = 0) gives zeros; what stands in keys and values a
  * row may not see, infinities and NaN included, does not reach it.  Scores,
  * maxima, sums and outputs are held in fp32; the weights exp(s - m) are
- * rounded to the activation dtype (at most 1, relative error half a step)
- * for the matrix cores, and the sum is taken over the rounded weights, so
- * they add up to one; y is rounded once.
+ * rounded to the activation dtype for the matrix cores (half a step each),
+ * their sum is that of the unrounded ones, and y is rounded once.
  * GPU limits: head_dim 64 or 128, q_heads a multiple of kv_heads and at most
  * 256, strides non-negative multiples of 8 elements below 2^40, tensors
  * 16-byte aligned.
@@ -563,7 +562,7 @@ typedef struct {
  *   nondecreasing from 0 to q_tokens (k_tokens); entries are clamped into
  *   that range and a sequence that would end before it starts is empty.
  *   Rows of y outside every sequence are not written.
- * sequences in 0..65536, q_tokens and k_tokens <= 2^21.
+ * sequences <= 16384, q_tokens and k_tokens <= 2^21, k_token and v_token <= 2^26.
  */
 int paro_attention_prompt(const paro_attention_shape *shape, const void *q, const void *k, const void *v,
                           paro_dtype dt, const int64_t *cu_q, const int64_t *cu_k, int64_t sequences,
@@ -604,7 +603,7 @@ size_t paro_attention_decode_workspace_bytes(const paro_kv_cache *cache, int64_t
  * paro_attention_shape) become the newest positions of slot slots[i], i.e.
  * lengths[slots[i]] - (cu[i+1] - cu[i]) and up, which paro_kv_reserve has
  * granted before.  cu: DEVICE int64 [n + 1], or NULL for one row per entry
- * (tokens == n).  n <= 65536.  Rows whose position or page does not exist
+ * (tokens == n).  n <= 16384.  Rows whose position or page does not exist
  * are skipped; of entries that name the same slot the first one counts and
  * the others are skipped.  Nothing else of the cache is written.
  */

@@ -11,7 +11,7 @@
 namespace paro {
 
 constexpr int kMaxSlots = 4096;      // the planning kernels keep per-slot tables in LDS
-constexpr int kMaxSequences = 65536;
+constexpr int kMaxSequences = 16384;  // with 256 heads and the most rows, under 2^32 threads a launch
 constexpr int kMaxDecodeRows = 32768;  // a grid dimension
 
 // One layer of a paged cache as the kernels see it.
@@ -22,6 +22,12 @@ struct KvLayer {
   int64_t page_stride;     // elements per page: kv_heads * page_size * head_dim
   int num_pages, max_pages, slots;
   int page_shift;          // log2(page_size)
+  // positions that a slot holds (0 for one outside the cache)
+  __device__ int length(int slot) const {
+    if (slot < 0 || slot >= slots) return 0;
+    const int n = lengths[slot], most = max_pages << page_shift;
+    return n < 0 ? 0 : n > most ? most : n;
+  }
 };
 
 struct AttentionArgs {

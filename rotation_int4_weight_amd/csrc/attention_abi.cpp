@@ -23,6 +23,7 @@ using paro::overlap;
 constexpr int64_t kMaxRows = int64_t(1) << 21;
 constexpr int kMaxHeads = 256;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxTokenStride = int64_t(1) << 26;  // eight rows are loaded with 32-bit offsets
 constexpr int64_t kMaxPool = int64_t(1) << 22;
 constexpr int64_t kMaxTable = int64_t(1) << 20;
 constexpr int64_t kMaxLength = int64_t(1) << 30;
@@ -246,6 +247,9 @@ int paro_attention_prompt(const paro_attention_shape *s, const void *q, const vo
   if ((rc = check_stride(s->k_token, "k_token")) || (rc = check_stride(s->k_head, "k_head")) ||
       (rc = check_stride(s->v_token, "v_token")) || (rc = check_stride(s->v_head, "v_head")))
     return rc;
+  if (s->k_token > kMaxTokenStride || s->v_token > kMaxTokenStride)
+    return fail(PARO_ERR_UNSUPPORTED, "k_token=%lld, v_token=%lld: at most %lld", (long long)s->k_token,
+                (long long)s->v_token, (long long)kMaxTokenStride);
   if (!cu_q || !cu_k) return fail(PARO_ERR_NULL, "cu_q and cu_k are required");
   if (!aligned(cu_q, 8) || !aligned(cu_k, 8)) return fail(PARO_ERR_ALIGN, "cu_q and cu_k must be 8-byte aligned");
   if (k_tokens > 0 && (!k || !v)) return fail(PARO_ERR_NULL, "k and v are required");

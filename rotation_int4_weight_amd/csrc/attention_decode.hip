@@ -151,9 +151,9 @@ __device__ __forceinline__ void step(State<DIM> &st, Tile<DIM> &t, const u32x4 (
   float sum = 0.f;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const uint32_t w = pack2<DT>(__builtin_amdgcn_exp2f(s[2 * u] - ref), __builtin_amdgcn_exp2f(s[2 * u + 1] - ref));
-    p[u] = w;
-    sum += act_to_f32<DT>(w & 0xffffu) + act_to_f32<DT>(w >> 16);
+    const float e0 = __builtin_amdgcn_exp2f(s[2 * u] - ref), e1 = __builtin_amdgcn_exp2f(s[2 * u + 1] - ref);
+    sum += e0 + e1;
+    p[u] = pack2<DT>(e0, e1);
   }
   st.l = st.l * keep + sum;
 #pragma unroll
@@ -204,8 +204,7 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
       if (h >= heads) q[s] = u32x4{0, 0, 0, 0};
     }
   }
-  int len = 0;
-  if (slot >= 0 && slot < a.kv.slots) len = min(max(a.kv.lengths[slot], 0), a.kv.max_pages << a.kv.page_shift);
+  const int len = a.kv.length(slot);
   // equal parts of whole steps
   const int part = len <= kWhole ? kWhole
                                  : (int)((((int64_t)len + plan.splits - 1) / plan.splits + kUnit - 1) / kUnit * kUnit);

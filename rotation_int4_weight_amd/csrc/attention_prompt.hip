@@ -1,0 +1,406 @@
+// attention_prompt.hip - attention over prompts (paro_attention_prompt over
+// packed K and V, paro_attention_prompt_cached over the cache's pages).
+//
+// A workgroup takes BM rows of one key-value head, a row being a (token,
+// query head of the group) pair, so that the heads that share K and V share
+// their tiles, short prompts fill a tile and the diagonal wastes little.  K
+// and V stream through LDS in tiles of 64 keys (two buffers, loaded straight
+// into LDS), and a wave keeps everything of its 32 rows in registers:
+//   S^T = K Q^T and O^T = V^T P^T on v_mfma_f32_32x32x16.  Both have the row
+//   in lane%32, so maxima and sums need one swap of lane halves.  S^T leaves
+//   half h of a wave with the keys 8n + 4h + 0..3 of each 32; the second
+//   product's contraction is numbered the same way, so the weights go from
+//   one product to the other without leaving their lane.  V^T fragments are
+//   read from row-major V by the transposing LDS read (16 lanes receive 16
+//   channels of 4 keys).
+//   Running maximum m and sum l: a tile's weights are exp2((s - m) scale2),
+//   relative to an m that is only moved (and what was summed before scaled)
+//   when some row's maximum rose by more than 2^8 over it: any m gives the
+//   same quotient, and 256 is far from the types' limits.
+// LDS rows are 16-byte chunks, chunk c of row r stored at c ^ f(r), so that
+// both reads touch every bank once.
+//
+// A masked key has weight 0, but 0 times a V that is not finite is NaN: a wave
+// whose sums are not all finite at the end computes its rows again, one by
+// one, with masked keys left out.
+#include <float.h>
+#include <math.h>
+
+#include "attention.hpp"
+#include "common.hpp"
+#include "mfma.hpp"
+
+namespace paro {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) void *lds_ptr;
+typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
+
+constexpr int kKeys = 64;  // keys per tile
+
+template <int DT>
+__device__ __forceinline__ f32x16 mfma32x32x16(const u32x4 &a, const u32x4 &b, const f32x16 &c) {
+  if constexpr (DT == kF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+
+// The chunk permutation of LDS row r (see the header).
+template <int DIM>
+__device__ __forceinline__ int swizzle(int r) {
+  if constexpr (DIM == 128) return ((r & 3) << 2) | ((r >> 2) & 3);
+  else return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+}
+
+// One sequence's part in a tile of rows.
+struct Rows {
+  int64_t q0;  // its first query row
+  int64_t k0;  // its first key (packed)
+  int n_q, n_k;
+  int index;            // tile of BM rows within the sequence and head
+  const int32_t *table; // cache
+};
+
+// The sequence of row tile t, by a scan of the sequences 64 at a time (every
+// lane's sequence: ceil(n_q * group / BM) tiles).  False: no such tile.
+template <bool CACHED, int BM>
+__device__ __forceinline__ bool find_tile(const AttentionArgs &a, int64_t t, Rows &r) {
+  const int lane = lane_id();
+  for (int s0 = 0; s0 < a.sequences; s0 += 64) {
+    const int s = s0 + lane;
+    int64_t q0 = 0, n = 0;
+    if (s < a.sequences) {
+      q0 = a.cu_q[s] < 0 ? 0 : a.cu_q[s];
+      const int64_t q1 = a.cu_q[s + 1] > a.q_tokens ? a.q_tokens : a.cu_q[s + 1];
+      n = q1 > q0 ? q1 - q0 : 0;
+    }
+    const int64_t tiles = (n * a.group + BM - 1) / BM;
+    int64_t ends = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t o = __shfl_up(ends, d, 64);
+      if (lane >= d) ends += o;
+    }
+    const uint64_t past = __ballot(ends > t);
+    if (past) {
+      const int j = __builtin_ctzll(past);
+      r.index = __builtin_amdgcn_readfirstlane((int)(t - __shfl(ends - tiles, j, 64)));
+      r.n_q = __builtin_amdgcn_readfirstlane((int)__shfl(n, j, 64));
+      const int64_t at = __shfl(q0, j, 64);
+      r.q0 = __builtin_amdgcn_readfirstlane((int)at);
+      const int sq = s0 + j;
+      if constexpr (CACHED) {
+        const int slot = a.slots[sq];
+        r.n_k = __builtin_amdgcn_readfirstlane(a.kv.length(slot));
+        r.table = a.kv.table + (int64_t)(r.n_k > 0 ? slot : 0) * a.kv.max_pages;
+        r.k0 = 0;
+      } else {
+        const int64_t k0 = a.cu_k[sq] < 0 ? 0 : a.cu_k[sq];
+        const int64_t k1 = a.cu_k[sq + 1] > a.k_tokens ? a.k_tokens : a.cu_k[sq + 1];
+        r.n_k = __builtin_amdgcn_readfirstlane(k1 > k0 ? (int)(k1 - k0) : 0);
+        r.k0 = __builtin_amdgcn_readfirstlane(k1 > k0 ? (int)k0 : 0);
+        r.table = nullptr;
+      }
+      return true;
+    }
+    t -= __shfl(ends, 63, 64);
+  }
+  return false;
+}
+
+template <bool CACHED>
+__device__ __forceinline__ int64_t page_base(const AttentionArgs &a, const Rows &r, int kvh, int dim, int64_t pos) {
+  int page = r.table[pos >> a.kv.page_shift];
+  page = page < 0 ? 0 : page >= a.kv.num_pages ? a.kv.num_pages - 1 : page;
+  return (int64_t)page * a.kv.page_stride +
+         (((int64_t)kvh << a.kv.page_shift) + (pos & ((1 << a.kv.page_shift) - 1))) * dim;
+}
+
+// One row by one wave with masked keys left out: the way around values that
+// are not finite.  Keys 64 at a time, lane j with key j's score; the output's
+// channels lie over the lanes.
+template <int DT, int DIM, bool CACHED>
+__device__ __forceinline__ void row_by_wave(const AttentionArgs &a, const Rows &r, int kvh, int token,
+                                                      int head) {
+  const int lane = lane_id();
+  const int64_t row = r.q0 + token;
+  const int seen = a.causal ? min(r.n_k, token + 1 + r.n_k - r.n_q) : r.n_k;
+  const uint16_t *q = a.q + row * a.q_token + head * a.q_head;
+  const auto at = [&](const uint16_t *packed, const uint16_t *paged, int64_t ts, int64_t hs, int j) {
+    if constexpr (CACHED) return paged + page_base<CACHED>(a, r, kvh, DIM, j);
+    else return packed + (r.k0 + j) * ts + kvh * hs;
+  };
+  float m = -INFINITY, l = 0.f, acc[DIM / 64] = {};
+  for (int j0 = 0; j0 < seen; j0 += 64) {
+    const int j = j0 + lane;
+    float s = -INFINITY;
+    if (j < seen) {
+      const uint16_t *k = at(a.k, a.kv.k, a.k_token, a.k_head, j);
+      s = 0.f;
+      for (int d = 0; d < DIM; ++d) s = fmaf(act_to_f32<DT>(q[d]), act_to_f32<DT>(k[d]), s);
+      s *= a.scale;
+    }
+    float top = s;
+    for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
+    const float p = j < seen ? expf(s - ref) : 0.f, keep = expf(m - ref);
+    l = l * keep + p;
+    m = mn;
+    for (int c = 0; c < DIM / 64; ++c) acc[c] *= keep;
+    const int n = min(64, seen - j0);
+    for (int jj = 0; jj < n; ++jj) {
+      const float w = __shfl(p, jj, 64);
+      const uint16_t *v = at(a.v, a.kv.v, a.v_token, a.v_head, j0 + jj);
+      for (int c = 0; c < DIM / 64; ++c) acc[c] = fmaf(w, act_to_f32<DT>(v[c * 64 + lane]), acc[c]);
+    }
+  }
+  for (int o = 32; o; o >>= 1) l += __shfl_xor(l, o, 64);
+  uint16_t *y = a.y + row * a.y_token + head * a.y_head;
+  for (int c = 0; c < DIM / 64; ++c)
+    y[c * 64 + lane] = (uint16_t)(pack2<DT>(seen > 0 ? acc[c] / l : 0.f, 0.f) & 0xffffu);
+}
+
+// Loads of one tile of 64 keys into LDS, 1 KB (kRowsPer rows) per wave
+// instruction; rows past the sequence's end are filled with zeros.
+template <int DIM, bool CACHED, int NW>
+struct Loader {
+  static constexpr int kRowsPer = 512 / DIM;
+  static constexpr int kLoads = kKeys * DIM * 2 / 1024 / NW;  // per wave, for K and for V
+  uint32_t k_off, v_off;  // this lane's byte offset from an instruction's first row
+  __device__ __forceinline__ void init(const AttentionArgs &a, int wave, int lane) {
+    constexpr int kChunks = DIM / 8;
+    const int r = lane / kChunks;
+    const int chunk = (lane % kChunks) ^ swizzle<DIM>(wave * kRowsPer + r);
+    k_off = (uint32_t)(r * (CACHED ? DIM : a.k_token) * 2 + chunk * 16);
+    v_off = (uint32_t)(r * (CACHED ? DIM : a.v_token) * 2 + chunk * 16);
+  }
+  // bytes from the first of `rows` rows (of token stride ts) to past the last
+  static __device__ __forceinline__ uint32_t span(int rows, int64_t ts) {
+    return rows <= 0 ? 0u : (uint32_t)((rows - 1) * ts * 2 + DIM * 2);
+  }
+  __device__ __forceinline__ void load(const AttentionArgs &a, const Rows &r, int kvh, int j0, char *k_lds, char *v_lds,
+                                       int wave) const {
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int i = wave + NW * n, row = i * kRowsPer, left = min(kRowsPer, r.n_k - (j0 + row));
+      const uint16_t *kb, *vb;
+      if constexpr (CACHED) {
+        const int64_t at = page_base<CACHED>(a, r, kvh, DIM, min(j0 + row, r.n_k - 1));
+        kb = a.kv.k + at;
+        vb = a.kv.v + at;
+      } else {
+        const int64_t at = r.k0 + j0 + row;
+        kb = a.k + at * a.k_token + kvh * a.k_head;
+        vb = a.v + at * a.v_token + kvh * a.v_head;
+      }
+      const __amdgpu_buffer_rsrc_t rk = raw_rsrc(kb, span(left, CACHED ? DIM : a.k_token));
+      const __amdgpu_buffer_rsrc_t rv = raw_rsrc(vb, span(left, CACHED ? DIM : a.v_token));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_ptr)(k_lds + 1024 * i), 16, k_off, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr)(v_lds + 1024 * i), 16, v_off, 0, 0, 0);
+    }
+  }
+};
+
+template <int DT, int DIM, bool CACHED, int NW>
+__global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionArgs a, int row_tiles) {
+  constexpr int BM = 32 * NW, KS = DIM / 16, DB = DIM / 32;
+  constexpr int kTileBytes = kKeys * DIM * 2;
+  __shared__ __align__(1024) char lds[4 * kTileBytes];  // K, K, V, V
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
+  const int h = lane >> 5, col = lane & 31;
+  // key-value heads next to each other in the launch order: workgroups go to
+  // the XCDs in turn, so with 8 heads each XCD's L2 holds one head's K and V;
+  // the longest tiles (a sequence's last) first
+  const int kvh = (int)(blockIdx.x % a.kv_heads);
+  const int64_t t = row_tiles - 1 - (int64_t)(blockIdx.x / a.kv_heads);
+  Rows r;
+  if (!find_tile<CACHED, BM>(a, t, r)) return;
+  const int rows = r.n_q * a.group;  // rows of the sequence and key-value head
+  const int base = r.index * BM + wave * 32;
+  const int mine = min(base + col, rows - 1);  // rows past the end repeat the last one and are not stored
+  const int token = mine / a.group, head = kvh * a.group + mine % a.group;
+  const int shift = r.n_k - r.n_q;
+  // keys that a row sees, and the fewest and most of the wave's and the workgroup's rows
+  const auto seen_by = [&](int row) {
+    const int n = a.causal ? min(r.n_k, row / a.group + 1 + shift) : r.n_k;
+    return max(n, 0);
+  };
+  const int seen = seen_by(mine);
+  const int wave_least = seen_by(min(base, rows - 1)), wave_most = seen_by(min(base + 31, rows - 1));
+  const int most = __builtin_amdgcn_readfirstlane(seen_by(min((r.index + 1) * BM, rows) - 1));
+
+  // Q^T fragments: row lane%32, channels 16 s + 8 h..; a negative scale goes to Q
+  u32x4 q[KS];
+  {
+    const uint16_t *qp = a.q + (r.q0 + token) * a.q_token + head * a.q_head + 8 * h;
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      q[s] = *reinterpret_cast<const u32x4 *>(qp + 16 * s);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) q[s][c] ^= flip;
+    }
+  }
+  const float scale2 = fmaxf(fabsf(a.scale) * 1.44269504088896340736f, FLT_MIN);
+
+  // LDS addresses: K fragment s at k_at[s] (+ 32 rows), V^T fragment (db, half) at v_at (+ 16 rows per step)
+  uint32_t k_at[KS], v_at[DB][2];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) k_at[s] = (uint32_t)(col * DIM * 2 + (((2 * s + h) ^ swizzle<DIM>(col)) << 4));
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int row = 8 * u + 4 * h + ((lane >> 2) & 3);
+      const int chunk = 4 * db + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+      v_at[db][u] = (uint32_t)(2 * kTileBytes + row * DIM * 2 + ((chunk ^ swizzle<DIM>(row)) << 4) + 8 * (lane & 1));
+    }
+
+  f32x16 o[DB];
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
+  float m = -INFINITY, l = 0.f;
+
+  Loader<DIM, CACHED, NW> loader;
+  loader.init(a, wave, lane);
+  if (most > 0) loader.load(a, r, kvh, 0, lds, lds + 2 * kTileBytes, wave);
+  for (int j0 = 0, buf = 0; j0 < most; j0 += kKeys, buf ^= 1) {
+    // this tile has landed, and every wave is done with the other buffer
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (j0 + kKeys < most)
+      loader.load(a, r, kvh, j0 + kKeys, lds + (buf ^ 1) * kTileBytes, lds + (2 + (buf ^ 1)) * kTileBytes, wave);
+    if (j0 >= wave_most) continue;  // no row of this wave sees the tile
+    const char *tile = lds + buf * kTileBytes;
+    f32x16 s[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[kb][i] = 0.f;
+#pragma unroll
+    for (int x = 0; x < KS; ++x)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        const u32x4 k = *reinterpret_cast<const u32x4 *>(tile + k_at[x] + kb * 32 * DIM * 2);
+        s[kb] = mfma32x32x16<DT>(k, q[x], s[kb]);
+      }
+    if (j0 + kKeys > wave_least) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (j0 + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) >= seen) s[kb][i] = -INFINITY;
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
+    {
+      const uint32_t u = __float_as_uint(top);
+      const auto w = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+      top = fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    }
+    // true too where m is still -infinity and top is not
+    if (__any((top - m) * scale2 > 8.f)) {
+      const float mn = fmaxf(m, top);
+      const float keep = m == mn ? 1.f : __builtin_amdgcn_exp2f((m - mn) * scale2);
+      m = mn;
+      l *= keep;
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[db][i] *= keep;
+    }
+    const float ref = m == -INFINITY ? 0.f : m * scale2;
+    u32x4 p[4];
+    float sums[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], scale2, -ref));
+        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i + 1], scale2, -ref));
+        sums[(i >> 1) & 3] += e0 + e1;
+        p[2 * kb + (i >> 3)][(i & 7) >> 1] = pack2<DT>(e0, e1);
+      }
+    l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+      for (int db = 0; db < DB; ++db) {
+        const char *vt = tile + ks * 16 * DIM * 2;
+        const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(vt + v_at[db][0]));
+        const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(vt + v_at[db][1]));
+        const u32x2 w0 = __builtin_bit_cast(u32x2, v0), w1 = __builtin_bit_cast(u32x2, v1);
+        o[db] = mfma32x32x16<DT>(u32x4{w0[0], w0[1], w1[0], w1[1]}, p[ks], o[db]);
+      }
+  }
+
+  {
+    const uint32_t u = __float_as_uint(l);
+    const auto w = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    l = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+  }
+  const bool stored = base + col < rows;
+  const float inv = seen > 0 ? 1.f / l : 0.f;
+  float worst = 0.f;  // NaN as soon as one value is not finite (x * 0 is NaN then)
+  uint16_t *y = a.y + (r.q0 + token) * a.y_token + head * a.y_head + 8 * h;
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {  // channels 32 db + 16 n: half h holds 4 h.. and 8 + 4 h..
+      uint32_t w[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float x0 = o[db][8 * n + 4 * u + 2 * c] * inv, x1 = o[db][8 * n + 4 * u + 2 * c + 1] * inv;
+          worst = __builtin_fmaf(x0, 0.f, worst);
+          worst = __builtin_fmaf(x1, 0.f, worst);
+          w[u][c] = seen > 0 ? pack2<DT>(x0, x1) : 0u;
+        }
+      // lanes 0..31 take the lower 8 channels of their row, lanes 32..63 the upper
+      const auto lo = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+      const auto hi = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+      if (stored) *reinterpret_cast<u32x4 *>(y + 32 * db + 16 * n) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+    }
+  if (__any(stored && worst != 0.f)) {
+#pragma unroll 1
+    for (int i = 0; i < 32 && base + i < rows; ++i)
+      row_by_wave<DT, DIM, CACHED>(a, r, kvh, (base + i) / a.group, kvh * a.group + (base + i) % a.group);
+  }
+}
+
+template <bool CACHED>
+hipError_t launch(const AttentionArgs &a, hipStream_t st) {
+  constexpr int NW = 4, BM = 32 * NW;
+  const int64_t tiles = a.q_tokens * a.group / BM + a.sequences;
+  const dim3 grid((unsigned)(tiles * a.kv_heads));
+#define PARO_PROMPT(DT, DIM) \
+  hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, NW>), grid, dim3(64 * NW), 0, st, a, (int)tiles)
+  if (a.dt == kF16) {
+    if (a.head_dim == 64) PARO_PROMPT(kF16, 64);
+    else PARO_PROMPT(kF16, 128);
+  } else {
+    if (a.head_dim == 64) PARO_PROMPT(kBF16, 64);
+    else PARO_PROMPT(kBF16, 128);
+  }
+#undef PARO_PROMPT
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attention_prompt(const AttentionArgs &a, bool cached, hipStream_t st) {
+  return cached ? launch<true>(a, st) : launch<false>(a, st);
+}
+
+}  // namespace paro
