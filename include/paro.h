@@ -562,7 +562,7 @@ typedef struct {
  *   nondecreasing from 0 to q_tokens (k_tokens); entries are clamped into
  *   that range and a sequence that would end before it starts is empty.
  *   Rows of y outside every sequence are not written.
- * sequences <= 16384, q_tokens and k_tokens <= 2^21, k_token and v_token <= 2^26.
+ * sequences <= 16384, q_tokens and k_tokens <= 2^21, k_token and v_token <= 2^24.
  */
 int paro_attention_prompt(const paro_attention_shape *shape, const void *q, const void *k, const void *v,
                           paro_dtype dt, const int64_t *cu_q, const int64_t *cu_k, int64_t sequences,

@@ -23,7 +23,7 @@ using paro::overlap;
 constexpr int64_t kMaxRows = int64_t(1) << 21;
 constexpr int kMaxHeads = 256;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
-constexpr int64_t kMaxTokenStride = int64_t(1) << 26;  // eight rows are loaded with 32-bit offsets
+constexpr int64_t kMaxTokenStride = int64_t(1) << 24;  // a tile of 64 keys is loaded with 32-bit offsets
 constexpr int64_t kMaxPool = int64_t(1) << 22;
 constexpr int64_t kMaxTable = int64_t(1) << 20;
 constexpr int64_t kMaxLength = int64_t(1) << 30;

@@ -26,6 +26,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "attention.hpp"
 #include "common.hpp"
 #include "mfma.hpp"
@@ -49,6 +51,13 @@ __device__ __forceinline__ f32x16 mfma32x32x16(const u32x4 &a, const u32x4 &b, c
   else
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
+}
+
+// Two floats to the type, rounded to nearest even, by one instruction.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2_rne(float lo, float hi) {
+  if constexpr (DT == kF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, f16x2));
+  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
 // The chunk permutation of LDS row r (see the header).
@@ -166,44 +175,59 @@ __device__ __forceinline__ void row_by_wave(const AttentionArgs &a, const Rows &
     y[c * 64 + lane] = (uint16_t)(pack2<DT>(seen > 0 ? acc[c] / l : 0.f, 0.f) & 0xffffu);
 }
 
-// Loads of one tile of 64 keys into LDS, 1 KB (kRowsPer rows) per wave
-// instruction; rows past the sequence's end are filled with zeros.
+// Loads of a tile's K or V into LDS, 1 KB (kRowsPer rows) per wave
+// instruction; rows past the sequence's end are filled with zeros.  Packed
+// tiles are one buffer; in the cache the rows of an instruction lie in one
+// page, whose index is looked up a tile ahead.
 template <int DIM, bool CACHED, int NW>
 struct Loader {
   static constexpr int kRowsPer = 512 / DIM;
-  static constexpr int kLoads = kKeys * DIM * 2 / 1024 / NW;  // per wave, for K and for V
-  uint32_t k_off, v_off;  // this lane's byte offset from an instruction's first row
-  __device__ __forceinline__ void init(const AttentionArgs &a, int wave, int lane) {
+  static constexpr int kLoads = kKeys * DIM * 2 / 1024 / NW;  // per wave and tile
+  static constexpr int kRowStep = kRowsPer * NW;              // rows between a wave's loads
+  const uint16_t *from;  // packed: the head's first key; cache: the head in page 0
+  int64_t token;         // elements between keys
+  uint32_t off[kLoads];  // this lane's byte offsets (cache: one)
+  int pages[CACHED ? kLoads : 1];
+
+  __device__ __forceinline__ void init(const AttentionArgs &a, const Rows &r, const uint16_t *packed, int64_t ts,
+                                       int64_t hs, const uint16_t *paged, int kvh, int wave, int lane) {
     constexpr int kChunks = DIM / 8;
-    const int r = lane / kChunks;
-    const int chunk = (lane % kChunks) ^ swizzle<DIM>(wave * kRowsPer + r);
-    k_off = (uint32_t)(r * (CACHED ? DIM : a.k_token) * 2 + chunk * 16);
-    v_off = (uint32_t)(r * (CACHED ? DIM : a.v_token) * 2 + chunk * 16);
-  }
-  // bytes from the first of `rows` rows (of token stride ts) to past the last
-  static __device__ __forceinline__ uint32_t span(int rows, int64_t ts) {
-    return rows <= 0 ? 0u : (uint32_t)((rows - 1) * ts * 2 + DIM * 2);
-  }
-  __device__ __forceinline__ void load(const AttentionArgs &a, const Rows &r, int kvh, int j0, char *k_lds, char *v_lds,
-                                       int wave) const {
+    const int row = wave * kRowsPer + lane / kChunks;
+    const int chunk = (lane % kChunks) ^ swizzle<DIM>(row);
+    token = CACHED ? DIM : ts;
+    from = CACHED ? paged + ((int64_t)kvh << a.kv.page_shift) * DIM : packed + r.k0 * ts + kvh * hs;
 #pragma unroll
-    for (int n = 0; n < kLoads; ++n) {
-      const int i = wave + NW * n, row = i * kRowsPer, left = min(kRowsPer, r.n_k - (j0 + row));
-      const uint16_t *kb, *vb;
-      if constexpr (CACHED) {
-        const int64_t at = page_base<CACHED>(a, r, kvh, DIM, min(j0 + row, r.n_k - 1));
-        kb = a.kv.k + at;
-        vb = a.kv.v + at;
-      } else {
-        const int64_t at = r.k0 + j0 + row;
-        kb = a.k + at * a.k_token + kvh * a.k_head;
-        vb = a.v + at * a.v_token + kvh * a.v_head;
+    for (int n = 0; n < kLoads; ++n)
+      off[n] = (uint32_t)((CACHED ? lane / kChunks : row + n * kRowStep) * token * 2 + chunk * 16);
+    if constexpr (CACHED) look_up(a, r, 0, wave);
+  }
+  __device__ __forceinline__ void look_up(const AttentionArgs &a, const Rows &r, int j0, int wave) {
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n)
+      pages[n] = r.table[min(j0 + wave * kRowsPer + n * kRowStep, r.n_k - 1) >> a.kv.page_shift];
+  }
+  // the tile at key j0 (after look_up of it), and the look-up of the one after
+  __device__ __forceinline__ void load(const AttentionArgs &a, const Rows &r, int j0, char *to, int wave) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass does not know the buffer type
+    if constexpr (CACHED) {
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) {
+        const int row = j0 + wave * kRowsPer + n * kRowStep, left = min(kRowsPer, r.n_k - row);
+        const int page = min(max(pages[n], 0), a.kv.num_pages - 1);
+        const uint16_t *p = from + page * a.kv.page_stride + (row & ((1 << a.kv.page_shift) - 1)) * DIM;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(raw_rsrc(p, left > 0 ? (uint32_t)left * DIM * 2 : 0u),
+                                                 (lds_ptr)(to + 1024 * (wave + NW * n)), 16, off[0], 0, 0, 0);
       }
-      const __amdgpu_buffer_rsrc_t rk = raw_rsrc(kb, span(left, CACHED ? DIM : a.k_token));
-      const __amdgpu_buffer_rsrc_t rv = raw_rsrc(vb, span(left, CACHED ? DIM : a.v_token));
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_ptr)(k_lds + 1024 * i), 16, k_off, 0, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr)(v_lds + 1024 * i), 16, v_off, 0, 0, 0);
+      look_up(a, r, j0 + kKeys, wave);
+    } else {
+      const int left = min(kKeys, r.n_k - j0);
+      const __amdgpu_buffer_rsrc_t rs =
+          raw_rsrc(from + j0 * token, left > 0 ? (uint32_t)((left - 1) * token * 2 + DIM * 2) : 0u);
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(to + 1024 * (wave + NW * n)), 16, off[n], 0, 0, 0);
     }
+#endif
   }
 };
 
@@ -269,15 +293,22 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
     for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
   float m = -INFINITY, l = 0.f;
 
-  Loader<DIM, CACHED, NW> loader;
-  loader.init(a, wave, lane);
-  if (most > 0) loader.load(a, r, kvh, 0, lds, lds + 2 * kTileBytes, wave);
-  for (int j0 = 0, buf = 0; j0 < most; j0 += kKeys, buf ^= 1) {
+  Loader<DIM, CACHED, NW> load_k, load_v;
+  if (most > 0) {
+    load_k.init(a, r, a.k, a.k_token, a.k_head, a.kv.k, kvh, wave, lane);
+    load_v.init(a, r, a.v, a.v_token, a.v_head, a.kv.v, kvh, wave, lane);
+    load_k.load(a, r, 0, lds, wave);
+    load_v.load(a, r, 0, lds + 2 * kTileBytes, wave);
+  }
+  const auto step = [&](int j0, auto which) __attribute__((always_inline)) {
+    constexpr int buf = decltype(which)::value;
     // this tile has landed, and every wave is done with the other buffer
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (j0 + kKeys < most)
-      loader.load(a, r, kvh, j0 + kKeys, lds + (buf ^ 1) * kTileBytes, lds + (2 + (buf ^ 1)) * kTileBytes, wave);
-    if (j0 >= wave_most) continue;  // no row of this wave sees the tile
+    if (j0 + kKeys < most) {
+      load_k.load(a, r, j0 + kKeys, lds + (buf ^ 1) * kTileBytes, wave);
+      load_v.load(a, r, j0 + kKeys, lds + (2 + (buf ^ 1)) * kTileBytes, wave);
+    }
+    if (j0 >= wave_most) return;  // no row of this wave sees the tile
     const char *tile = lds + buf * kTileBytes;
     f32x16 s[2];
 #pragma unroll
@@ -329,7 +360,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
         const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], scale2, -ref));
         const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i + 1], scale2, -ref));
         sums[(i >> 1) & 3] += e0 + e1;
-        p[2 * kb + (i >> 3)][(i & 7) >> 1] = pack2<DT>(e0, e1);
+        p[2 * kb + (i >> 3)][(i & 7) >> 1] = pack2_rne<DT>(e0, e1);
       }
     l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
 #pragma unroll
@@ -342,6 +373,10 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
         const u32x2 w0 = __builtin_bit_cast(u32x2, v0), w1 = __builtin_bit_cast(u32x2, v1);
         o[db] = mfma32x32x16<DT>(u32x4{w0[0], w0[1], w1[0], w1[1]}, p[ks], o[db]);
       }
+  };
+  for (int j0 = 0; j0 < most; j0 += 2 * kKeys) {
+    step(j0, std::integral_constant<int, 0>());
+    if (j0 + kKeys < most) step(j0 + kKeys, std::integral_constant<int, 1>());
   }
 
   {
@@ -365,7 +400,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
           const float x0 = o[db][8 * n + 4 * u + 2 * c] * inv, x1 = o[db][8 * n + 4 * u + 2 * c + 1] * inv;
           worst = __builtin_fmaf(x0, 0.f, worst);
           worst = __builtin_fmaf(x1, 0.f, worst);
-          w[u][c] = seen > 0 ? pack2<DT>(x0, x1) : 0u;
+          w[u][c] = seen > 0 ? pack2_rne<DT>(x0, x1) : 0u;
         }
       // lanes 0..31 take the lower 8 channels of their row, lanes 32..63 the upper
       const auto lo = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
