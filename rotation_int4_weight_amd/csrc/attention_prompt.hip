@@ -42,6 +42,7 @@ typedef __attribute__((address_space(3))) void *lds_ptr;
 typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
 
 constexpr int kKeys = 64;  // keys per tile
+constexpr int kFewTiles = 96;
 
 template <int DT>
 __device__ __forceinline__ f32x16 mfma32x32x16(const u32x4 &a, const u32x4 &b, const f32x16 &c) {
@@ -175,69 +176,148 @@ __device__ __forceinline__ void row_by_wave(const AttentionArgs &a, const Rows &
     y[c * 64 + lane] = (uint16_t)(pack2<DT>(seen > 0 ? acc[c] / l : 0.f, 0.f) & 0xffffu);
 }
 
-// Loads of a tile's K or V into LDS, 1 KB (kRowsPer rows) per wave
+// Loads of a tile's K and V into LDS, 1 KB (kRowsPer rows) per wave
 // instruction; rows past the sequence's end are filled with zeros.  Packed
-// tiles are one buffer; in the cache the rows of an instruction lie in one
-// page, whose index is looked up a tile ahead.
-template <int DIM, bool CACHED, int NW>
+// tiles are one buffer; in the cache a buffer is up to 16 rows, which lie in
+// one page, and the page's index is looked up a tile ahead.
+template <int DIM, bool CACHED, int NW, int KEYS>
 struct Loader {
   static constexpr int kRowsPer = 512 / DIM;
-  static constexpr int kLoads = kKeys * DIM * 2 / 1024 / NW;  // per wave and tile
-  static constexpr int kRowStep = kRowsPer * NW;              // rows between a wave's loads
-  const uint16_t *from;  // packed: the head's first key; cache: the head in page 0
-  int64_t token;         // elements between keys
-  uint32_t off[kLoads];  // this lane's byte offsets (cache: one)
-  int pages[CACHED ? kLoads : 1];
+  static constexpr int kLoads = KEYS * DIM * 2 / 1024 / NW;  // per wave and tile, NW waves sharing it
+  static constexpr int kRowStep = kRowsPer * NW;             // rows between a wave's loads
+  static constexpr int kPerBuffer = !CACHED ? kLoads : kRowStep < 16 ? 16 / kRowStep : 1;
+  static constexpr int kBuffers = kLoads / kPerBuffer;
+  const uint16_t *k, *v;      // packed: the head's first key; cache: the head in page 0
+  uint32_t k_off[kPerBuffer], v_off[CACHED ? 1 : kPerBuffer];  // this lane's byte offsets in a buffer
+  int pages[kBuffers];
 
-  __device__ __forceinline__ void init(const AttentionArgs &a, const Rows &r, const uint16_t *packed, int64_t ts,
-                                       int64_t hs, const uint16_t *paged, int kvh, int wave, int lane) {
+  __device__ __forceinline__ void init(const AttentionArgs &a, const Rows &r, int kvh, int j0, int wave, int lane) {
     constexpr int kChunks = DIM / 8;
-    const int row = wave * kRowsPer + lane / kChunks;
-    const int chunk = (lane % kChunks) ^ swizzle<DIM>(row);
-    token = CACHED ? DIM : ts;
-    from = CACHED ? paged + ((int64_t)kvh << a.kv.page_shift) * DIM : packed + r.k0 * ts + kvh * hs;
+    const int64_t in_page = ((int64_t)kvh << a.kv.page_shift) * DIM;
+    k = CACHED ? a.kv.k + in_page : a.k + r.k0 * a.k_token + kvh * a.k_head;
+    v = CACHED ? a.kv.v + in_page : a.v + r.k0 * a.v_token + kvh * a.v_head;
 #pragma unroll
-    for (int n = 0; n < kLoads; ++n)
-      off[n] = (uint32_t)((CACHED ? lane / kChunks : row + n * kRowStep) * token * 2 + chunk * 16);
-    if constexpr (CACHED) look_up(a, r, 0, wave);
+    for (int n = 0; n < kPerBuffer; ++n) {
+      const int row = wave * kRowsPer + n * kRowStep + lane / kChunks;
+      const int chunk = ((lane % kChunks) ^ swizzle<DIM>(row)) * 16;
+      if constexpr (CACHED) {
+        k_off[n] = (uint32_t)((n * kRowStep + lane / kChunks) * DIM * 2 + chunk);
+      } else {
+        k_off[n] = (uint32_t)(row * a.k_token * 2 + chunk);
+        v_off[n] = (uint32_t)(row * a.v_token * 2 + chunk);
+      }
+    }
+    if constexpr (CACHED) look_up(a, r, j0, wave);
   }
   __device__ __forceinline__ void look_up(const AttentionArgs &a, const Rows &r, int j0, int wave) {
 #pragma unroll
-    for (int n = 0; n < kLoads; ++n)
-      pages[n] = r.table[min(j0 + wave * kRowsPer + n * kRowStep, r.n_k - 1) >> a.kv.page_shift];
+    for (int b = 0; b < kBuffers; ++b)
+      pages[b] = r.table[min(j0 + wave * kRowsPer + b * kPerBuffer * kRowStep, r.n_k - 1) >> a.kv.page_shift];
   }
-  // the tile at key j0 (after look_up of it), and the look-up of the one after
-  __device__ __forceinline__ void load(const AttentionArgs &a, const Rows &r, int j0, char *to, int wave) {
+  // the tile at key j0 (after look_up of it), and the look-up of the next one, `step` keys on
+  __device__ __forceinline__ void load(const AttentionArgs &a, const Rows &r, int j0, int step, char *to_k, char *to_v,
+                                       int wave) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass does not know the buffer type
-    if constexpr (CACHED) {
 #pragma unroll
-      for (int n = 0; n < kLoads; ++n) {
-        const int row = j0 + wave * kRowsPer + n * kRowStep, left = min(kRowsPer, r.n_k - row);
-        const int page = min(max(pages[n], 0), a.kv.num_pages - 1);
-        const uint16_t *p = from + page * a.kv.page_stride + (row & ((1 << a.kv.page_shift) - 1)) * DIM;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(raw_rsrc(p, left > 0 ? (uint32_t)left * DIM * 2 : 0u),
-                                                 (lds_ptr)(to + 1024 * (wave + NW * n)), 16, off[0], 0, 0, 0);
+    for (int b = 0; b < kBuffers; ++b) {
+      __amdgpu_buffer_rsrc_t rk, rv;
+      if constexpr (CACHED) {
+        const int row = j0 + wave * kRowsPer + b * kPerBuffer * kRowStep;
+        const int left = min(kPerBuffer == 1 ? kRowsPer : 16, r.n_k - row);
+        const int page = min(max(pages[b], 0), a.kv.num_pages - 1);
+        const int64_t at = page * a.kv.page_stride + (row & ((1 << a.kv.page_shift) - 1)) * DIM;
+        const uint32_t bytes = left > 0 ? (uint32_t)left * DIM * 2 : 0u;
+        rk = raw_rsrc(k + at, bytes);
+        rv = raw_rsrc(v + at, bytes);
+      } else {
+        const int left = min(KEYS, r.n_k - j0);
+        rk = raw_rsrc(k + j0 * a.k_token, left > 0 ? (uint32_t)((left - 1) * a.k_token * 2 + DIM * 2) : 0u);
+        rv = raw_rsrc(v + j0 * a.v_token, left > 0 ? (uint32_t)((left - 1) * a.v_token * 2 + DIM * 2) : 0u);
       }
-      look_up(a, r, j0 + kKeys, wave);
-    } else {
-      const int left = min(kKeys, r.n_k - j0);
-      const __amdgpu_buffer_rsrc_t rs =
-          raw_rsrc(from + j0 * token, left > 0 ? (uint32_t)((left - 1) * token * 2 + DIM * 2) : 0u);
 #pragma unroll
-      for (int n = 0; n < kLoads; ++n)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(to + 1024 * (wave + NW * n)), 16, off[n], 0, 0, 0);
+      for (int n = 0; n < kPerBuffer; ++n) {
+        const int at = 1024 * (wave + NW * (b * kPerBuffer + n));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_ptr)(to_k + at), 16, k_off[n], 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr)(to_v + at), 16, CACHED ? k_off[n] : v_off[n], 0, 0, 0);
+      }
     }
+    if constexpr (CACHED) look_up(a, r, j0 + step, wave);
 #endif
   }
 };
 
+// Joins the waves' sums of the same 32 rows (each relative to its own m2, the
+// maximum times scale2) and writes the rows: thread (row, 8 channels).
 template <int DT, int DIM, bool CACHED, int NW>
-__global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionArgs a, int row_tiles) {
-  constexpr int BM = 32 * NW, KS = DIM / 16, DB = DIM / 32;
-  constexpr int kTileBytes = kKeys * DIM * 2;
-  __shared__ __align__(1024) char lds[4 * kTileBytes];  // K, K, V, V
+__device__ __forceinline__ void join_waves(const AttentionArgs &a, const Rows &r, int kvh, int base, int rows,
+                                           const f32x16 (&o)[DIM / 32], float m2, float l, float *lds) {
+  constexpr int RS = DIM + 4;  // LDS row: its channels, then m2 and l
+  const int lane = lane_id(), wave = wave_id(), h = lane >> 5, col = lane & 31;
+  __syncthreads();  // every wave is done with its tiles
+  float *mine = lds + (wave * 32 + col) * RS;
+#pragma unroll
+  for (int db = 0; db < DIM / 32; ++db)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      *reinterpret_cast<f32x4 *>(mine + 32 * db + 2 * i + 4 * h) =
+          f32x4{o[db][i], o[db][i + 1], o[db][i + 2], o[db][i + 3]};
+  if (h == 0) {
+    mine[DIM] = m2;
+    mine[DIM + 1] = l;
+  }
+  __syncthreads();
+  bool bad = false;
+  for (int e = threadIdx.x; e < 32 * DIM / 8; e += 64 * NW) {
+    const int row = e / (DIM / 8), c = e % (DIM / 8) * 8;
+    if (base + row >= rows) continue;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, lds[(w * 32 + row) * RS + DIM]);
+    float sum = 0.f;
+    f32x4 x0 = {0.f, 0.f, 0.f, 0.f}, x1 = x0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float *part = lds + (w * 32 + row) * RS;
+      const float keep = part[DIM] == top ? 1.f : __builtin_amdgcn_exp2f(part[DIM] - top);
+      sum += keep * part[DIM + 1];
+      x0 += keep * *reinterpret_cast<const f32x4 *>(part + c);
+      x1 += keep * *reinterpret_cast<const f32x4 *>(part + c + 4);
+    }
+    const int token = (base + row) / a.group, head = kvh * a.group + (base + row) % a.group;
+    const bool any = r.n_k > 0 && (!a.causal || token + 1 + r.n_k - r.n_q > 0);
+    const float inv = any ? 1.f / sum : 0.f;
+    float worst = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x0[i] *= inv;
+      x1[i] *= inv;
+      worst = __builtin_fmaf(x0[i], 0.f, __builtin_fmaf(x1[i], 0.f, worst));
+    }
+    bad |= worst != 0.f;
+    const u32x4 y = {pack2_rne<DT>(x0[0], x0[1]), pack2_rne<DT>(x0[2], x0[3]), pack2_rne<DT>(x1[0], x1[1]),
+                     pack2_rne<DT>(x1[2], x1[3])};
+    *reinterpret_cast<u32x4 *>(a.y + (r.q0 + token) * a.y_token + head * a.y_head + c) = any ? y : u32x4{0, 0, 0, 0};
+  }
+  if (__syncthreads_or(bad)) {
+#pragma unroll 1
+    for (int i = wave; i < 32 && base + i < rows; i += NW)
+      row_by_wave<DT, DIM, CACHED>(a, r, kvh, (base + i) / a.group, kvh * a.group + (base + i) % a.group);
+  }
+}
+
+// SPLIT: the waves share 32 rows and take tiles of 32 keys in turn, each with
+// LDS buffers of its own; their sums are joined at the end.
+template <int DT, int DIM, bool CACHED, int NW, bool SPLIT>
+__global__ void __launch_bounds__(64 * NW, SPLIT && DIM == 128 ? 1 : 2) prompt_attention_kernel(AttentionArgs a, int row_tiles) {
+  constexpr int BM = SPLIT ? 32 : 32 * NW, KS = DIM / 16, DB = DIM / 32;
+  constexpr int KEYS = SPLIT ? 32 : kKeys, KB = KEYS / 32;
+  constexpr int kTileBytes = KEYS * DIM * 2;
+  __shared__ __align__(1024) char all_lds[(SPLIT ? NW : 1) * 4 * kTileBytes];  // K, K, V, V
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
   const int h = lane >> 5, col = lane & 31;
+  char *const lds = all_lds + (SPLIT ? wave * 4 * kTileBytes : 0);
+  const int begin = SPLIT ? wave * KEYS : 0, stride = SPLIT ? NW * KEYS : KEYS;  // this wave's tiles
+  const int share = SPLIT ? 0 : wave;                                            // of a tile's loads
   // key-value heads next to each other in the launch order: workgroups go to
   // the XCDs in turn, so with 8 heads each XCD's L2 holds one head's K and V;
   // the longest tiles (a sequence's last) first
@@ -246,7 +326,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
   Rows r;
   if (!find_tile<CACHED, BM>(a, t, r)) return;
   const int rows = r.n_q * a.group;  // rows of the sequence and key-value head
-  const int base = r.index * BM + wave * 32;
+  const int base = r.index * BM + (SPLIT ? 0 : wave * 32);
   const int mine = min(base + col, rows - 1);  // rows past the end repeat the last one and are not stored
   const int token = mine / a.group, head = kvh * a.group + mine % a.group;
   const int shift = r.n_k - r.n_q;
@@ -293,45 +373,42 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
     for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
   float m = -INFINITY, l = 0.f;
 
-  Loader<DIM, CACHED, NW> load_k, load_v;
-  if (most > 0) {
-    load_k.init(a, r, a.k, a.k_token, a.k_head, a.kv.k, kvh, wave, lane);
-    load_v.init(a, r, a.v, a.v_token, a.v_head, a.kv.v, kvh, wave, lane);
-    load_k.load(a, r, 0, lds, wave);
-    load_v.load(a, r, 0, lds + 2 * kTileBytes, wave);
+  Loader<DIM, CACHED, SPLIT ? 1 : NW, KEYS> loader;
+  if (begin < most) {
+    loader.init(a, r, kvh, begin, share, lane);
+    loader.load(a, r, begin, stride, lds, lds + 2 * kTileBytes, share);
   }
   const auto step = [&](int j0, auto which) __attribute__((always_inline)) {
     constexpr int buf = decltype(which)::value;
-    // this tile has landed, and every wave is done with the other buffer
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (j0 + kKeys < most) {
-      load_k.load(a, r, j0 + kKeys, lds + (buf ^ 1) * kTileBytes, wave);
-      load_v.load(a, r, j0 + kKeys, lds + (2 + (buf ^ 1)) * kTileBytes, wave);
-    }
+    // this tile has landed, and every wave that reads the other buffer is done with it
+    if constexpr (SPLIT) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (j0 + stride < most)
+      loader.load(a, r, j0 + stride, stride, lds + (buf ^ 1) * kTileBytes, lds + (2 + (buf ^ 1)) * kTileBytes, share);
     if (j0 >= wave_most) return;  // no row of this wave sees the tile
     const char *tile = lds + buf * kTileBytes;
-    f32x16 s[2];
+    f32x16 s[KB];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[kb][i] = 0.f;
 #pragma unroll
     for (int x = 0; x < KS; ++x)
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
+      for (int kb = 0; kb < KB; ++kb) {
         const u32x4 k = *reinterpret_cast<const u32x4 *>(tile + k_at[x] + kb * 32 * DIM * 2);
         s[kb] = mfma32x32x16<DT>(k, q[x], s[kb]);
       }
-    if (j0 + kKeys > wave_least) {
+    if (j0 + KEYS > wave_least) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (j0 + 32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) >= seen) s[kb][i] = -INFINITY;
     }
     float top = s[0][0];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
     {
@@ -351,10 +428,10 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
         for (int i = 0; i < 16; ++i) o[db][i] *= keep;
     }
     const float ref = m == -INFINITY ? 0.f : m * scale2;
-    u32x4 p[4];
+    u32x4 p[2 * KB];
     float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
         const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], scale2, -ref));
@@ -364,7 +441,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
       }
     l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
+    for (int ks = 0; ks < 2 * KB; ++ks)
 #pragma unroll
       for (int db = 0; db < DB; ++db) {
         const char *vt = tile + ks * 16 * DIM * 2;
@@ -374,15 +451,19 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
         o[db] = mfma32x32x16<DT>(u32x4{w0[0], w0[1], w1[0], w1[1]}, p[ks], o[db]);
       }
   };
-  for (int j0 = 0; j0 < most; j0 += 2 * kKeys) {
+  for (int j0 = begin; j0 < most; j0 += 2 * stride) {
     step(j0, std::integral_constant<int, 0>());
-    if (j0 + kKeys < most) step(j0 + kKeys, std::integral_constant<int, 1>());
+    if (j0 + stride < most) step(j0 + stride, std::integral_constant<int, 1>());
   }
 
   {
     const uint32_t u = __float_as_uint(l);
     const auto w = __builtin_amdgcn_permlane32_swap(u, u, false, false);
     l = __uint_as_float(w[0]) + __uint_as_float(w[1]);
+  }
+  if constexpr (SPLIT) {
+    join_waves<DT, DIM, CACHED, NW>(a, r, kvh, base, rows, o, m * scale2, l, reinterpret_cast<float *>(all_lds));
+    return;
   }
   const bool stored = base + col < rows;
   const float inv = seen > 0 ? 1.f / l : 0.f;
@@ -414,22 +495,27 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
   }
 }
 
-template <bool CACHED>
-hipError_t launch(const AttentionArgs &a, hipStream_t st) {
+template <int DT, int DIM, bool CACHED>
+hipError_t launch_typed(const AttentionArgs &a, hipStream_t st) {
   constexpr int NW = 4, BM = 32 * NW;
   const int64_t tiles = a.q_tokens * a.group / BM + a.sequences;
-  const dim3 grid((unsigned)(tiles * a.kv_heads));
-#define PARO_PROMPT(DT, DIM) \
-  hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, NW>), grid, dim3(64 * NW), 0, st, a, (int)tiles)
-  if (a.dt == kF16) {
-    if (a.head_dim == 64) PARO_PROMPT(kF16, 64);
-    else PARO_PROMPT(kF16, 128);
+  if (tiles * a.kv_heads <= kFewTiles && (CACHED || a.k_tokens > kKeys)) {
+    constexpr int SW = 512 / DIM;  // waves whose buffers fit the LDS
+    const int64_t small = a.q_tokens * a.group / 32 + a.sequences;
+    hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, SW, true>), dim3((unsigned)(small * a.kv_heads)),
+                       dim3(64 * SW), 0, st, a, (int)small);
   } else {
-    if (a.head_dim == 64) PARO_PROMPT(kBF16, 64);
-    else PARO_PROMPT(kBF16, 128);
+    hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, NW, false>), dim3((unsigned)(tiles * a.kv_heads)),
+                       dim3(64 * NW), 0, st, a, (int)tiles);
   }
-#undef PARO_PROMPT
   return hipGetLastError();
+}
+
+template <bool CACHED>
+hipError_t launch(const AttentionArgs &a, hipStream_t st) {
+  if (a.dt == kF16)
+    return a.head_dim == 64 ? launch_typed<kF16, 64, CACHED>(a, st) : launch_typed<kF16, 128, CACHED>(a, st);
+  return a.head_dim == 64 ? launch_typed<kBF16, 64, CACHED>(a, st) : launch_typed<kBF16, 128, CACHED>(a, st);
 }
 
 }  // namespace
