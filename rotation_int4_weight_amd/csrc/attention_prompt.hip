@@ -176,6 +176,26 @@ __device__ __forceinline__ void row_by_wave(const AttentionArgs &a, const Rows &
     y[c * 64 + lane] = (uint16_t)(pack2<DT>(seen > 0 ? acc[c] / l : 0.f, 0.f) & 0xffffu);
 }
 
+// One wave instruction of 64 x 16 bytes into LDS.  As asm where a wave counts
+// its own loads: for builtin loads the compiler makes every transposing LDS
+// read wait for all that are in flight.  There is no output register, the
+// tile loop waits by itself, and the wait states cover a descriptor or m0
+// written just before.
+__device__ __forceinline__ void load_lds(const uint16_t *base, uint32_t bytes, char *lds, uint32_t off) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr)lds);
+  const uint64_t b = (uint64_t)base;
+  const u32x4 r = {(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b),
+                   (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32) & 0xffffu),
+                   (uint32_t)__builtin_amdgcn_readfirstlane(bytes), (uint32_t)kRawBufferWord3};
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(r)
+               : "memory");
+}
+// All but the last n of this wave's vector-memory operations have completed.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
 // Loads of a tile's K and V into LDS, 1 KB (kRowsPer rows) per wave
 // instruction; rows past the sequence's end are filled with zeros.  Packed
 // tiles are one buffer; in the cache a buffer is up to 16 rows, which lie in
@@ -214,35 +234,50 @@ struct Loader {
     for (int b = 0; b < kBuffers; ++b)
       pages[b] = r.table[min(j0 + wave * kRowsPer + b * kPerBuffer * kRowStep, r.n_k - 1) >> a.kv.page_shift];
   }
-  // the tile at key j0 (after look_up of it), and the look-up of the next one, `step` keys on
-  __device__ __forceinline__ void load(const AttentionArgs &a, const Rows &r, int j0, int step, char *to_k, char *to_v,
-                                       int wave) {
+  // first element of buffer b's rows in the tile at key j0, and the bytes of its K or V rows there are
+  __device__ __forceinline__ int64_t buffer_at(const AttentionArgs &a, int j0, int b, int wave) const {
+    if constexpr (!CACHED) return j0;  // in keys
+    const int row = j0 + wave * kRowsPer + b * kPerBuffer * kRowStep;
+    const int page = min(max(pages[b], 0), a.kv.num_pages - 1);
+    return page * a.kv.page_stride + (row & ((1 << a.kv.page_shift) - 1)) * DIM;
+  }
+  __device__ __forceinline__ uint32_t buffer_bytes(const Rows &r, int j0, int b, int wave, int64_t token) const {
+    const int left = CACHED ? min(kPerBuffer == 1 ? kRowsPer : 16, r.n_k - (j0 + wave * kRowsPer + b * kPerBuffer * kRowStep))
+                            : min(KEYS, r.n_k - j0);
+    return left > 0 ? (uint32_t)((left - 1) * (CACHED ? DIM : token) * 2 + DIM * 2) : 0u;
+  }
+  // the tile at key j0 (after look_up of it), and the look-up of the next one
+  __device__ __forceinline__ void load(const AttentionArgs &a, const Rows &r, int j0, char *to_k, char *to_v, int wave) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass does not know the buffer type
 #pragma unroll
     for (int b = 0; b < kBuffers; ++b) {
-      __amdgpu_buffer_rsrc_t rk, rv;
-      if constexpr (CACHED) {
-        const int row = j0 + wave * kRowsPer + b * kPerBuffer * kRowStep;
-        const int left = min(kPerBuffer == 1 ? kRowsPer : 16, r.n_k - row);
-        const int page = min(max(pages[b], 0), a.kv.num_pages - 1);
-        const int64_t at = page * a.kv.page_stride + (row & ((1 << a.kv.page_shift) - 1)) * DIM;
-        const uint32_t bytes = left > 0 ? (uint32_t)left * DIM * 2 : 0u;
-        rk = raw_rsrc(k + at, bytes);
-        rv = raw_rsrc(v + at, bytes);
-      } else {
-        const int left = min(KEYS, r.n_k - j0);
-        rk = raw_rsrc(k + j0 * a.k_token, left > 0 ? (uint32_t)((left - 1) * a.k_token * 2 + DIM * 2) : 0u);
-        rv = raw_rsrc(v + j0 * a.v_token, left > 0 ? (uint32_t)((left - 1) * a.v_token * 2 + DIM * 2) : 0u);
-      }
+      const int64_t at = buffer_at(a, j0, b, wave);
+      const __amdgpu_buffer_rsrc_t rk =
+          raw_rsrc(k + (CACHED ? at : at * a.k_token), buffer_bytes(r, j0, b, wave, a.k_token));
+      const __amdgpu_buffer_rsrc_t rv =
+          raw_rsrc(v + (CACHED ? at : at * a.v_token), buffer_bytes(r, j0, b, wave, a.v_token));
 #pragma unroll
       for (int n = 0; n < kPerBuffer; ++n) {
-        const int at = 1024 * (wave + NW * (b * kPerBuffer + n));
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_ptr)(to_k + at), 16, k_off[n], 0, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr)(to_v + at), 16, CACHED ? k_off[n] : v_off[n], 0, 0, 0);
+        const int to = 1024 * (wave + NW * (b * kPerBuffer + n));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_ptr)(to_k + to), 16, k_off[n], 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr)(to_v + to), 16, CACHED ? k_off[n] : v_off[n], 0, 0, 0);
       }
     }
-    if constexpr (CACHED) look_up(a, r, j0 + step, wave);
+    if constexpr (CACHED) look_up(a, r, j0 + KEYS, wave);
 #endif
+  }
+  // K or V alone by asm loads (kLoads of them)
+  template <bool V>
+  __device__ __forceinline__ void load_one(const AttentionArgs &a, const Rows &r, int j0, char *to) {
+#pragma unroll
+    for (int b = 0; b < kBuffers; ++b) {
+      const int64_t at = buffer_at(a, j0, b, 0), token = V ? a.v_token : a.k_token;
+      const uint16_t *base = (V ? v : k) + (CACHED ? at : at * token);
+      const uint32_t bytes = buffer_bytes(r, j0, b, 0, token);
+#pragma unroll
+      for (int n = 0; n < kPerBuffer; ++n)
+        load_lds(base, bytes, to + 1024 * (b * kPerBuffer + n), V && !CACHED ? v_off[n] : k_off[n]);
+    }
   }
 };
 
@@ -275,7 +310,7 @@ __device__ __forceinline__ void join_waves(const AttentionArgs &a, const Rows &r
     for (int w = 0; w < NW; ++w) top = fmaxf(top, lds[(w * 32 + row) * RS + DIM]);
     float sum = 0.f;
     f32x4 x0 = {0.f, 0.f, 0.f, 0.f}, x1 = x0;
-#pragma unroll
+#pragma unroll 2
     for (int w = 0; w < NW; ++w) {
       const float *part = lds + (w * 32 + row) * RS;
       const float keep = part[DIM] == top ? 1.f : __builtin_amdgcn_exp2f(part[DIM] - top);
@@ -306,16 +341,20 @@ __device__ __forceinline__ void join_waves(const AttentionArgs &a, const Rows &r
 }
 
 // SPLIT: the waves share 32 rows and take tiles of 32 keys in turn, each with
-// LDS buffers of its own; their sums are joined at the end.
+// LDS buffers of its own (one for K, one for V, so that twice as many waves
+// fit: the next K is loaded once the scores are formed, the next V once the
+// values are summed); their sums are joined at the end.
 template <int DT, int DIM, bool CACHED, int NW, bool SPLIT>
-__global__ void __launch_bounds__(64 * NW, SPLIT && DIM == 128 ? 1 : 2) prompt_attention_kernel(AttentionArgs a, int row_tiles) {
+__global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionArgs a, int row_tiles) {
   constexpr int BM = SPLIT ? 32 : 32 * NW, KS = DIM / 16, DB = DIM / 32;
   constexpr int KEYS = SPLIT ? 32 : kKeys, KB = KEYS / 32;
   constexpr int kTileBytes = KEYS * DIM * 2;
-  __shared__ __align__(1024) char all_lds[(SPLIT ? NW : 1) * 4 * kTileBytes];  // K, K, V, V
+  constexpr int kBuffers = SPLIT ? 1 : 2;  // of K, then of V
+  constexpr int kJoinBytes = SPLIT ? NW * 32 * (DIM + 4) * 4 : 0, kAllBytes = (SPLIT ? NW : 1) * 2 * kBuffers * kTileBytes;
+  __shared__ __align__(1024) char all_lds[kJoinBytes > kAllBytes ? kJoinBytes : kAllBytes];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
   const int h = lane >> 5, col = lane & 31;
-  char *const lds = all_lds + (SPLIT ? wave * 4 * kTileBytes : 0);
+  char *const lds = all_lds + (SPLIT ? wave * 2 * kTileBytes : 0);
   const int begin = SPLIT ? wave * KEYS : 0, stride = SPLIT ? NW * KEYS : KEYS;  // this wave's tiles
   const int share = SPLIT ? 0 : wave;                                            // of a tile's loads
   // key-value heads next to each other in the launch order: workgroups go to
@@ -363,7 +402,7 @@ __global__ void __launch_bounds__(64 * NW, SPLIT && DIM == 128 ? 1 : 2) prompt_a
     for (int u = 0; u < 2; ++u) {
       const int row = 8 * u + 4 * h + ((lane >> 2) & 3);
       const int chunk = 4 * db + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-      v_at[db][u] = (uint32_t)(2 * kTileBytes + row * DIM * 2 + ((chunk ^ swizzle<DIM>(row)) << 4) + 8 * (lane & 1));
+      v_at[db][u] = (uint32_t)(kBuffers * kTileBytes + row * DIM * 2 + ((chunk ^ swizzle<DIM>(row)) << 4) + 8 * (lane & 1));
     }
 
   f32x16 o[DB];
@@ -376,16 +415,25 @@ __global__ void __launch_bounds__(64 * NW, SPLIT && DIM == 128 ? 1 : 2) prompt_a
   Loader<DIM, CACHED, SPLIT ? 1 : NW, KEYS> loader;
   if (begin < most) {
     loader.init(a, r, kvh, begin, share, lane);
-    loader.load(a, r, begin, stride, lds, lds + 2 * kTileBytes, share);
+    if constexpr (SPLIT) {
+      loader.template load_one<false>(a, r, begin, lds);
+      loader.template load_one<true>(a, r, begin, lds + kTileBytes);
+      if constexpr (CACHED) loader.look_up(a, r, begin + stride, share);
+    } else {
+      loader.load(a, r, begin, lds, lds + 2 * kTileBytes, share);
+    }
   }
   const auto step = [&](int j0, auto which) __attribute__((always_inline)) {
     constexpr int buf = decltype(which)::value;
-    // this tile has landed, and every wave that reads the other buffer is done with it
-    if constexpr (SPLIT) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (j0 + stride < most)
-      loader.load(a, r, j0 + stride, stride, lds + (buf ^ 1) * kTileBytes, lds + (2 + (buf ^ 1)) * kTileBytes, share);
-    if (j0 >= wave_most) return;  // no row of this wave sees the tile
+    const bool more = j0 + stride < most;
+    if constexpr (SPLIT) {
+      wait_loads<decltype(loader)::kLoads>();  // K has landed; V may be on its way
+    } else {
+      // this tile has landed, and every wave is done with the other buffer
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (more) loader.load(a, r, j0 + stride, lds + (buf ^ 1) * kTileBytes, lds + (2 + (buf ^ 1)) * kTileBytes, share);
+    }
+    if (!SPLIT && j0 >= wave_most) return;  // no row of this wave sees the tile
     const char *tile = lds + buf * kTileBytes;
     f32x16 s[KB];
 #pragma unroll
@@ -399,6 +447,10 @@ __global__ void __launch_bounds__(64 * NW, SPLIT && DIM == 128 ? 1 : 2) prompt_a
         const u32x4 k = *reinterpret_cast<const u32x4 *>(tile + k_at[x] + kb * 32 * DIM * 2);
         s[kb] = mfma32x32x16<DT>(k, q[x], s[kb]);
       }
+    if constexpr (SPLIT) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // K has been read
+      if (more) loader.template load_one<false>(a, r, j0 + stride, lds);
+    }
     if (j0 + KEYS > wave_least) {
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
@@ -440,6 +492,10 @@ __global__ void __launch_bounds__(64 * NW, SPLIT && DIM == 128 ? 1 : 2) prompt_a
         p[2 * kb + (i >> 3)][(i & 7) >> 1] = pack2_rne<DT>(e0, e1);
       }
     l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+    if constexpr (SPLIT) {  // V has landed; the next K may be on its way
+      if (more) wait_loads<decltype(loader)::kLoads>();
+      else wait_loads<0>();
+    }
 #pragma unroll
     for (int ks = 0; ks < 2 * KB; ++ks)
 #pragma unroll
@@ -450,10 +506,21 @@ __global__ void __launch_bounds__(64 * NW, SPLIT && DIM == 128 ? 1 : 2) prompt_a
         const u32x2 w0 = __builtin_bit_cast(u32x2, v0), w1 = __builtin_bit_cast(u32x2, v1);
         o[db] = mfma32x32x16<DT>(u32x4{w0[0], w0[1], w1[0], w1[1]}, p[ks], o[db]);
       }
+    if constexpr (SPLIT) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // V has been read
+      if (more) {
+        loader.template load_one<true>(a, r, j0 + stride, lds + kTileBytes);
+        if constexpr (CACHED) loader.look_up(a, r, j0 + 2 * stride, share);
+      }
+    }
   };
-  for (int j0 = begin; j0 < most; j0 += 2 * stride) {
-    step(j0, std::integral_constant<int, 0>());
-    if (j0 + stride < most) step(j0 + stride, std::integral_constant<int, 1>());
+  if constexpr (SPLIT) {
+    for (int j0 = begin; j0 < most; j0 += stride) step(j0, std::integral_constant<int, 0>());
+  } else {
+    for (int j0 = 0; j0 < most; j0 += 2 * kKeys) {
+      step(j0, std::integral_constant<int, 0>());
+      if (j0 + kKeys < most) step(j0 + kKeys, std::integral_constant<int, 1>());
+    }
   }
 
   {
@@ -500,7 +567,7 @@ hipError_t launch_typed(const AttentionArgs &a, hipStream_t st) {
   constexpr int NW = 4, BM = 32 * NW;
   const int64_t tiles = a.q_tokens * a.group / BM + a.sequences;
   if (tiles * a.kv_heads <= kFewTiles && (CACHED || a.k_tokens > kKeys)) {
-    constexpr int SW = 512 / DIM;  // waves whose buffers fit the LDS
+    constexpr int SW = 8;
     const int64_t small = a.q_tokens * a.group / 32 + a.sequences;
     hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, SW, true>), dim3((unsigned)(small * a.kv_heads)),
                        dim3(64 * SW), 0, st, a, (int)small);
