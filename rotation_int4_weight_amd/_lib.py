@@ -527,10 +527,12 @@ def _launch(fn, device, stream, *args):
     import torch
     if device.type != "cuda":
         raise ParoError(1, fn.__name__, f"tensors in device memory are required, not on {device}")
+    # the raw handle: looking up a Stream object takes longer than the rest of a call's checks
+    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream_handle(stream)
     if device.index == torch.cuda.current_device():
-        return fn(*args, _stream_handle(stream))
+        return fn(*args, handle)
     with torch.cuda.device(device):
-        return fn(*args, _stream_handle(stream))
+        return fn(*args, handle)
 
 
 def _shape_of(q, kv_heads, scale, causal, qs, ys, ks=(0, 0), vs=(0, 0)):

@@ -45,21 +45,22 @@ struct Pool {
 };
 
 // Exclusive prefix sum of v over the workgroup; total: the sum.
-__device__ __forceinline__ int block_scan(int v, int *wave_sums, int &total) {
-  int incl = v;
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T *wave_sums, T &total) {
+  T incl = v;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(incl, d, 64);
+    const T o = __shfl_up(incl, d, 64);
     if (lane_id() >= d) incl += o;
   }
   __syncthreads();  // wave_sums may still be read from the call before
   if (lane_id() == 63) wave_sums[wave_id()] = incl;
   __syncthreads();
-  int before = 0;
+  T before = 0;
   total = 0;
 #pragma unroll
   for (int w = 0; w < kPlanWaves; ++w) {
-    const int s = wave_sums[w];
+    const T s = wave_sums[w];
     before += w < wave_id() ? s : 0;
     total += s;
   }
@@ -124,65 +125,52 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(Pool p, cons
   __shared__ int first[kMaxSlots];  // first entry of a slot, then the first new position of an entry's pages
   __shared__ int ends[kMaxSlots];   // pages that an entry and those before it need
   __shared__ int wave_sums[kPlanWaves];
+  __shared__ int64_t long_sums[kPlanWaves];
   __shared__ int copies;
   if (threadIdx.x == 0) copies = 0;
   first_entries(slots, n, p.slots, first);
 
-  // what each entry needs; sums stop at num_pages + 1 (more is never granted)
-  const int i0 = threadIdx.x * kEntriesPerThread;
+  // what each entry needs, 1024 entries at a time (thread: one entry); the
+  // sums stop at num_pages + 1 (more is never granted)
   int need[kEntriesPerThread], at[kEntriesPerThread], newlen[kEntriesPerThread], shared[kEntriesPerThread];
-  int mine = 0;
+  int64_t run = 0;
 #pragma unroll
   for (int u = 0; u < kEntriesPerThread; ++u) {
-    const int i = i0 + u;
+    const int i = u * kPlanThreads + (int)threadIdx.x;
     need[u] = 0;
     newlen[u] = -1;  // refused
     shared[u] = -1;
     at[u] = 0;
-    if (i >= n) continue;
-    const int s = slots[i], g = grow[i];
-    if (s < 0 || s >= p.slots || first[s] != i || g < 0) continue;
-    const int len = p.lengths[s];
-    const int64_t most = (int64_t)p.max_pages << p.page_shift;
-    if (len < 0 || (int64_t)len + g > most) continue;
-    newlen[u] = len + g;
-    const int have = p.held(len), want = p.held(newlen[u]);
-    at[u] = have;
-    if (g > 0 && (len & ((1 << p.page_shift) - 1)) != 0) {
-      const int last = p.table[(int64_t)s * p.max_pages + have - 1];
-      if (last >= 0 && last < p.num_pages && p.refs[last] > 1) {
-        shared[u] = last;
-        at[u] = have - 1;
+    if (u * kPlanThreads >= n) continue;
+    const int s = i < n ? slots[i] : -1, g = i < n ? grow[i] : 0;
+    if (s >= 0 && s < p.slots && first[s] == i && g >= 0) {
+      const int len = p.lengths[s];
+      if (len >= 0 && (int64_t)len + g <= ((int64_t)p.max_pages << p.page_shift)) {
+        newlen[u] = len + g;
+        const int have = p.held(len);
+        at[u] = have;
+        if (g > 0 && (len & ((1 << p.page_shift) - 1)) != 0) {
+          const int last = p.table[(int64_t)s * p.max_pages + have - 1];
+          if (last >= 0 && last < p.num_pages && p.refs[last] > 1) {
+            shared[u] = last;
+            at[u] = have - 1;
+          }
+        }
+        need[u] = p.held(newlen[u]) - at[u];
       }
     }
-    need[u] = min(want - at[u], p.num_pages + 1);
-    mine = min(mine + need[u], p.num_pages + 1);
+    int64_t all;
+    const int64_t end = run + block_scan((int64_t)need[u], long_sums, all) + need[u];
+    run += all;
+    if (i < n) ends[i] = (int)min(end, (int64_t)p.num_pages + 1);
   }
+  const int total = (int)min(run, (int64_t)p.num_pages);
   __syncthreads();  // first[] is read no more as entries
-  int total;
-  // at most 1024 * (2^22 + 1) = 2^32: scanned in units that cannot overflow
-  // because each thread's sum is cut at num_pages + 1 <= 2^22 + 1 and the
-  // running sums are compared, not used, past num_pages
-  int64_t run;
-  {
-    // two scans: the low 16 and the high bits of the threads' sums
-    int lo_total, hi_total;
-    const int lo = block_scan(mine & 0xffff, wave_sums, lo_total);
-    const int hi = block_scan(mine >> 16, wave_sums, hi_total);
-    run = (int64_t)lo + ((int64_t)hi << 16);
-    const int64_t all = (int64_t)lo_total + ((int64_t)hi_total << 16);
-    total = (int)(all > p.num_pages ? p.num_pages : all);
-  }
 #pragma unroll
   for (int u = 0; u < kEntriesPerThread; ++u) {
-    const int i = i0 + u;
-    run = run + need[u] > p.num_pages ? (int64_t)p.num_pages + 1 : run + need[u];
-    if (i < n) {
-      ends[i] = (int)run;
-      first[i] = at[u];
-    }
+    const int i = u * kPlanThreads + (int)threadIdx.x;
+    if (i < n) first[i] = at[u];
   }
-  __syncthreads();
   const int found = scan_pages(
       p, total, wave_sums, [](int, int r) { return r == 0; },
       [&](int rank, int page) {
@@ -192,7 +180,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(Pool p, cons
   __syncthreads();  // the list is written, and every refs value that decides has been read
 #pragma unroll
   for (int u = 0; u < kEntriesPerThread; ++u) {
-    const int i = i0 + u;
+    const int i = u * kPlanThreads + (int)threadIdx.x;
     if (i >= n) continue;
     const bool yes = newlen[u] >= 0 && (need[u] == 0 || ends[i] <= free);
     granted[i] = yes;
@@ -232,8 +220,23 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(Pool p, cons
 // four 16-byte loads in flight.
 constexpr int kPiece = 16384;
 
-__global__ void __launch_bounds__(256) copy_pages_kernel(char *__restrict__ k, char *__restrict__ v, Work w, int layers,
+// MOVED: the pages leave their places for good, so the tables are rewritten too
+// (every workgroup takes some slots first).
+template <bool MOVED>
+__global__ void __launch_bounds__(256) copy_pages_kernel(char *__restrict__ k, char *__restrict__ v, Pool p,
+                                                         const int32_t *__restrict__ used_in, Work w, int layers,
                                                          int64_t num_pages, int64_t page_bytes) {
+  if constexpr (MOVED) {
+    const int used = used_in[0];
+    for (int s = blockIdx.x; s < p.slots; s += gridDim.x) {
+      const int pages = p.held(p.lengths[s]);
+      int32_t *row = p.table + (int64_t)s * p.max_pages;
+      for (int j = threadIdx.x; j < pages; j += 256) {
+        const int page = row[j];
+        if (page >= used && page < p.num_pages) row[j] = w.map[page];
+      }
+    }
+  }
   const int64_t copies = w.copies[0];
   const int pieces = (int)((page_bytes + kPiece - 1) / kPiece);
   const int64_t items = copies * layers * 2 * pieces;
@@ -353,15 +356,6 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Pool p, int3
   }
 }
 
-__global__ void __launch_bounds__(256) compact_table_kernel(Pool p, const int32_t *__restrict__ used_in, Work w) {
-  const int s = blockIdx.y, pages = p.held(p.lengths[s]), used = used_in[0];
-  int32_t *row = p.table + (int64_t)s * p.max_pages;
-  for (int j = blockIdx.x * 256 + threadIdx.x; j < pages; j += gridDim.x * 256) {
-    const int page = row[j];
-    if (page >= used && page < p.num_pages) row[j] = w.map[page];
-  }
-}
-
 // ---- append ----
 
 // A wave writes one row of K and of V.  Its sequence is found by a 64-way
@@ -430,12 +424,18 @@ Pool pool_of(const paro_kv_cache &c) {
   return p;
 }
 
-hipError_t launch_copies(const paro_kv_cache &c, const Work &w, int64_t most_copies, hipStream_t st) {
+// used: compaction's; null for copies that leave their sources in place
+hipError_t launch_copies(const paro_kv_cache &c, const Work &w, int64_t most_copies, const int32_t *used,
+                         hipStream_t st) {
   const int64_t page_bytes = (int64_t)c.kv_heads * c.page_size * c.head_dim * 2;
   const int64_t items = most_copies * c.layers * 2 * ((page_bytes + kPiece - 1) / kPiece);
-  const unsigned grid = (unsigned)std::min<int64_t>(items, 2048);
-  hipLaunchKernelGGL(copy_pages_kernel, dim3(grid), dim3(256), 0, st, (char *)c.k, (char *)c.v, w, c.layers, c.num_pages,
-                     page_bytes);
+  const dim3 grid((unsigned)std::min<int64_t>(std::max<int64_t>(items, used ? c.slots : 1), 2048)), block(256);
+  if (used)
+    hipLaunchKernelGGL(copy_pages_kernel<true>, grid, block, 0, st, (char *)c.k, (char *)c.v, pool_of(c), used, w,
+                       c.layers, c.num_pages, page_bytes);
+  else
+    hipLaunchKernelGGL(copy_pages_kernel<false>, grid, block, 0, st, (char *)c.k, (char *)c.v, pool_of(c), used, w,
+                       c.layers, c.num_pages, page_bytes);
   return hipGetLastError();
 }
 
@@ -451,7 +451,7 @@ hipError_t launch_kv_reserve(const paro_kv_cache &c, const int32_t *slots, const
   const Work w = work_of(work, c.num_pages);
   hipLaunchKernelGGL(reserve_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, pool_of(c), slots, grow, n, granted, w);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e : launch_copies(c, w, n, st);
+  return e != hipSuccess ? e : launch_copies(c, w, n, nullptr, st);
 }
 
 hipError_t launch_kv_fork(const paro_kv_cache &c, const int32_t *parents, const int32_t *children, int n,
@@ -475,12 +475,8 @@ hipError_t launch_kv_compact(const paro_kv_cache &c, int32_t *used, int32_t *wor
   const Work w = work_of(work, c.num_pages);
   const Pool p = pool_of(c);
   hipLaunchKernelGGL(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p, used, w);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const unsigned blocks = (unsigned)std::min((c.max_pages + 255) / 256, 16);
-  hipLaunchKernelGGL(compact_table_kernel, dim3(blocks, (unsigned)c.slots), dim3(256), 0, st, p, used, w);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  return launch_copies(c, w, c.num_pages / 2, st);
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : launch_copies(c, w, c.num_pages / 2, used, st);
 }
 
 hipError_t launch_kv_append(const KvLayer &kv, int kv_heads, int head_dim, const uint16_t *k, int64_t k_token,
