@@ -520,6 +520,78 @@ def bench_mxfp4(args, paro, synth, np, torch, dev):
     print(json.dumps(out), flush=True)
 
 
+ATTENTION_METRIC = "Attention between the q/k/v and the output projections: prompt TFLOP/s, decode cache GB/s, % of roofline"
+KERNEL_FILES["attention"] = ("attention_prompt.hip", "attention.hpp", "common.hpp", "mfma.hpp")
+KERNEL_FILES["attention_decode"] = ("attention_decode.hip", "attention.hpp", "common.hpp", "mfma.hpp")
+HEAD_DIM = 128  # the Llama-3-8B heads: q_proj has 32 of them, k_proj and v_proj 8
+
+
+def bench_attention(args, paro, synth, np, torch, dev):
+    """Time the attention of the decoder layer whose projections workload 4
+    is: --op attention, one causal prompt of the workload's tokens over packed
+    q, k, v (paro_attention_prompt); --op attention_decode, one serving step
+    of 64 sequences of that length over a paged cache (paro_kv_append, then
+    paro_attention_decode), the cache larger than the MALL."""
+    spec = synth.WORKLOADS[4]
+    layers = {name: O for name, _, O in spec["layers"]}
+    heads, kv_heads = layers["q_proj"] // HEAD_DIM, layers["k_proj"] // HEAD_DIM
+    M, tdt = spec["tokens"], torch.bfloat16
+    gen = torch.Generator(device=dev).manual_seed(0)
+    rand = lambda *shape: torch.randn(shape, device=dev, dtype=tdt, generator=gen)
+    stream = torch.cuda.current_stream()
+    if args.op == "attention":
+        nsets = max(1, -(-MALL_ROTATION_BYTES // (2 * M * (heads + 2 * kv_heads) * HEAD_DIM)))
+        sets = [(rand(M, heads, HEAD_DIM), rand(M, kv_heads, HEAD_DIM), rand(M, kv_heads, HEAD_DIM))
+                for _ in range(nsets)]
+        y = torch.empty_like(sets[0][0])
+        cu = torch.tensor([0, M], dtype=torch.int64, device=dev)
+        step = lambda i: paro.paro_attention_prompt(*sets[i % nsets], cu, cu, y, stream=stream)
+        work = 4.0 * HEAD_DIM * heads * M * (M + 1) / 2
+        unit, scale, peak, bound = "TFLOP/s", 1e12, MFMA_PEAK_TFLOPS, "mfma"
+        config = {"workload": "llama3-8b-attention-prompt-t%d-bf16" % M, "buffer_sets": nsets}
+    else:
+        rows, page = 64, 16
+        per = M // page
+        cache = paro.KVCache.empty(1, rows * per, kv_heads, page, HEAD_DIM, rows, per, tdt, device=dev)
+        cache.k.normal_(generator=gen)
+        cache.v.normal_(generator=gen)
+        order = torch.randperm(rows * per, device=dev, generator=gen).to(torch.int32)
+        cache.table.copy_(order.view(rows, per))
+        cache.refs.fill_(1)
+        cache.lengths.fill_(M)
+        slots = torch.arange(rows, dtype=torch.int32, device=dev)
+        q, k, v = rand(rows, heads, HEAD_DIM), rand(rows, kv_heads, HEAD_DIM), rand(rows, kv_heads, HEAD_DIM)
+        y = torch.empty_like(q)
+        ws = paro.make_workspace(paro.paro_attention_decode_workspace_bytes(cache, rows, heads), device=dev)
+
+        def step(i):
+            paro.paro_kv_append(cache, 0, k, v, slots, stream=stream)
+            paro.paro_attention_decode(cache, 0, q, slots, y, ws, stream=stream)
+        work = 4.0 * rows * M * kv_heads * HEAD_DIM  # K and V read once
+        unit, scale, peak, bound = "GB/s", 1e9, HBM_PEAK_GBS, "hbm"
+        config = {"workload": "llama3-8b-attention-decode-r%d-t%d-bf16" % (rows, M), "page_size": page}
+    for i in range(args.warmup):
+        step(i)
+    torch.cuda.synchronize()
+    t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    t0.record(stream)
+    for i in range(args.steps):
+        step(i)
+    t1.record(stream)
+    torch.cuda.synchronize()
+    us = t0.elapsed_time(t1) * 1e3 / args.steps
+    value = work / (us * 1e-6) / scale
+    print(json.dumps({
+        "metric": ATTENTION_METRIC, "value": round(value, 3), "unit": unit, "n_gpus": 1, "steps": args.steps,
+        "warmup": args.warmup, "ms_per_step": round(us / 1e3, 6), "higher_is_better": True, "scaling": "weak",
+        "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+        "config": {**config, "heads": heads, "kv_heads": kv_heads, "head_dim": HEAD_DIM, "parallelism": "single-gpu"},
+        "roofline": {"bound": bound, "achieved": round(value, 1), "peak": peak, "unit": unit,
+                     "frac": round(value / peak, 4), "avg_launch_us": round(us, 3)},
+        "kernel_sources": kernel_source_hash(args.op),
+    }), flush=True)
+
+
 def measured_ceiling(decode, layers, M, tdt, torch, dev, stream, achieved):
     """What this GPU delivers, measured live beside the spec peak.
     decode (HBM-bound): a plain device-to-device copy of 512 MiB, bytes read
@@ -592,14 +664,17 @@ def main():
                          "paro_w4a16_linear_prepared_multi, one GEMM launch per group")
     ap.add_argument("--no-ceiling", action="store_true",
                     help="skip the measured ceiling (device copy for decode, library dense GEMM for prefill)")
-    ap.add_argument("--op", choices=("linear", "quantize", "rotate", "rotate_backward", "moe", "mxfp4"),
+    ap.add_argument("--op", choices=("linear", "quantize", "rotate", "rotate_backward", "moe", "mxfp4", "attention",
+                                     "attention_decode"),
                     default="linear",
                     help="linear: the inference hot path (default); quantize: the offline W -> (qweight, "
                          "qzeros, scales) transform of the workload's first layer; rotate_backward: the "
                          "calibration-time backward of the scaling and rotation over that layer's input; "
                          "moe: the mixture-of-experts projection of workload 5 (synth.MOE_WORKLOADS); "
                          "mxfp4: the W4A4 MXFP4 linear of the workload's first layer; rotate: the input "
-                         "scaling and rotation of every layer (dense prefill form, staged form beside it)")
+                         "scaling and rotation of every layer (dense prefill form, staged form beside it); "
+                         "attention, attention_decode: the attention of the decoder layer, one prompt of 4096 "
+                         "tokens or one step of 64 sequences of 4096 over the paged cache")
     ap.add_argument("--calib-copy", type=int, default=0, metavar="BYTES",
                     help="instead of the benchmark: copy BYTES between two device buffers --steps times "
                          "(reference dispatches for scaling the FETCH_SIZE / WRITE_SIZE counters)")
@@ -644,6 +719,9 @@ def main():
         return
     if args.op == "mxfp4":
         bench_mxfp4(args, paro, synth, np, torch, dev)
+        return
+    if args.op in ("attention", "attention_decode"):
+        bench_attention(args, paro, synth, np, torch, dev)
         return
     spec = synth.WORKLOADS[args.workload]
     M, act = spec["tokens"], spec["act"]
