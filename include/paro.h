@@ -536,6 +536,8 @@ typedef struct {
  *   Start: lengths 0, refs 0, table -1 everywhere.
  * Table entries and lengths are not read on the host; kernels clamp them, so
  * an invalid state yields wrong numbers, never an out-of-bounds access.
+ * Calls on one cache follow each other (stream order, or the caller's
+ * events); calls that only read it (the attention ones) may overlap.
  * GPU limits: slots <= 4096, num_pages <= 2^22, max_pages <= 2^20 and
  * max_pages * page_size <= 2^30, layers <= 1024, kv_heads <= 256; k and v
  * 16-byte aligned, refs, table and lengths 4-byte aligned.

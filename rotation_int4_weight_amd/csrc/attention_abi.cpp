@@ -164,7 +164,8 @@ int check_cache_and_shape(const paro_kv_cache *c, int layer, const paro_attentio
 int check_apart_from_cache(const paro_kv_cache *c, const paro_attention_shape *s, const void *y, int64_t rows) {
   const size_t yb = extent(rows, s->q_heads, s->head_dim, s->y_token, s->y_head);
   if (overlap(y, yb, c->k, pool_bytes(c)) || overlap(y, yb, c->v, pool_bytes(c)) ||
-      overlap(y, yb, c->table, (size_t)c->slots * c->max_pages * 4) || overlap(y, yb, c->lengths, (size_t)c->slots * 4))
+      overlap(y, yb, c->table, (size_t)c->slots * c->max_pages * 4) ||
+      overlap(y, yb, c->lengths, (size_t)c->slots * 4) || overlap(y, yb, c->refs, (size_t)c->num_pages * 4))
     return fail(PARO_ERR_SHAPE, "y overlaps the cache");
   return PARO_OK;
 }

@@ -77,34 +77,47 @@ struct Rows {
   const int32_t *table; // cache
 };
 
-// The sequence of row tile t, by a scan of the sequences 64 at a time (every
-// lane's sequence: ceil(n_q * group / BM) tiles).  False: no such tile.
+// The sequence of row tile t, by a scan of the sequences (ceil(n_q * group /
+// BM) tiles each), 256 at a time, a lane taking four.  False: no such tile.
 template <bool CACHED, int BM>
-__device__ __forceinline__ bool find_tile(const AttentionArgs &a, int64_t t, Rows &r) {
+__device__ __forceinline__ bool find_tile(const AttentionArgs &a, int t, Rows &r) {
   const int lane = lane_id();
-  for (int s0 = 0; s0 < a.sequences; s0 += 64) {
-    const int s = s0 + lane;
-    int64_t q0 = 0, n = 0;
-    if (s < a.sequences) {
-      q0 = a.cu_q[s] < 0 ? 0 : a.cu_q[s];
-      const int64_t q1 = a.cu_q[s + 1] > a.q_tokens ? a.q_tokens : a.cu_q[s + 1];
-      n = q1 > q0 ? q1 - q0 : 0;
+  const auto bound = [&](int s) {  // cu_q[s] in range; the end again past the last sequence
+    const int64_t v = a.cu_q[min(s, a.sequences)];
+    return (int)(v < 0 ? 0 : v > a.q_tokens ? a.q_tokens : v);
+  };
+  for (int s0 = 0; s0 < a.sequences; s0 += 256) {
+    int tiles[4], q[5], ends = 0;
+#pragma unroll
+    for (int u = 0; u < 5; ++u) q[u] = bound(s0 + 4 * lane + u);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      tiles[u] = (max(q[u + 1] - q[u], 0) * a.group + BM - 1) / BM;
+      ends += tiles[u];
     }
-    const int64_t tiles = (n * a.group + BM - 1) / BM;
-    int64_t ends = tiles;
+    int before = ends;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int64_t o = __shfl_up(ends, d, 64);
+      const int o = __shfl_up(ends, d, 64);
       if (lane >= d) ends += o;
     }
+    before = ends - before;
     const uint64_t past = __ballot(ends > t);
     if (past) {
       const int j = __builtin_ctzll(past);
-      r.index = __builtin_amdgcn_readfirstlane((int)(t - __shfl(ends - tiles, j, 64)));
-      r.n_q = __builtin_amdgcn_readfirstlane((int)__shfl(n, j, 64));
-      const int64_t at = __shfl(q0, j, 64);
-      r.q0 = __builtin_amdgcn_readfirstlane((int)at);
-      const int sq = s0 + j;
+      int index = t - __builtin_amdgcn_readfirstlane(__shfl(before, j, 64)), u = 0;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int n = __builtin_amdgcn_readfirstlane(__shfl(tiles[i], j, 64));
+        if (u == i && index >= n) {
+          index -= n;
+          ++u;
+        }
+      }
+      const int sq = s0 + 4 * j + u, q0 = bound(sq);
+      r.index = __builtin_amdgcn_readfirstlane(index);
+      r.q0 = __builtin_amdgcn_readfirstlane(q0);
+      r.n_q = __builtin_amdgcn_readfirstlane(bound(sq + 1) - q0);
       if constexpr (CACHED) {
         const int slot = a.slots[sq];
         r.n_k = __builtin_amdgcn_readfirstlane(a.kv.length(slot));
@@ -119,7 +132,7 @@ __device__ __forceinline__ bool find_tile(const AttentionArgs &a, int64_t t, Row
       }
       return true;
     }
-    t -= __shfl(ends, 63, 64);
+    t -= __builtin_amdgcn_readfirstlane(__shfl(ends, 63, 64));
   }
   return false;
 }
@@ -361,7 +374,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
   // the XCDs in turn, so with 8 heads each XCD's L2 holds one head's K and V;
   // the longest tiles (a sequence's last) first
   const int kvh = (int)(blockIdx.x % a.kv_heads);
-  const int64_t t = row_tiles - 1 - (int64_t)(blockIdx.x / a.kv_heads);
+  const int t = row_tiles - 1 - (int)(blockIdx.x / a.kv_heads);
   Rows r;
   if (!find_tile<CACHED, BM>(a, t, r)) return;
   const int rows = r.n_q * a.group;  // rows of the sequence and key-value head

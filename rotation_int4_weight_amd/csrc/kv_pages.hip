@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(256) free_kernel(Pool p, const int32_t *__rest
   const int i = blockIdx.x, s = slots[i];
   if (s < 0 || s >= p.slots) return;
   bool earlier = false;  // an earlier entry names the slot: that one frees it
+#pragma unroll 4
   for (int j = threadIdx.x; j < i; j += 256) earlier |= slots[j] == s;
   if (__syncthreads_or(earlier)) return;
   const int pages = p.held(p.lengths[s]);
@@ -392,6 +393,7 @@ __global__ void __launch_bounds__(256) append_kernel(KvLayer kv, int kv_heads, i
   const int s = slots[i];
   if (s < 0 || s >= kv.slots) return;
   bool earlier = false;
+#pragma unroll 8
   for (int j = lane; j < i; j += 64) earlier |= slots[j] == s;
   if (__any(earlier)) return;
   const int most = kv.max_pages << kv.page_shift;

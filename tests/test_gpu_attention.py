@@ -143,6 +143,32 @@ def test_prompt_no_rows_and_no_sequences():
     assert bool((y == 0).all())
 
 
+@pytest.mark.parametrize("n", [255, 256, 257, 1030])
+def test_prompt_many_sequences(n):
+    """More sequences than one step of the sequence scan: short, empty and longer ones."""
+    counts = [(i * 7) % 4 for i in range(n)]
+    counts[n // 2] = counts[-1] = 140
+    for cached in (False, True):
+        heads, kv_heads, dim, dtype = 6, 2, 64, torch.float16
+        rows = sum(counts)
+        q = randn((rows, heads, dim), dtype, n, 1.5)
+        y = torch.full_like(q, NAN)
+        if cached:
+            c = filled_cache(paro, counts, 16, kv_heads, dim, dtype, n)
+            paro.paro_attention_prompt_cached(c, 0, q, torch.arange(n, dtype=torch.int32, device="cuda"),
+                                              offsets(counts), y)
+            k, v = (torch.cat([x[i] for x in (cached_rows(c, 0, s) for s in range(n) if counts[s])]) for i in (0, 1))
+        else:
+            k, v = randn((rows, kv_heads, dim), dtype, 1), randn((rows, kv_heads, dim), dtype, 2)
+            paro.paro_attention_prompt(q, k, v, offsets(counts), offsets(counts), y)
+        at = 0
+        for i, m in enumerate(counts):
+            if m and (i < 8 or m > 3 or i % 37 == 0 or i > n - 5):
+                check_rows(y[at:at + m], q[at:at + m], k[at:at + m], v[at:at + m], default_scale(dim))
+            at += m
+        assert not torch.isnan(y).any()
+
+
 def test_prompt_repeats_to_the_bit_and_on_another_stream():
     q, k, v = randn((333, 8, 128), torch.bfloat16, 0), randn((333, 2, 128), torch.bfloat16, 1), randn(
         (333, 2, 128), torch.bfloat16, 2)
