@@ -187,9 +187,12 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
   __shared__ float jm[16], jl[16];
   __shared__ int s_last;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
-  const int split = blockIdx.x;
-  const int tile = (int)(blockIdx.y % plan.head_tiles), kvh = (int)(blockIdx.y / plan.head_tiles);
-  const int64_t row = blockIdx.z;
+  // The part is the slowest index: workgroups go to the XCDs in turn, and with
+  // it the fastest those that have work (short rows have one part) would sit on
+  // few of them.
+  const int split = blockIdx.z;
+  const int tile = (int)(blockIdx.x % plan.head_tiles), kvh = (int)(blockIdx.x / plan.head_tiles);
+  const int64_t row = blockIdx.y;
   const int heads = min(16, a.group - 16 * tile);  // query heads of this workgroup
   const int head0 = kvh * a.group + 16 * tile;
   const int slot = a.slots[row];
@@ -383,7 +386,7 @@ size_t attention_decode_partial_bytes(const DecodeAttentionPlan &p, int64_t rows
 
 hipError_t launch_attention_decode(const AttentionArgs &a, const DecodeAttentionPlan &p, uint32_t *counters,
                                    float *partials, hipStream_t st) {
-  const dim3 grid((unsigned)p.splits, (unsigned)(a.kv_heads * p.head_tiles), (unsigned)a.sequences);
+  const dim3 grid((unsigned)(a.kv_heads * p.head_tiles), (unsigned)a.sequences, (unsigned)p.splits);
 #define PARO_DECODE(DT, DIM) \
   hipLaunchKernelGGL((decode_attention_kernel<DT, DIM>), grid, dim3(256), 0, st, a, p, counters, partials)
   if (a.dt == kF16) {
