@@ -507,8 +507,10 @@ size_t paro_mxfp4_linear_prepared_workspace_bytes(const paro_w4_layer *layer, in
  * (i + n_k < n_q, or n_k = 0) gives zeros; what stands in keys and values a
  * row may not see, infinities and NaN included, does not reach it.  Scores,
  * maxima, sums and outputs are held in fp32; the weights exp(s - m) are
- * rounded to the activation dtype for the matrix cores (half a step each),
- * their sum is that of the unrounded ones, and y is rounded once.
+ * rounded to the activation dtype for the matrix cores (half a step each;
+ * fp16 ones below 2^-21 of the row's largest, 2^-29 in paro_attention_decode,
+ * fall into its subnormals), their sum is that of the unrounded ones, and y is
+ * rounded once.
  * GPU limits: head_dim 64 or 128, q_heads a multiple of kv_heads and at most
  * 256, strides non-negative multiples of 8 elements below 2^40, tensors
  * 16-byte aligned.

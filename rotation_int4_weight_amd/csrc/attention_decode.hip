@@ -16,6 +16,9 @@
 //     channels) and turned into V^T fragments by v_perm in the lane.
 //   - The head stays in lane%16 from S^T to O^T, so maxima and sums are per
 //     lane; only the maximum crosses lanes (two permlane swaps per 32 keys).
+//   - fp16 weights are exp2(s - m + 15) (inside the type; the quotient is the
+//     same), so that those down to 2^-29 of the largest stay above its
+//     subnormals: a long row may have many.
 //   - 32 keys of K and V are in flight per wave while 32 are worked on.
 // Parts are joined with their maxima (through LDS between the waves, through
 // the workspace between workgroups, by the last one to arrive, in order).
@@ -155,9 +158,10 @@ __device__ __forceinline__ void step(State<DIM> &st, Tile<DIM> &t, const u32x4 (
   st.m = m;
   u32x4 p;
   float sum = 0.f;
+  const float low = ref - (DT == kF16 ? 15.f : 0.f);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const float e0 = __builtin_amdgcn_exp2f(s[2 * u] - ref), e1 = __builtin_amdgcn_exp2f(s[2 * u + 1] - ref);
+    const float e0 = __builtin_amdgcn_exp2f(s[2 * u] - low), e1 = __builtin_amdgcn_exp2f(s[2 * u + 1] - low);
     sum += e0 + e1;
     p[u] = pack2<DT>(e0, e1);
   }

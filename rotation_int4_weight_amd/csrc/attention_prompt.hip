@@ -16,7 +16,8 @@
 //   Running maximum m and sum l: a tile's weights are exp2((s - m) scale2),
 //   relative to an m that is only moved (and what was summed before scaled)
 //   when some row's maximum rose by more than 2^8 over it: any m gives the
-//   same quotient, and 256 is far from the types' limits.
+//   same quotient.  fp16 weights are 2^7 larger (up to 2^15, inside the type),
+//   so that those down to 2^-21 of the largest stay above its subnormals.
 // LDS rows are 16-byte chunks, chunk c of row r stored at c ^ f(r), so that
 // both reads touch every bank once.
 //
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[db][i] *= keep;
     }
-    const float ref = m == -INFINITY ? 0.f : m * scale2;
+    const float ref = m == -INFINITY ? 0.f : m * scale2 - (DT == kF16 ? 7.f : 0.f);
     u32x4 p[2 * KB];
     float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

@@ -57,6 +57,31 @@ def test_prompt_scales_and_large_scores():
     run_prompt([90], [90], 4, 2, 64, torch.float16, scale=3.0, qs=1.0, seed=6)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim,dtype", [(64, torch.bfloat16), (64, torch.float16), (128, torch.bfloat16),
+                                       (128, torch.float16)])
+def test_prompt_many_row_tiles(dim, dtype, causal):
+    """More than 96 row tiles and key-value heads: workgroups of 128 rows that share their keys."""
+    run_prompt([400, 129, 65, 1], [400, 129, 65, 1], 16, 8, dim, dtype, causal=causal, seed=11)
+    run_prompt([150, 200, 3], [333, 70, 3], 56, 8, dim, dtype, causal=causal, seed=12)
+
+
+@pytest.mark.parametrize("layout", ["fused", "heads_first"])
+def test_prompt_strides_many_row_tiles(layout):
+    n, heads, kv_heads, dim, dtype = 340, 64, 16, 64, torch.bfloat16
+    if layout == "fused":
+        rows = randn((n, heads + 2 * kv_heads, dim), dtype, 1)
+        q, k, v = rows[:, :heads], rows[:, heads:heads + kv_heads], rows[:, heads + kv_heads:]
+        y = torch.full((n, heads, dim + 8), NAN, dtype=dtype, device="cuda")[..., :dim]
+    else:
+        q, k, v = (randn((h, n, dim), dtype, i).transpose(0, 1) for i, h in enumerate((heads, kv_heads, kv_heads)))
+        y = torch.full((heads, n, dim), NAN, dtype=dtype, device="cuda").transpose(0, 1)
+    cu = offsets([140, 200])
+    paro.paro_attention_prompt(q, k, v, cu, cu, y)
+    for a, b in ((0, 140), (140, 340)):
+        check_rows(y[a:b], q[a:b], k[a:b], v[a:b], default_scale(dim))
+
+
 @pytest.mark.parametrize("layout", ["fused", "heads_first", "broadcast"])
 def test_prompt_strides(layout):
     n, heads, kv_heads, dim, dtype = 75, 6, 2, 64, torch.float16
@@ -92,6 +117,28 @@ def test_prompt_masked_places_do_not_reach_a_row(bad, dim):
     paro.paro_attention_prompt(q, k, v, offsets(counts), offsets(counts), y)
     for lo, hi in ((0, cut[0]), (100, cut[1])):
         check_rows(y[lo:hi], q[lo:hi], k[lo:hi], v[lo:hi], default_scale(dim))
+
+
+@pytest.mark.parametrize("bad", [NAN, float("inf"), "lowest"])
+def test_prompt_masked_places_many_row_tiles(bad):
+    """The same with more than 96 row tiles and key-value heads, packed and over the cache."""
+    dtype, n, heads, kv_heads, dim = torch.float16, 420, 32, 8, 64
+    bad = torch.finfo(dtype).min if bad == "lowest" else bad
+    q, k, v = (randn((n, h, dim), dtype, i) for i, h in enumerate((heads, kv_heads, kv_heads)))
+    cut = 201  # first bad row
+    k[cut:], v[cut:] = bad, bad
+    y = torch.full_like(q, 7.0)
+    paro.paro_attention_prompt(q, k, v, offsets([n]), offsets([n]), y)
+    z = torch.full_like(q, 7.0)
+    c = paro.KVCache.empty(1, 20, kv_heads, 32, dim, 1, 16, dtype)
+    c.table[0, :14] = torch.arange(14, 0, -1, dtype=torch.int32)
+    c.refs[1:15] = 1
+    c.lengths[0] = n
+    slots = torch.zeros(1, dtype=torch.int32, device="cuda")
+    paro.paro_kv_append(c, 0, k, v, slots, offsets([n]))
+    paro.paro_attention_prompt_cached(c, 0, q, slots, offsets([n]), z)
+    for got in (y, z):
+        check_rows(got[:cut], q[:cut], k[:cut], v[:cut], default_scale(dim))
 
 
 def test_prompt_bad_values_reach_the_rows_that_see_them():
@@ -185,6 +232,34 @@ def test_prompt_repeats_to_the_bit_and_on_another_stream():
         assert torch.equal(y, first)
 
 
+def faint_case(dtype, n, dim, gap):
+    """One key far above all others (gap: in powers of two), with a value of 0 where the others have 1: y is the sum of
+    the n - 1 small weights.  Scores are exact: q = (1, 0, ...), k = (score, 0, ...), scale = log(2)."""
+    q, k, v = (torch.zeros((r, 1, dim), dtype=dtype, device="cuda") for r in (1, n, n))
+    q[:, :, 0], k[n // 3, :, 0] = 1.0, float(gap)
+    v.fill_(1.0)
+    v[n // 3] = 0.0
+    small = (n - 1) * 2.0 ** -gap
+    return q, k, v, small / (1.0 + small)
+
+
+def check_faint(y, want, dtype):
+    # scores to gap * 2^-22 (log 2 in fp32 and two products); weights and y by half a
+    # step of fp16 each, the sums by fp32 steps; an fp16 y below 2^-14 by half a subnormal step
+    err = (y.double() - want).abs().max()
+    assert float(err) <= want * (2 * 2.0 ** -11 + 64 * 2.0 ** -22) + 2.0 ** -25
+
+
+@pytest.mark.parametrize("n,heads", [(3000, 1), (3000, 64)])
+def test_prompt_small_weights_in_fp16(n, heads):
+    q, k, v, want = faint_case(torch.float16, n, 64, 20.5)
+    q = q.expand(130, heads, 64).contiguous()
+    k, v = k.expand(n, heads, 64).contiguous(), v.expand(n, heads, 64).contiguous()
+    y = torch.empty_like(q)
+    paro.paro_attention_prompt(q, k, v, offsets([130]), offsets([n]), y, scale=0.6931471805599453, causal=False)
+    check_faint(y, want, torch.float16)
+
+
 # ---- over the cache ----
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -271,6 +346,22 @@ def test_decode_workspace_serves_several_shapes():
             for r in range(n):
                 k, v = cached_rows(c, 0, r)
                 check_rows(y[r:r + 1], q[r:r + 1], k, v, default_scale(dim))
+
+
+@pytest.mark.parametrize("n", [500, 50000])
+def test_decode_small_weights_in_fp16(n):
+    q, k, v, want = faint_case(torch.float16, n, 128, 27.5)
+    pages = -(-n // 16)
+    c = paro.KVCache.empty(1, pages, 1, 16, 128, 1, pages, torch.float16)
+    c.table[0] = torch.arange(pages, dtype=torch.int32)
+    c.refs.fill_(1)
+    c.lengths[0] = n
+    slots = torch.zeros(1, dtype=torch.int32, device="cuda")
+    paro.paro_kv_append(c, 0, k, v, slots, offsets([n]))
+    y = torch.empty_like(q)
+    paro.paro_attention_decode(c, 0, q, slots, y, paro.make_workspace(
+        paro.paro_attention_decode_workspace_bytes(c, 1, 1)), scale=0.6931471805599453)
+    check_faint(y, want, torch.float16)
 
 
 def test_decode_empty_foreign_and_clamped():
