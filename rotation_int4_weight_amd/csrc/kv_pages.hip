@@ -7,9 +7,9 @@
 // host round trip and can be captured into a graph.  Decisions that depend on
 // all entries (which page is free, who is first) are made by one workgroup of
 // 1024 threads; the data then moves in a second, wide launch that reads the
-// list of page copies the first one left in the workspace.  Free pages are
-// taken in ascending order and ties go to the earliest entry, so the same
-// state and call give the same result.
+// list of page copies the first one left in the workspace (short forks need no
+// second one).  Free pages are taken in ascending order and ties go to the
+// earliest entry, so the same state and call give the same result.
 #include <algorithm>
 
 #include "attention.hpp"
@@ -266,6 +266,26 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(char *__restrict__ k, c
 
 // ---- fork ----
 
+// Rows are shared in the planning launch where its 16 waves need at most this
+// many steps of 64 table entries, were every row full (fork and free in one
+// launch less / with it, us: 8 rows of 64 5.8 / 6.9, 16 of 256 (4 steps) 7.3 /
+// 7.1, 16 of 512 10.0 / 7.7, 64 of 128 11.4 / 8.8; a launch is 3 us of host time).
+constexpr int kForkSteps = 4;
+
+// pages of a parent's row to the child's, by `threads` threads from `thread` on
+__device__ __forceinline__ void share_pages(const Pool &p, int parent, int child, int pages, int thread, int threads) {
+  const int32_t *from = p.table + (int64_t)parent * p.max_pages;
+  int32_t *to = p.table + (int64_t)child * p.max_pages;
+  for (int j = thread; j < pages; j += threads) {
+    const int page = from[j];
+    to[j] = page;
+    if (page >= 0 && page < p.num_pages) atomicAdd(&p.refs[page], 1);
+  }
+}
+
+// APPLY: the rows are shared here too, a wave taking an entry; otherwise
+// w.src[i] leaves the number of pages to share to fork_apply_kernel.
+template <bool APPLY>
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(Pool p, const int32_t *__restrict__ parents,
                                                                 const int32_t *__restrict__ children, int n,
                                                                 int32_t *__restrict__ granted, Work w) {
@@ -290,8 +310,15 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(Pool p, const i
     const int i = u * kPlanThreads + threadIdx.x;
     if (i >= n) continue;
     granted[i] = yes[u];
-    w.src[i] = yes[u] ? p.held(len[u]) : 0;  // pages to share
+    const int pages = yes[u] ? p.held(len[u]) : 0;
+    if constexpr (APPLY) first[i] = pages;
+    else w.src[i] = pages;
     if (yes[u]) p.lengths[children[i]] = len[u];
+  }
+  if constexpr (APPLY) {
+    __syncthreads();
+    for (int i = wave_id(); i < n; i += kPlanWaves)
+      if (first[i] > 0) share_pages(p, parents[i], children[i], first[i], lane_id(), 64);
   }
 }
 
@@ -301,13 +328,7 @@ __global__ void __launch_bounds__(256) fork_apply_kernel(Pool p, const int32_t *
                                                          const int32_t *__restrict__ children, Work w) {
   const int i = blockIdx.y, pages = w.src[i];
   if (pages == 0) return;
-  const int32_t *from = p.table + (int64_t)parents[i] * p.max_pages;
-  int32_t *to = p.table + (int64_t)children[i] * p.max_pages;
-  for (int j = blockIdx.x * 256 + threadIdx.x; j < pages; j += gridDim.x * 256) {
-    const int page = from[j];
-    to[j] = page;
-    if (page >= 0 && page < p.num_pages) atomicAdd(&p.refs[page], 1);
-  }
+  share_pages(p, parents[i], children[i], pages, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }
 
 // ---- free ----
@@ -460,7 +481,12 @@ hipError_t launch_kv_fork(const paro_kv_cache &c, const int32_t *parents, const 
                           int32_t *granted, int32_t *work, hipStream_t st) {
   const Work w = work_of(work, c.num_pages);
   const Pool p = pool_of(c);
-  hipLaunchKernelGGL(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, p, parents, children, n, granted, w);
+  const int steps = ((n + kPlanWaves - 1) / kPlanWaves) * ((c.max_pages + 63) / 64);
+  if (steps <= kForkSteps) {
+    hipLaunchKernelGGL(fork_plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, st, p, parents, children, n, granted, w);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(fork_plan_kernel<false>, dim3(1), dim3(kPlanThreads), 0, st, p, parents, children, n, granted, w);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const unsigned blocks = (unsigned)std::min((c.max_pages + 255) / 256, 16);
