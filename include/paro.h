@@ -590,8 +590,9 @@ int paro_attention_prompt_cached(const paro_kv_cache *cache, int layer, const pa
  * outside the cache gives zeros.
  *   workspace: paro_attention_decode_workspace_bytes bytes, 16-byte aligned,
  *   zero-filled before its first use with this library; each completed call
- *   leaves its counters zero.  Calls that overlap in time need separate
- *   ones.  The split of the length depends on rows, q_heads and the cache's
+ *   leaves its counter area zero, which is that of the linears' workspaces,
+ *   so one workspace of the largest size may serve those and this one after
+ *   another.  Calls that overlap in time need separate ones.  The split of the length depends on rows, q_heads and the cache's
  *   sizes and on each length alone, and parts are joined in order: a
  *   repeated call gives identical bits.
  * rows <= 32768.
@@ -624,7 +625,9 @@ int paro_kv_append(const paro_kv_cache *cache, int layer, const void *k, int64_t
  * earlier entry names the same slot, or the pages that it and the entries
  * before it need are more than are free.
  * workspace: paro_kv_workspace_bytes(cache) bytes, 16-byte aligned; needs no
- * clearing; the same holds for paro_kv_fork and paro_kv_compact.
+ * clearing, and the counter area of the linears and of paro_attention_decode
+ * at its start is left alone, so it may be theirs too; the same holds for
+ * paro_kv_fork and paro_kv_compact.
  */
 int paro_kv_reserve(const paro_kv_cache *cache, const int32_t *slots, const int32_t *grow, int64_t n,
                     int32_t *granted, void *workspace, size_t workspace_bytes, void *stream);

@@ -25,6 +25,15 @@ inline bool overlap(const void *a, size_t an, const void *b, size_t bn) {
 
 inline bool act_dtype(int dt) { return dt == PARO_F16 || dt == PARO_BF16; }
 
+constexpr int64_t kMaxOut = int64_t(1) << 21;
+// Every workspace of the linears, the decode attention and the cache's pages
+// starts with a fixed counter area: for the split-K reduction one 32-bit
+// counter on its own 128-byte line per 128-column tile, at most kMaxOut/128
+// tiles; for the attention's join its first kDecodeCounters words.  A
+// zero-filled workspace stays valid across shapes, paths and these calls: none
+// ever writes anything but zeros-at-exit into it.
+constexpr size_t kCounterBytes = (size_t)(kMaxOut / 128) * 128;
+
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace paro

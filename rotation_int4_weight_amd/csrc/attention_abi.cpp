@@ -17,6 +17,7 @@ using paro::align_up;
 using paro::aligned;
 using paro::fail;
 using paro::hip_fail;
+using paro::kCounterBytes;
 using paro::ok;
 using paro::overlap;
 
@@ -28,7 +29,7 @@ constexpr int64_t kMaxPool = int64_t(1) << 22;
 constexpr int64_t kMaxTable = int64_t(1) << 20;
 constexpr int64_t kMaxLength = int64_t(1) << 30;
 constexpr int kMaxLayers = 1024;
-constexpr size_t kDecodeCounterBytes = (size_t)paro::kDecodeCounters * 4;
+static_assert((size_t)paro::kDecodeCounters * 4 <= paro::kCounterBytes, "the join's counters fit the counter area");
 
 int page_shift(int page_size) {
   for (int s = 4; s <= 8; ++s)
@@ -40,6 +41,8 @@ int check_head_dim(int d) {
   if (d != 64 && d != 128) return fail(PARO_ERR_UNSUPPORTED, "head_dim=%d: the GPU path supports 64 and 128", d);
   return PARO_OK;
 }
+
+int32_t *kv_work(void *workspace) { return (int32_t *)((char *)workspace + kCounterBytes); }
 
 int64_t page_elements(const paro_kv_cache *c) { return (int64_t)c->kv_heads * c->page_size * c->head_dim; }
 size_t pool_bytes(const paro_kv_cache *c) { return (size_t)c->layers * c->num_pages * page_elements(c) * 2; }
@@ -306,7 +309,7 @@ size_t paro_attention_decode_workspace_bytes(const paro_kv_cache *c, int64_t row
     return 0;
   const paro::DecodeAttentionPlan p =
       paro::plan_attention_decode(rows, q_heads, c->kv_heads, (int64_t)c->max_pages * c->page_size);
-  return kDecodeCounterBytes + paro::attention_decode_partial_bytes(p, rows, c->kv_heads, c->head_dim);
+  return kCounterBytes + paro::attention_decode_partial_bytes(p, rows, c->kv_heads, c->head_dim);
 }
 
 int paro_attention_decode(const paro_kv_cache *c, int layer, const paro_attention_shape *s, const void *q,
@@ -340,7 +343,7 @@ int paro_attention_decode(const paro_kv_cache *c, int layer, const paro_attentio
   const paro::DecodeAttentionPlan p =
       paro::plan_attention_decode(rows, s->q_heads, c->kv_heads, (int64_t)c->max_pages * c->page_size);
   hipError_t e = paro::launch_attention_decode(a, p, (uint32_t *)workspace,
-                                               (float *)((char *)workspace + kDecodeCounterBytes),
+                                               (float *)((char *)workspace + kCounterBytes),
                                                (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "decode attention launch");
   return ok();
@@ -378,7 +381,7 @@ int paro_kv_append(const paro_kv_cache *c, int layer, const void *k, int64_t k_t
 
 size_t paro_kv_workspace_bytes(const paro_kv_cache *c) {
   if (check_cache(c, false)) return 0;
-  return paro::kv_work_ints(*c) * 4;
+  return kCounterBytes + paro::kv_work_ints(*c) * 4;
 }
 
 int paro_kv_reserve(const paro_kv_cache *c, const int32_t *slots, const int32_t *grow, int64_t n, int32_t *granted,
@@ -393,7 +396,7 @@ int paro_kv_reserve(const paro_kv_cache *c, const int32_t *slots, const int32_t 
     return rc;
   if (overlap(granted, (size_t)n * 4, slots, (size_t)n * 4) || overlap(granted, (size_t)n * 4, grow, (size_t)n * 4))
     return fail(PARO_ERR_SHAPE, "granted overlaps slots or grow");
-  hipError_t e = paro::launch_kv_reserve(*c, slots, grow, (int)n, granted, (int32_t *)workspace, (hipStream_t)stream);
+  hipError_t e = paro::launch_kv_reserve(*c, slots, grow, (int)n, granted, kv_work(workspace), (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "kv reserve launch");
   return ok();
 }
@@ -413,7 +416,7 @@ int paro_kv_fork(const paro_kv_cache *c, const int32_t *parents, const int32_t *
       overlap(granted, (size_t)n * 4, children, (size_t)n * 4))
     return fail(PARO_ERR_SHAPE, "granted overlaps parents or children");
   hipError_t e =
-      paro::launch_kv_fork(*c, parents, children, (int)n, granted, (int32_t *)workspace, (hipStream_t)stream);
+      paro::launch_kv_fork(*c, parents, children, (int)n, granted, kv_work(workspace), (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "kv fork launch");
   return ok();
 }
@@ -434,7 +437,7 @@ int paro_kv_compact(const paro_kv_cache *c, int32_t *used, void *workspace, size
   if (rc) return rc;
   if ((rc = check_kv_workspace(c, workspace, workspace_bytes)) || (rc = check_list(c, used, 1, workspace, "used")))
     return rc;
-  hipError_t e = paro::launch_kv_compact(*c, used, (int32_t *)workspace, (hipStream_t)stream);
+  hipError_t e = paro::launch_kv_compact(*c, used, kv_work(workspace), (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "kv compact launch");
   return ok();
 }

@@ -49,6 +49,8 @@ using paro::align_up;
 using paro::aligned;
 using paro::fail;
 using paro::hip_fail;
+using paro::kCounterBytes;
+using paro::kMaxOut;
 using paro::ok;
 using paro::overlap;
 
@@ -57,13 +59,6 @@ constexpr int kMaxKrot = 64;
 // The prefill GEMM addresses a 256-row activation tile with 32-bit buffer
 // offsets (256 * I * 2 bytes < 2^32).
 constexpr int64_t kMaxDim = int64_t(1) << 22;
-constexpr int64_t kMaxOut = int64_t(1) << 21;
-// Every workspace starts with a fixed counter area for the split-K
-// reduction (one 32-bit counter on its own 128-byte line per 128-column tile,
-// at most kMaxOut/128 tiles), so a zero-filled workspace stays valid across
-// shapes and paths: no path ever writes anything but zeros-at-exit into it.
-constexpr size_t kCounterBytes = (size_t)(kMaxOut / 128) * 128;
-
 int64_t group_of(const paro_w4_layer *L) { return L->group_size == -1 ? L->in_features : L->group_size; }
 
 // Shape rules of the method ("ParoQuant" wiki: even groups dividing I; AWQ

@@ -173,6 +173,8 @@ def test_workspace_sizes():
     need = lib.paro_attention_decode_workspace_bytes
     assert need(ctypes.byref(c), 0, 8) == 0 and need(ctypes.byref(c), 4, 7) == 0 and need(None, 4, 8) == 0
     assert need(ctypes.byref(c), 4, 8) > 0
+    # behind the counter area that the linears' workspaces start with: 2^14 lines of 128 bytes
+    assert need(ctypes.byref(c), 4, 8) >= 2 ** 21 and lib.paro_kv_workspace_bytes(ctypes.byref(c)) > 2 ** 21
     assert lib.paro_kv_workspace_bytes(ctypes.byref(c)) >= 4 * 64 and lib.paro_kv_workspace_bytes(None) == 0
 
 

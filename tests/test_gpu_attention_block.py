@@ -238,3 +238,40 @@ def test_stream_argument_forms():
         torch.cuda.synchronize()
         ys.append(y)
     assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
+
+
+def test_one_workspace_for_linears_attention_and_pages():
+    """The linears, the attention's join and the page calls share their workspace's counter area, one after another."""
+    dt, rows, dim = synth.F16, 2, 128
+    host = synth.make_layer(970, 0, 1024, 16384)
+    lin = paro.DeviceLayer(host)
+    cache = paro.KVCache.empty(1, 600, 2, 16, dim, 4, 300, torch_dtype(dt))
+    lengths = [2500, 1800]
+    e = lambda *s: torch.full(s, float("nan"), dtype=cache.dtype, device="cuda")  # noqa: E731
+    x = torch.from_numpy(np.ascontiguousarray(synth.make_x(971, 0, rows, 1024, dt)).view(np.int16)).cuda()
+    x = x.view(cache.dtype)
+    need = max(paro.paro_w4a16_linear_workspace_bytes(lin, rows), paro.paro_kv_workspace_bytes(cache),
+               max(paro.paro_attention_decode_workspace_bytes(cache, r, 8) for r in (1, 2)))
+    shared, alone = paro.make_workspace(need), paro.make_workspace(need)
+    want, got = e(rows, 16384), e(rows, 16384)
+    paro.paro_w4a16_linear(lin, x, want, alone)
+    granted = ints([-1, -1])
+    paro.paro_kv_reserve(cache, ints([1, 3]), ints(lengths), granted, shared)
+    assert granted.tolist() == [1, 1]
+    k = torch.randn((sum(lengths), 2, dim), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    k = k.to(cache.dtype)
+    paro.paro_kv_append(cache, 0, k, -k, ints([1, 3]), offsets(lengths))
+    q = k[5:7].repeat(1, 4, 1).contiguous()
+    for i in range(3):
+        a = e(rows, 8, dim)
+        paro.paro_attention_decode(cache, 0, q, ints([1, 3]), a, shared)
+        paro.paro_attention_decode(cache, 0, q[:1], ints([3]), e(1, 8, dim), shared)
+        paro.paro_w4a16_linear(lin, x, got, shared)
+        assert torch.equal(got, want)
+        paro.paro_kv_fork(cache, ints([1]), ints([0]), granted[:1], shared)
+        paro.paro_kv_free(cache, ints([0]))
+        paro.paro_kv_compact(cache, granted[:1], shared)
+        paro.paro_w4a16_linear(lin, x, got.fill_(float("nan")), shared)
+        assert torch.equal(got, want)
+        for r, (lo, n) in enumerate(((0, 2500), (2500, 1800))):
+            check_rows(a[r:r + 1], q[r:r + 1], k[lo:lo + n], -k[lo:lo + n], default_scale(dim))
