@@ -3,7 +3,8 @@
  *
  *   Y = (X . D^-1 . R) . Q(W_r)^T + b
  *
- * computed by hand-written HIP kernels.  Notation and stored tensors follow
+ * computed by hand-written HIP kernels, and the attention and key-value cache
+ * between such linears.  Notation and stored tensors follow
  * the "ParoQuant" page of the GPTQModel wiki (GPT-QModel 7.7.0):
  *   - Concepts / Pairwise Givens rotations: within each group of G input
  *     channels a stage splits the channels into disjoint pairs; a pair (a, b)

@@ -3,8 +3,10 @@
     Y = (X . D^-1 . R) . Q(W_r)^T + b
 
 computed by hand-written HIP kernels for gfx950 behind the C-ABI of
-include/paro.h (libparo.so).  This package is the thin ctypes binding with the
-same entry-point names; PyTorch supplies device memory and streams only.
+include/paro.h (libparo.so), with the attention and the paged key-value cache
+that stand between such linears in a decoder layer.  This package is the thin
+ctypes binding with the same entry-point names; PyTorch supplies device memory
+and streams only.
 """
 from ._lib import (BF16, EXPORTS, F16, F32, PATH_AUTO, PATH_DECODE_FUSED, PATH_DECODE_SPLIT,
                    PATH_PREFILL, DeviceLayer, ParoError, load, make_workspace,
