@@ -22,8 +22,12 @@
 // both reads touch every bank once.
 //
 // A masked key has weight 0, but 0 times a V that is not finite is NaN: a wave
-// whose sums are not all finite at the end computes its rows again, one by
-// one, with masked keys left out (slow, and right).
+// whose sums are not all finite at the end looks for such values among the
+// keys that some of its rows may not see (at most the last tiles'), and if
+// there are any computes its rows again, one by one, with masked keys left out
+// (a prompt of 8192 with one in its last key: 38 ms instead of 0.56; one that
+// all rows see costs 0.1 ms).  Searching every tile with masked keys beforehand
+// cost each prompt 1 to 2 us.
 //
 // What bounds it: 16.9 million MFMAs of 32 cycles each for a causal prompt of
 // 8192 (32 heads over 8, 128 channels) are 220 us at 2.4 GHz, but with random
@@ -155,12 +159,31 @@ __device__ __forceinline__ bool find_tile(const AttentionArgs &a, int t, Rows &r
   return false;
 }
 
-template <bool CACHED>
 __device__ __forceinline__ int64_t page_base(const AttentionArgs &a, const Rows &r, int kvh, int dim, int64_t pos) {
   int page = r.table[pos >> a.kv.page_shift];
   page = page < 0 ? 0 : page >= a.kv.num_pages ? a.kv.num_pages - 1 : page;
   return (int64_t)page * a.kv.page_stride +
          (((int64_t)kvh << a.kv.page_shift) + (pos & ((1 << a.kv.page_shift) - 1))) * dim;
+}
+
+template <int DIM, bool CACHED>
+__device__ __forceinline__ const uint16_t *v_row(const AttentionArgs &a, const Rows &r, int kvh, int j) {
+  return CACHED ? a.kv.v + page_base(a, r, kvh, DIM, j) : a.v + (r.k0 + j) * a.v_token + kvh * a.v_head;
+}
+
+// Whether V holds a value that is not finite among the keys that a wave's rows
+// had in their tiles (up to the end of the tile with key most - 1) and that not
+// all of them see (from key least on).
+template <int DT, int DIM, bool CACHED>
+__device__ __forceinline__ bool masked_not_finite(const AttentionArgs &a, const Rows &r, int kvh, int least, int most) {
+  constexpr uint32_t kInf = DT == kF16 ? 0x7c00u : 0x7f80u;
+  const int end = min(r.n_k, (most + kKeys - 1) / kKeys * kKeys);
+  bool bad = false;
+  for (int j = least; j < end; ++j) {
+    const uint16_t *v = v_row<DIM, CACHED>(a, r, kvh, j);
+    for (int c = lane_id(); c < DIM; c += 64) bad |= (v[c] & kInf) == kInf;
+  }
+  return __any(bad);
 }
 
 // One row by one wave with masked keys left out: the way around values that
@@ -173,18 +196,20 @@ __device__ __forceinline__ void row_by_wave(const AttentionArgs &a, const Rows &
   const int64_t row = r.q0 + token;
   const int seen = a.causal ? min(r.n_k, token + 1 + r.n_k - r.n_q) : r.n_k;
   const uint16_t *q = a.q + row * a.q_token + head * a.q_head;
-  const auto at = [&](const uint16_t *packed, const uint16_t *paged, int64_t ts, int64_t hs, int j) {
-    if constexpr (CACHED) return paged + page_base<CACHED>(a, r, kvh, DIM, j);
-    else return packed + (r.k0 + j) * ts + kvh * hs;
-  };
   float m = -INFINITY, l = 0.f, acc[DIM / 64] = {};
   for (int j0 = 0; j0 < seen; j0 += 64) {
     const int j = j0 + lane;
     float s = -INFINITY;
     if (j < seen) {
-      const uint16_t *k = at(a.k, a.kv.k, a.k_token, a.k_head, j);
+      const uint16_t *k = CACHED ? a.kv.k + page_base(a, r, kvh, DIM, j) : a.k + (r.k0 + j) * a.k_token + kvh * a.k_head;
       s = 0.f;
-      for (int d = 0; d < DIM; ++d) s = fmaf(act_to_f32<DT>(q[d]), act_to_f32<DT>(k[d]), s);
+      for (int d = 0; d < DIM; d += 8) {
+        const u32x4 x = *reinterpret_cast<const u32x4 *>(q + d), z = *reinterpret_cast<const u32x4 *>(k + d);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          s = fmaf(act_to_f32<DT>((uint16_t)(x[c >> 1] >> (16 * (c & 1)))),
+                   act_to_f32<DT>((uint16_t)(z[c >> 1] >> (16 * (c & 1)))), s);
+      }
       s *= a.scale;
     }
     float top = s;
@@ -197,7 +222,7 @@ __device__ __forceinline__ void row_by_wave(const AttentionArgs &a, const Rows &
     const int n = min(64, seen - j0);
     for (int jj = 0; jj < n; ++jj) {
       const float w = __shfl(p, jj, 64);
-      const uint16_t *v = at(a.v, a.kv.v, a.v_token, a.v_head, j0 + jj);
+      const uint16_t *v = v_row<DIM, CACHED>(a, r, kvh, j0 + jj);
       for (int c = 0; c < DIM / 64; ++c) acc[c] = fmaf(w, act_to_f32<DT>(v[c * 64 + lane]), acc[c]);
     }
   }
@@ -316,7 +341,7 @@ struct Loader {
 // maximum times scale2) and writes the rows: thread (row, 8 channels).
 template <int DT, int DIM, bool CACHED, int NW>
 __device__ __forceinline__ void join_waves(const AttentionArgs &a, const Rows &r, int kvh, int base, int rows,
-                                           const f32x16 (&o)[DIM / 32], float m2, float l, float *lds) {
+                                           int least, int most, const f32x16 (&o)[DIM / 32], float m2, float l, float *lds) {
   constexpr int RS = DIM + 4;  // LDS row: its channels, then m2 and l
   const int lane = lane_id(), wave = wave_id(), h = lane >> 5, col = lane & 31;
   __syncthreads();  // every wave is done with its tiles
@@ -364,7 +389,8 @@ __device__ __forceinline__ void join_waves(const AttentionArgs &a, const Rows &r
                      pack2_rne<DT>(x1[2], x1[3])};
     *reinterpret_cast<u32x4 *>(a.y + (r.q0 + token) * a.y_token + head * a.y_head + c) = any ? y : u32x4{0, 0, 0, 0};
   }
-  if (__syncthreads_or(bad)) {
+  // tiles are 32 keys here, the search's 64: it may find a value that no tile held
+  if (__syncthreads_or(bad) && masked_not_finite<DT, DIM, CACHED>(a, r, kvh, least, most)) {
 #pragma unroll 1
     for (int i = wave; i < 32 && base + i < rows; i += NW)
       row_by_wave<DT, DIM, CACHED>(a, r, kvh, (base + i) / a.group, kvh * a.group + (base + i) % a.group);
@@ -560,7 +586,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
     l = __uint_as_float(w[0]) + __uint_as_float(w[1]);
   }
   if constexpr (SPLIT) {
-    join_waves<DT, DIM, CACHED, NW>(a, r, kvh, base, rows, o, m * scale2, l, reinterpret_cast<float *>(all_lds));
+    join_waves<DT, DIM, CACHED, NW>(a, r, kvh, base, rows, wave_least, wave_most, o, m * scale2, l, reinterpret_cast<float *>(all_lds));
     return;
   }
   const bool stored = base + col < rows;
@@ -586,7 +612,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
       const auto hi = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
       if (stored) *reinterpret_cast<u32x4 *>(y + 32 * db + 16 * n) = u32x4{lo[0], hi[0], lo[1], hi[1]};
     }
-  if (__any(stored && worst != 0.f)) {
+  if (__any(stored && worst != 0.f) && masked_not_finite<DT, DIM, CACHED>(a, r, kvh, wave_least, wave_most)) {
 #pragma unroll 1
     for (int i = 0; i < 32 && base + i < rows; ++i)
       row_by_wave<DT, DIM, CACHED>(a, r, kvh, (base + i) / a.group, kvh * a.group + (base + i) % a.group);

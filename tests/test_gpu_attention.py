@@ -155,6 +155,27 @@ def test_prompt_bad_values_reach_the_rows_that_see_them():
     assert not inf.any() and not nan.any()
 
 
+@pytest.mark.parametrize("n,heads,kv_heads", [(300, 4, 1), (300, 64, 16)])
+def test_prompt_bad_value_beside_and_before_masked_ones(n, heads, kv_heads):
+    """Every tile and wave that a bad value can share with rows that may not see it: one at a time, moved along a tile."""
+    dtype, dim = torch.bfloat16, 64
+    q, k, clean = (randn((n, h, dim), dtype, i) for i, h in enumerate((heads, kv_heads, kv_heads)))
+    cu, good = offsets([n]), torch.empty_like(q)
+    paro.paro_attention_prompt(q, k, clean, cu, cu, good)
+    for at in (0, 63, 64, 100, 127, 128, 131, 190, 298, 299):
+        v = clean.clone()
+        v[at, :, 7] = NAN
+        y = torch.full_like(q, 5.0)
+        paro.paro_attention_prompt(q, k, v, cu, cu, y)
+        assert bool(torch.isnan(y[at:, :, 7]).all())
+        y[at:, :, 7] = good[at:, :, 7]
+        # rows computed again sum in another order: both within the bound, so at most two of them apart
+        assert not torch.isnan(y).any()
+        check_rows(y[max(0, at - 40):at + 2], q[max(0, at - 40):at + 2], k[:at + 2], clean[:at + 2], default_scale(dim))
+        same = torch.cat([y[:max(0, at - 130)], y[at + 130:]])
+        assert torch.equal(same, torch.cat([good[:max(0, at - 130)], good[at + 130:]]))
+
+
 def test_prompt_rows_outside_the_sequences_stay():
     q, k, v = randn((60, 4, 64), torch.float16, 0), randn((60, 2, 64), torch.float16, 1), randn((60, 2, 64),
                                                                                                torch.float16, 2)
