@@ -579,11 +579,18 @@ int paro_attention_prompt(const paro_attention_shape *shape, const void *q, cons
  * cached prefix before it; call paro_kv_reserve and paro_kv_append for the
  * chunk first).  slots: DEVICE int32 [sequences]; a slot outside the cache
  * counts as empty.  shape's heads and head_dim must be the cache's; k and v
- * strides are not used.  q and y must not overlap the cache.
+ * strides are not used.  y must not overlap q or the cache.
+ *   workspace: NULL, or as for paro_attention_decode, of
+ *   paro_attention_prompt_cached_workspace_bytes bytes (0: it is not used):
+ *   with it the keys of few rows (a short chunk, a draft to verify) are split
+ *   over workgroups.  Results with and without it agree to rounding; either
+ *   repeats to the bit.
  */
 int paro_attention_prompt_cached(const paro_kv_cache *cache, int layer, const paro_attention_shape *shape,
                                  const void *q, const int32_t *slots, const int64_t *cu_q, int64_t sequences,
-                                 int64_t q_tokens, void *y, void *stream);
+                                 int64_t q_tokens, void *y, void *workspace, size_t workspace_bytes, void *stream);
+size_t paro_attention_prompt_cached_workspace_bytes(const paro_kv_cache *cache, int64_t sequences, int64_t q_tokens,
+                                                    int q_heads);
 /*
  * One new token per sequence: row r of q [rows][q_heads][head_dim] attends
  * to all lengths[slots[r]] positions of its slot (its own among them, see

@@ -23,7 +23,8 @@ from ._lib import (BF16, EXPORTS, F16, F32, PATH_AUTO, PATH_DECODE_FUSED, PATH_D
                    paro_mxfp4_quantize_activations, paro_mxfp4_gemm, paro_mxfp4_linear,
                    paro_mxfp4_linear_workspace_bytes, paro_mxfp4_activation_workspace_bytes,
                    paro_mxfp4_linear_prepared, paro_mxfp4_linear_prepared_workspace_bytes,
-                   KVCache, paro_attention_prompt, paro_attention_prompt_cached, paro_attention_decode,
+                   KVCache, paro_attention_prompt, paro_attention_prompt_cached,
+                   paro_attention_prompt_cached_workspace_bytes, paro_attention_decode,
                    paro_attention_decode_workspace_bytes, paro_kv_append, paro_kv_reserve, paro_kv_fork,
                    paro_kv_free, paro_kv_compact, paro_kv_workspace_bytes)
 
@@ -42,6 +43,7 @@ __all__ = ["BF16", "EXPORTS", "F16", "F32", "PATH_AUTO", "PATH_DECODE_FUSED", "P
            "paro_mxfp4_quantize_activations", "paro_mxfp4_gemm", "paro_mxfp4_linear",
            "paro_mxfp4_linear_workspace_bytes", "paro_mxfp4_activation_workspace_bytes",
            "paro_mxfp4_linear_prepared", "paro_mxfp4_linear_prepared_workspace_bytes",
-           "KVCache", "paro_attention_prompt", "paro_attention_prompt_cached", "paro_attention_decode",
+           "KVCache", "paro_attention_prompt", "paro_attention_prompt_cached",
+           "paro_attention_prompt_cached_workspace_bytes", "paro_attention_decode",
            "paro_attention_decode_workspace_bytes", "paro_kv_append", "paro_kv_reserve", "paro_kv_fork",
            "paro_kv_free", "paro_kv_compact", "paro_kv_workspace_bytes"]

@@ -37,7 +37,7 @@ EXPORTS = ("paro_scale_rotate", "paro_w4_unpack_dequant", "paro_w4a16_linear",
            "paro_w4a16_linear_workspace_bytes",
            "paro_w4a16_linear_choose_path", "paro_validate_layer", "paro_last_error",
            "paro_abi_version", "paro_attention_prompt", "paro_attention_prompt_cached",
-           "paro_attention_decode", "paro_attention_decode_workspace_bytes", "paro_kv_append",
+           "paro_attention_prompt_cached_workspace_bytes", "paro_attention_decode", "paro_attention_decode_workspace_bytes", "paro_kv_append",
            "paro_kv_reserve", "paro_kv_fork", "paro_kv_free", "paro_kv_compact",
            "paro_kv_workspace_bytes")
 
@@ -130,7 +130,9 @@ def load(path: str | None = None):
     lib.paro_w4a16_linear_choose_path.argtypes = [P, I64]
     lib.paro_validate_layer.argtypes = [P]
     lib.paro_attention_prompt.argtypes = [P, P, P, P, I32, P, P, I64, I64, I64, P, P]
-    lib.paro_attention_prompt_cached.argtypes = [P, I32, P, P, P, P, I64, I64, P, P]
+    lib.paro_attention_prompt_cached.argtypes = [P, I32, P, P, P, P, I64, I64, P, P, SZ, P]
+    lib.paro_attention_prompt_cached_workspace_bytes.argtypes = [P, I64, I64, I32]
+    lib.paro_attention_prompt_cached_workspace_bytes.restype = SZ
     lib.paro_attention_decode.argtypes = [P, I32, P, P, P, I64, P, P, SZ, P]
     lib.paro_attention_decode_workspace_bytes.argtypes = [P, I64, I32]
     lib.paro_attention_decode_workspace_bytes.restype = SZ
@@ -560,10 +562,15 @@ def paro_attention_prompt(q, k, v, cu_q, cu_k, y, scale=None, causal=True, strea
                    y.data_ptr()), what)
 
 
+def paro_attention_prompt_cached_workspace_bytes(cache: KVCache, sequences: int, tokens: int, q_heads: int) -> int:
+    return int(load().paro_attention_prompt_cached_workspace_bytes(cache.ref, sequences, tokens, q_heads))
+
+
 def paro_attention_prompt_cached(cache: KVCache, layer: int, q, slots, cu_q, y, scale=None, causal=True,
-                                 stream=None) -> None:
+                                 stream=None, workspace=None) -> None:
     """q, y: (tokens, q_heads, head_dim) of the cache's dtype: the newest rows of the slots; slots: int32
-    (sequences,); cu_q: int64 (sequences + 1,)."""
+    (sequences,); cu_q: int64 (sequences + 1,); workspace: zero-filled before its first use, of
+    paro_attention_prompt_cached_workspace_bytes() bytes: splits the keys of few rows over workgroups."""
     import torch
     what, dt, dev = "paro_attention_prompt_cached", cache.dtype, cache.device
     qs, ys = _rows(q, dt, dev, what, "q"), _rows(y, dt, dev, what, "y")
@@ -573,7 +580,8 @@ def paro_attention_prompt_cached(cache: KVCache, layer: int, q, slots, cu_q, y, 
     _index(cu_q, torch.int64, n + 1, dev, what, "cu_q")
     s = _shape_of(q, cache.c.kv_heads, scale, causal, qs, ys)
     _check(_launch(load().paro_attention_prompt_cached, dev, stream, cache.ref, layer, ctypes.byref(s), q.data_ptr(),
-                   slots.data_ptr(), cu_q.data_ptr(), n, q.shape[0], y.data_ptr()), what)
+                   slots.data_ptr(), cu_q.data_ptr(), n, q.shape[0], y.data_ptr(), _ptr(workspace),
+                   _scratch(workspace, dev, what)), what)
 
 
 def paro_attention_decode_workspace_bytes(cache: KVCache, rows: int, q_heads: int) -> int:

@@ -44,8 +44,14 @@ struct AttentionArgs {
   KvLayer kv;            // cache forms
 };
 
-// Prompts: K and V packed (cached = false) or in the cache's pages.
-hipError_t launch_attention_prompt(const AttentionArgs &a, bool cached, hipStream_t st);
+// Prompts: K and V packed (cached = false) or in the cache's pages.  Over the
+// cache, few rows may have their keys split over `splits` workgroups (at most
+// attention_prompt_splits; then there are fewer than kDecodeCounters of them).
+int attention_prompt_splits(int64_t q_tokens, int64_t sequences, int q_heads, int kv_heads, int64_t max_len);
+size_t attention_prompt_partial_bytes(int splits, int64_t q_tokens, int64_t sequences, int q_heads, int kv_heads,
+                                      int head_dim);
+hipError_t launch_attention_prompt(const AttentionArgs &a, bool cached, int splits, uint32_t *counters, float *sums,
+                                   hipStream_t st);
 
 // One token per row over the cache.  The length of a row is split over
 // `splits` workgroups where there are fewer than kDecodeCounters (row,

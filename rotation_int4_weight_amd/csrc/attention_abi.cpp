@@ -164,11 +164,14 @@ int check_cache_and_shape(const paro_kv_cache *c, int layer, const paro_attentio
   return PARO_OK;
 }
 
+bool overlaps_cache(const paro_kv_cache *c, const void *p, size_t bytes) {
+  return overlap(p, bytes, c->k, pool_bytes(c)) || overlap(p, bytes, c->v, pool_bytes(c)) ||
+         overlap(p, bytes, c->table, (size_t)c->slots * c->max_pages * 4) ||
+         overlap(p, bytes, c->lengths, (size_t)c->slots * 4) || overlap(p, bytes, c->refs, (size_t)c->num_pages * 4);
+}
+
 int check_apart_from_cache(const paro_kv_cache *c, const paro_attention_shape *s, const void *y, int64_t rows) {
-  const size_t yb = extent(rows, s->q_heads, s->head_dim, s->y_token, s->y_head);
-  if (overlap(y, yb, c->k, pool_bytes(c)) || overlap(y, yb, c->v, pool_bytes(c)) ||
-      overlap(y, yb, c->table, (size_t)c->slots * c->max_pages * 4) ||
-      overlap(y, yb, c->lengths, (size_t)c->slots * 4) || overlap(y, yb, c->refs, (size_t)c->num_pages * 4))
+  if (overlaps_cache(c, y, extent(rows, s->q_heads, s->head_dim, s->y_token, s->y_head)))
     return fail(PARO_ERR_SHAPE, "y overlaps the cache");
   return PARO_OK;
 }
@@ -213,10 +216,7 @@ int check_kv_workspace(const paro_kv_cache *c, const void *workspace, size_t byt
   if (!workspace || bytes < need)
     return fail(PARO_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace ? bytes : 0, need);
   if (!aligned(workspace, 16)) return fail(PARO_ERR_ALIGN, "workspace must be 16-byte aligned");
-  if (overlap(workspace, need, c->refs, (size_t)c->num_pages * 4) ||
-      overlap(workspace, need, c->table, (size_t)c->slots * c->max_pages * 4) ||
-      overlap(workspace, need, c->lengths, (size_t)c->slots * 4) || overlap(workspace, need, c->k, pool_bytes(c)) ||
-      overlap(workspace, need, c->v, pool_bytes(c)))
+  if (overlaps_cache(c, workspace, need))
     return fail(PARO_ERR_SHAPE, "the workspace overlaps the cache");
   return PARO_OK;
 }
@@ -272,14 +272,26 @@ int paro_attention_prompt(const paro_attention_shape *s, const void *q, const vo
   a.sequences = (int)sequences;
   a.q_tokens = q_tokens;
   a.k_tokens = k_tokens;
-  hipError_t e = paro::launch_attention_prompt(a, false, (hipStream_t)stream);
+  hipError_t e = paro::launch_attention_prompt(a, false, 1, nullptr, nullptr, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "prompt attention launch");
   return ok();
 }
 
+size_t paro_attention_prompt_cached_workspace_bytes(const paro_kv_cache *c, int64_t sequences, int64_t q_tokens,
+                                                    int q_heads) {
+  if (check_cache(c, false) || sequences <= 0 || sequences > paro::kMaxSequences || q_tokens <= 0 ||
+      q_tokens > kMaxRows || q_heads < 1 || q_heads > kMaxHeads || q_heads % c->kv_heads)
+    return 0;
+  const int splits = paro::attention_prompt_splits(q_tokens, sequences, q_heads, c->kv_heads,
+                                                   (int64_t)c->max_pages * c->page_size);
+  if (splits == 1) return 0;
+  return kCounterBytes +
+         paro::attention_prompt_partial_bytes(splits, q_tokens, sequences, q_heads, c->kv_heads, c->head_dim);
+}
+
 int paro_attention_prompt_cached(const paro_kv_cache *c, int layer, const paro_attention_shape *s, const void *q,
                                  const int32_t *slots, const int64_t *cu_q, int64_t sequences, int64_t q_tokens,
-                                 void *y, void *stream) {
+                                 void *y, void *workspace, size_t workspace_bytes, void *stream) {
   int rc = check_cache_and_shape(c, layer, s);
   if (!rc) rc = check_rows(q_tokens, "q_tokens", kMaxRows);
   if (!rc) rc = check_rows(sequences, "sequences", paro::kMaxSequences);
@@ -292,13 +304,31 @@ int paro_attention_prompt_cached(const paro_kv_cache *c, int layer, const paro_a
   const size_t yb = extent(q_tokens, s->q_heads, s->head_dim, s->y_token, s->y_head);
   if (overlap(y, yb, cu_q, (size_t)(sequences + 1) * 8) || overlap(y, yb, slots, (size_t)sequences * 4))
     return fail(PARO_ERR_SHAPE, "y overlaps cu_q or slots");
+  const size_t need = paro_attention_prompt_cached_workspace_bytes(c, sequences, q_tokens, s->q_heads);
+  const bool split = workspace && need > 0;
+  if (split) {
+    if (workspace_bytes < need)
+      return fail(PARO_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+    if (!aligned(workspace, 16)) return fail(PARO_ERR_ALIGN, "workspace must be 16-byte aligned");
+    if (overlap(workspace, need, y, yb) ||
+        overlap(workspace, need, q, extent(q_tokens, s->q_heads, s->head_dim, s->q_token, s->q_head)) ||
+        overlap(workspace, need, cu_q, (size_t)(sequences + 1) * 8) ||
+        overlap(workspace, need, slots, (size_t)sequences * 4) || overlaps_cache(c, workspace, need))
+      return fail(PARO_ERR_SHAPE, "the workspace overlaps q, y, cu_q, slots or the cache");
+  }
   paro::AttentionArgs a = attention_args(s, q, y, c->dt);
   a.cu_q = cu_q;
   a.slots = slots;
   a.sequences = (int)sequences;
   a.q_tokens = q_tokens;
   a.kv = kv_layer(c, layer);
-  hipError_t e = paro::launch_attention_prompt(a, true, (hipStream_t)stream);
+  hipError_t e = paro::launch_attention_prompt(
+      a, true,
+      split ? paro::attention_prompt_splits(q_tokens, sequences, s->q_heads, c->kv_heads,
+                                            (int64_t)c->max_pages * c->page_size)
+            : 1,
+      split ? (uint32_t *)workspace : nullptr, split ? (float *)((char *)workspace + kCounterBytes) : nullptr,
+      (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "cached prompt attention launch");
   return ok();
 }
@@ -330,10 +360,7 @@ int paro_attention_decode(const paro_kv_cache *c, int layer, const paro_attentio
   if (!aligned(workspace, 16)) return fail(PARO_ERR_ALIGN, "workspace must be 16-byte aligned");
   if (overlap(workspace, need, y, yb) ||
       overlap(workspace, need, q, extent(rows, s->q_heads, s->head_dim, s->q_token, s->q_head)) ||
-      overlap(workspace, need, slots, (size_t)rows * 4) || overlap(workspace, need, c->k, pool_bytes(c)) ||
-      overlap(workspace, need, c->v, pool_bytes(c)) ||
-      overlap(workspace, need, c->table, (size_t)c->slots * c->max_pages * 4) ||
-      overlap(workspace, need, c->lengths, (size_t)c->slots * 4))
+      overlap(workspace, need, slots, (size_t)rows * 4) || overlaps_cache(c, workspace, need))
     return fail(PARO_ERR_SHAPE, "the workspace overlaps q, y, slots or the cache");
   paro::AttentionArgs a = attention_args(s, q, y, c->dt);
   a.slots = slots;

@@ -43,6 +43,7 @@
 #include <float.h>
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attention.hpp"
@@ -65,6 +66,14 @@ constexpr int kKeys = 64;  // keys per tile
 // 18.1, 1024 rows over 9024 (264) 214 and 225.  A prompt of one key tile has
 // nothing to split (17 tokens: 5.8 us, 6.5 split).
 constexpr int kFewTiles = 96;
+// With a workspace the parts of few rows' keys fill the 256 CUs once (one
+// workgroup of the SPLIT kernel fits a CU), no part shorter than this: it is
+// two tiles per wave, and joining costs 2 to 3 us (4 rows over 1000 keys, one
+// part and two: 11.8 and 12.1 us; over 500, parts of 256: 9.0 and 10.9).  8 rows
+// over 32768 keys 186 and 40 us, over 131072 1216 and 135, 64 over 8064 51 and
+// 32.
+constexpr int kPartKeys = 512;
+constexpr int64_t kCus = 256;
 
 template <int DT>
 __device__ __forceinline__ f32x16 mfma32x32x16(const u32x4 &a, const u32x4 &b, const f32x16 &c) {
@@ -337,12 +346,32 @@ struct Loader {
   }
 };
 
+// What a workgroup of the SPLIT kernel has of its rows' keys, and where the
+// parts of other workgroups meet (parts == 1: nowhere).
+struct Part {
+  int index, parts;
+  float *sums;        // the parts of these rows: [parts][32][DIM + 4]
+  uint32_t *counter;  // workgroups that have stored theirs; zero between calls
+};
+// Two floats that another XCD will read or wrote: past the L2s.
+__device__ __forceinline__ void store_coherent(float *p, float x, float y) {
+  __hip_atomic_store(reinterpret_cast<uint64_t *>(p), (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x),
+                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x2 load_coherent(const float *p) {
+  const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return f32x2{__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))};
+}
+
 // Joins the waves' sums of the same 32 rows (each relative to its own m2, the
-// maximum times scale2) and writes the rows: thread (row, 8 channels).
-template <int DT, int DIM, bool CACHED, int NW>
+// maximum times scale2) and writes the rows: thread (row, 8 channels).  Where
+// the keys are in parts, each workgroup stores its joined sums and the last one
+// to arrive joins them, in their order.
+template <int DT, int DIM, bool CACHED, int NW, bool PARTS>
 __device__ __forceinline__ void join_waves(const AttentionArgs &a, const Rows &r, int kvh, int base, int rows,
-                                           int least, int most, const f32x16 (&o)[DIM / 32], float m2, float l, float *lds) {
-  constexpr int RS = DIM + 4;  // LDS row: its channels, then m2 and l
+                                           int least, int most, const f32x16 (&o)[DIM / 32], float m2, float l,
+                                           float *lds, const Part &part) {
+  constexpr int RS = DIM + 4;  // row of sums: its channels, then m2 and l
   const int lane = lane_id(), wave = wave_id(), h = lane >> 5, col = lane & 31;
   __syncthreads();  // every wave is done with its tiles
   float *mine = lds + (wave * 32 + col) * RS;
@@ -358,22 +387,7 @@ __device__ __forceinline__ void join_waves(const AttentionArgs &a, const Rows &r
   }
   __syncthreads();
   bool bad = false;
-  for (int e = threadIdx.x; e < 32 * DIM / 8; e += 64 * NW) {
-    const int row = e / (DIM / 8), c = e % (DIM / 8) * 8;
-    if (base + row >= rows) continue;
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) top = fmaxf(top, lds[(w * 32 + row) * RS + DIM]);
-    float sum = 0.f;
-    f32x4 x0 = {0.f, 0.f, 0.f, 0.f}, x1 = x0;
-#pragma unroll 2
-    for (int w = 0; w < NW; ++w) {
-      const float *part = lds + (w * 32 + row) * RS;
-      const float keep = part[DIM] == top ? 1.f : __builtin_amdgcn_exp2f(part[DIM] - top);
-      sum += keep * part[DIM + 1];
-      x0 += keep * *reinterpret_cast<const f32x4 *>(part + c);
-      x1 += keep * *reinterpret_cast<const f32x4 *>(part + c + 4);
-    }
+  const auto write = [&](int row, int c, f32x4 x0, f32x4 x1, float sum) {
     const int token = (base + row) / a.group, head = kvh * a.group + (base + row) % a.group;
     const bool any = r.n_k > 0 && (!a.causal || token + 1 + r.n_k - r.n_q > 0);
     const float inv = any ? 1.f / sum : 0.f;
@@ -388,6 +402,65 @@ __device__ __forceinline__ void join_waves(const AttentionArgs &a, const Rows &r
     const u32x4 y = {pack2_rne<DT>(x0[0], x0[1]), pack2_rne<DT>(x0[2], x0[3]), pack2_rne<DT>(x1[0], x1[1]),
                      pack2_rne<DT>(x1[2], x1[3])};
     *reinterpret_cast<u32x4 *>(a.y + (r.q0 + token) * a.y_token + head * a.y_head + c) = any ? y : u32x4{0, 0, 0, 0};
+  };
+  for (int e = threadIdx.x; e < 32 * DIM / 8; e += 64 * NW) {
+    const int row = e / (DIM / 8), c = e % (DIM / 8) * 8;
+    if (base + row >= rows) continue;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, lds[(w * 32 + row) * RS + DIM]);
+    float sum = 0.f;
+    f32x4 x0 = {0.f, 0.f, 0.f, 0.f}, x1 = x0;
+#pragma unroll 2
+    for (int w = 0; w < NW; ++w) {
+      const float *from = lds + (w * 32 + row) * RS;
+      const float keep = from[DIM] == top ? 1.f : __builtin_amdgcn_exp2f(from[DIM] - top);
+      sum += keep * from[DIM + 1];
+      x0 += keep * *reinterpret_cast<const f32x4 *>(from + c);
+      x1 += keep * *reinterpret_cast<const f32x4 *>(from + c + 4);
+    }
+    if (!PARTS || part.parts == 1) {
+      write(row, c, x0, x1, sum);
+    } else {
+      float *to = part.sums + ((int64_t)part.index * 32 + row) * RS;
+      store_coherent(to + c, x0[0], x0[1]);
+      store_coherent(to + c + 2, x0[2], x0[3]);
+      store_coherent(to + c + 4, x1[0], x1[1]);
+      store_coherent(to + c + 6, x1[2], x1[3]);
+      if (c == 0) store_coherent(to + DIM, top, sum);
+    }
+  }
+  if (PARTS && part.parts > 1) {
+    __builtin_amdgcn_s_waitcnt(0);  // this thread's sums have been stored
+    __syncthreads();
+    int *last = reinterpret_cast<int *>(lds);
+    if (threadIdx.x == 0) {
+      const uint32_t old = __hip_atomic_fetch_add(part.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      *last = old == (uint32_t)(part.parts - 1);
+    }
+    __syncthreads();
+    if (!*last) return;
+    for (int e = threadIdx.x; e < 32 * DIM / 8; e += 64 * NW) {
+      const int row = e / (DIM / 8), c = e % (DIM / 8) * 8;
+      if (base + row >= rows) continue;
+      float top = -INFINITY, sum = 0.f;
+      f32x4 x0 = {0.f, 0.f, 0.f, 0.f}, x1 = x0;
+#pragma unroll 4
+      for (int i = 0; i < part.parts; ++i) {
+        const float *from = part.sums + ((int64_t)i * 32 + row) * RS;
+        const f32x2 ml = load_coherent(from + DIM), y0 = load_coherent(from + c), y1 = load_coherent(from + c + 2),
+                    y2 = load_coherent(from + c + 4), y3 = load_coherent(from + c + 6);
+        const float mn = fmaxf(top, ml[0]);
+        const float ka = top == mn ? 1.f : __builtin_amdgcn_exp2f(top - mn),
+                    kb = ml[0] == mn ? 1.f : __builtin_amdgcn_exp2f(ml[0] - mn);
+        top = mn;
+        sum = sum * ka + ml[1] * kb;
+        x0 = x0 * ka + f32x4{y0[0], y0[1], y1[0], y1[1]} * kb;
+        x1 = x1 * ka + f32x4{y2[0], y2[1], y3[0], y3[1]} * kb;
+      }
+      write(row, c, x0, x1, sum);
+    }
+    if (threadIdx.x == 0) __hip_atomic_store(part.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   // tiles are 32 keys here, the search's 64: it may find a value that no tile held
   if (__syncthreads_or(bad) && masked_not_finite<DT, DIM, CACHED>(a, r, kvh, least, most)) {
@@ -400,9 +473,12 @@ __device__ __forceinline__ void join_waves(const AttentionArgs &a, const Rows &r
 // SPLIT: the waves share 32 rows and take tiles of 32 keys in turn, each with
 // LDS buffers of its own (one for K, one for V, so that twice as many waves
 // fit: the next K is loaded once the scores are formed, the next V once the
-// values are summed); their sums are joined at the end.
-template <int DT, int DIM, bool CACHED, int NW, bool SPLIT>
-__global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionArgs a, int row_tiles) {
+// values are summed); their sums are joined at the end.  PARTS: the keys go to
+// gridDim.z workgroups first (apart, since the one more range costs the SPLIT
+// kernel registers: 64 rows over 8064 keys 58 instead of 50 us).
+template <int DT, int DIM, bool CACHED, int NW, bool SPLIT, bool PARTS>
+__global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionArgs a, int row_tiles,
+                                                                      uint32_t *counters, float *sums) {
   constexpr int BM = SPLIT ? 32 : 32 * NW, KS = DIM / 16, DB = DIM / 32;
   constexpr int KEYS = SPLIT ? 32 : kKeys, KB = KEYS / 32;
   constexpr int kTileBytes = KEYS * DIM * 2;
@@ -412,7 +488,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
   const int h = lane >> 5, col = lane & 31;
   char *const lds = all_lds + (SPLIT ? wave * 2 * kTileBytes : 0);
-  const int begin = SPLIT ? wave * KEYS : 0, stride = SPLIT ? NW * KEYS : KEYS;  // this wave's tiles
+  const int stride = SPLIT ? NW * KEYS : KEYS;  // between this wave's tiles
   const int share = SPLIT ? 0 : wave;                                            // of a tile's loads
   // key-value heads next to each other in the launch order: workgroups go to
   // the XCDs in turn, so with 8 heads each XCD's L2 holds one head's K and V;
@@ -434,6 +510,15 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
   const int seen = seen_by(mine);
   const int wave_least = seen_by(min(base, rows - 1)), wave_most = seen_by(min(base + 31, rows - 1));
   const int most = __builtin_amdgcn_readfirstlane(seen_by(min((r.index + 1) * BM, rows) - 1));
+  // this workgroup's part of the keys, and this wave's first tile
+  int begin = SPLIT ? wave * KEYS : 0, end = most, keys = 0;
+  if constexpr (PARTS) {
+    const int splits = (int)gridDim.z, index = (int)blockIdx.z;
+    keys = max(kPartKeys, ((most + splits - 1) / splits + stride - 1) / stride * stride);
+    if (index > 0 && index * keys >= most) return;
+    begin += index * keys;
+    end = min(most, index * keys + keys);
+  }
 
   // Q^T fragments: row lane%32, channels 16 s + 8 h..; a negative scale goes to Q
   u32x4 q[KS];
@@ -470,7 +555,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
   float m = -INFINITY, l = 0.f;
 
   Loader<DIM, CACHED, SPLIT ? 1 : NW, KEYS> loader;
-  if (begin < most) {
+  if (begin < end) {
     loader.init(a, r, kvh, begin, share, lane);
     if constexpr (SPLIT) {
       loader.template load_one<false>(a, r, begin, lds);
@@ -482,7 +567,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
   }
   const auto step = [&](int j0, auto which) __attribute__((always_inline)) {
     constexpr int buf = decltype(which)::value;
-    const bool more = j0 + stride < most;
+    const bool more = j0 + stride < end;
     if constexpr (SPLIT) {
       wait_loads<decltype(loader)::kLoads>();  // K has landed; V may be on its way
     } else {
@@ -572,7 +657,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
     }
   };
   if constexpr (SPLIT) {
-    for (int j0 = begin; j0 < most; j0 += stride) step(j0, std::integral_constant<int, 0>());
+    for (int j0 = begin; j0 < end; j0 += stride) step(j0, std::integral_constant<int, 0>());
   } else {
     for (int j0 = 0; j0 < most; j0 += 2 * kKeys) {
       step(j0, std::integral_constant<int, 0>());
@@ -586,7 +671,15 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
     l = __uint_as_float(w[0]) + __uint_as_float(w[1]);
   }
   if constexpr (SPLIT) {
-    join_waves<DT, DIM, CACHED, NW>(a, r, kvh, base, rows, wave_least, wave_most, o, m * scale2, l, reinterpret_cast<float *>(all_lds));
+    Part part = {0, 1, nullptr, nullptr};
+    if constexpr (PARTS) {
+      part.index = (int)blockIdx.z;
+      part.parts = max(1, (most + keys - 1) / keys);
+      part.sums = sums + (int64_t)blockIdx.x * gridDim.z * 32 * (DIM + 4);
+      part.counter = counters + blockIdx.x;
+    }
+    join_waves<DT, DIM, CACHED, NW, PARTS>(a, r, kvh, base, rows, wave_least, wave_most, o, m * scale2, l, reinterpret_cast<float *>(all_lds),
+                                     part);
     return;
   }
   const bool stored = base + col < rows;
@@ -619,33 +712,62 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
   }
 }
 
+// Workgroups of `rows` rows that sequences of so many tokens in all take at most, per key-value head.
+int64_t row_tiles(int64_t q_tokens, int64_t sequences, int group, int rows) {
+  return q_tokens * group / rows + sequences;
+}
+
 template <int DT, int DIM, bool CACHED>
-hipError_t launch_typed(const AttentionArgs &a, hipStream_t st) {
-  constexpr int NW = 4, BM = 32 * NW;
-  const int64_t tiles = a.q_tokens * a.group / BM + a.sequences;
+hipError_t launch_typed(const AttentionArgs &a, int splits, uint32_t *counters, float *sums, hipStream_t st) {
+  constexpr int NW = 4;
+  const int64_t tiles = row_tiles(a.q_tokens, a.sequences, a.group, 32 * NW);
   if (tiles * a.kv_heads <= kFewTiles && (CACHED || a.k_tokens > kKeys)) {
     constexpr int SW = 8;
-    const int64_t small = a.q_tokens * a.group / 32 + a.sequences;
-    hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, SW, true>), dim3((unsigned)(small * a.kv_heads)),
-                       dim3(64 * SW), 0, st, a, (int)small);
+    const int64_t small = row_tiles(a.q_tokens, a.sequences, a.group, 32);
+    const dim3 grid((unsigned)(small * a.kv_heads), 1, (unsigned)splits), block(64 * SW);
+    if constexpr (CACHED) {
+      if (splits > 1) {
+        hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, SW, true, true>), grid, block, 0, st, a,
+                           (int)small, counters, sums);
+        return hipGetLastError();
+      }
+    }
+    hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, SW, true, false>), grid, block, 0, st, a, (int)small,
+                       counters, sums);
   } else {
-    hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, NW, false>), dim3((unsigned)(tiles * a.kv_heads)),
-                       dim3(64 * NW), 0, st, a, (int)tiles);
+    hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, NW, false, false>), dim3((unsigned)(tiles * a.kv_heads)),
+                       dim3(64 * NW), 0, st, a, (int)tiles, counters, sums);
   }
   return hipGetLastError();
 }
 
 template <bool CACHED>
-hipError_t launch(const AttentionArgs &a, hipStream_t st) {
+hipError_t launch(const AttentionArgs &a, int splits, uint32_t *counters, float *sums, hipStream_t st) {
   if (a.dt == kF16)
-    return a.head_dim == 64 ? launch_typed<kF16, 64, CACHED>(a, st) : launch_typed<kF16, 128, CACHED>(a, st);
-  return a.head_dim == 64 ? launch_typed<kBF16, 64, CACHED>(a, st) : launch_typed<kBF16, 128, CACHED>(a, st);
+    return a.head_dim == 64 ? launch_typed<kF16, 64, CACHED>(a, splits, counters, sums, st)
+                            : launch_typed<kF16, 128, CACHED>(a, splits, counters, sums, st);
+  return a.head_dim == 64 ? launch_typed<kBF16, 64, CACHED>(a, splits, counters, sums, st)
+                          : launch_typed<kBF16, 128, CACHED>(a, splits, counters, sums, st);
 }
 
 }  // namespace
 
-hipError_t launch_attention_prompt(const AttentionArgs &a, bool cached, hipStream_t st) {
-  return cached ? launch<true>(a, st) : launch<false>(a, st);
+int attention_prompt_splits(int64_t q_tokens, int64_t sequences, int q_heads, int kv_heads, int64_t max_len) {
+  const int group = q_heads / kv_heads;
+  if (row_tiles(q_tokens, sequences, group, 128) * kv_heads > kFewTiles) return 1;
+  const int64_t items = row_tiles(q_tokens, sequences, group, 32) * kv_heads;
+  return (int)std::max<int64_t>(1, std::min(kCus / items, (max_len + kPartKeys - 1) / kPartKeys));
+}
+
+size_t attention_prompt_partial_bytes(int splits, int64_t q_tokens, int64_t sequences, int q_heads, int kv_heads,
+                                      int head_dim) {
+  if (splits == 1) return 0;
+  return (size_t)row_tiles(q_tokens, sequences, q_heads / kv_heads, 32) * kv_heads * splits * 32 * (head_dim + 4) * 4;
+}
+
+hipError_t launch_attention_prompt(const AttentionArgs &a, bool cached, int splits, uint32_t *counters, float *sums,
+                                   hipStream_t st) {
+  return cached ? launch<true>(a, splits, counters, sums, st) : launch<false>(a, 1, nullptr, nullptr, st);
 }
 
 }  // namespace paro

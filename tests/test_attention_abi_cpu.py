@@ -35,9 +35,9 @@ def prompt(s=None, q=Q, k=K, v=V, dt=0, cu_q=CU, cu_k=CU, n=1, tq=0, tk=0, y=Y):
                                              tk, y, None)
 
 
-def cached(c=None, layer=0, s=None, q=Q, slots=LIST, cu=CU, n=1, tq=0, y=Y):
+def cached(c=None, layer=0, s=None, q=Q, slots=LIST, cu=CU, n=1, tq=0, y=Y, ws=None, nb=0):
     return _lib.load().paro_attention_prompt_cached(ctypes.byref(c or cache()), layer, ctypes.byref(s or shape()), q,
-                                                    slots, cu, n, tq, y, None)
+                                                    slots, cu, n, tq, y, ws, nb, None)
 
 
 def decode(c=None, layer=0, s=None, q=Q, slots=LIST, rows=0, y=Y, ws=WS, nb=BIG):
@@ -142,6 +142,21 @@ def test_decode_and_cached_arguments():
     for at in (A, A + STEP, A + 3 * STEP, A + 4 * STEP):
         assert decode(rows=2, y=at) == SHAPE and cached(tq=2, y=at) == SHAPE
     assert decode(rows=2, y=LIST) == SHAPE and cached(tq=2, y=CU) == SHAPE
+
+
+def test_cached_workspace():
+    big = cache(max_pages=400, num_pages=800)
+    need = lambda c, n, t, h: _lib.load().paro_attention_prompt_cached_workspace_bytes(ctypes.byref(c), n, t, h)  # noqa: E731
+    assert need(big, 1, 4, 8) > 2 ** 21 and need(cache(), 1, 4, 8) == 0  # 128 positions: nothing to split
+    assert need(big, 1, 5000, 8) == 0 and need(big, 200, 200, 8) == 0  # enough rows without
+    assert need(big, 0, 4, 8) == 0 and need(big, 1, 0, 8) == 0 and need(big, 1, 4, 7) == 0
+    assert need(big, -1, 4, 8) == 0 and need(big, 1, 1 << 30, 8) == 0 and need(big, 1 << 20, 4, 8) == 0
+    few = dict(c=big, n=1, tq=4)
+    n = need(big, 1, 4, 8)
+    assert cached(**few, ws=WS, nb=n - 1) == WORKSPACE and cached(**few, ws=WS, nb=0) == WORKSPACE
+    assert cached(**few, ws=WS + 8, nb=BIG) == ALIGN
+    for at in (Q, Y, CU, LIST, A, A + STEP, A + 2 * STEP, A + 3 * STEP, A + 4 * STEP):
+        assert cached(**few, ws=at, nb=BIG) == SHAPE
 
 
 def test_append_arguments():

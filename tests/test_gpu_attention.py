@@ -314,6 +314,55 @@ def test_chunk_layers_empty_and_foreign_slots():
     assert bool((y[93:] == 0).all())  # no keys
 
 
+def run_split_chunk(lengths, new, heads, kv_heads, dim, page, dtype, causal=True, layers=1, layer=0):
+    c = filled_cache(paro, lengths, page, kv_heads, dim, dtype, len(new), layers=layers)
+    q = randn((sum(new), heads, dim), dtype, 5, 1.5)
+    slots, cu = torch.arange(len(new), dtype=torch.int32, device="cuda"), offsets(new)
+    need = paro.paro_attention_prompt_cached_workspace_bytes(c, len(new), sum(new), heads)
+    assert need > 0
+    ws = paro.make_workspace(need)
+    first = None
+    for _ in range(3):  # the workspace serves again, and the bits repeat
+        y = torch.full_like(q, NAN)
+        paro.paro_attention_prompt_cached(c, layer, q, slots, cu, y, causal=causal, workspace=ws)
+        torch.cuda.synchronize()
+        first = y if first is None else first
+        assert torch.equal(y, first)
+    assert not ws[:2 ** 21].any()  # the counter area
+    at = 0
+    for s, n in enumerate(new):
+        k, v = cached_rows(c, layer, s)
+        check_rows(y[at:at + n], q[at:at + n], k, v, default_scale(dim), causal)
+        at += n
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim,heads", [(64, (7, 1)), (128, (8, 2)), (128, (4, 4))])
+def test_chunk_keys_split_over_workgroups(dim, heads, dtype):
+    run_split_chunk([5000], [6], *heads, dim, 64, dtype)
+    run_split_chunk([2300, 1, 0, 513, 40, 1024], [33, 1, 0, 5, 70, 2], *heads, dim, 16, dtype, layers=2, layer=1)
+    run_split_chunk([1500, 3], [17, 40], *heads, dim, 32, dtype, causal=False)
+
+
+def test_chunk_split_with_masked_and_visible_bad_values():
+    dtype, dim, n, m = torch.float16, 64, 3000, 40
+    c = filled_cache(paro, [n], 16, 1, dim, dtype, 1)
+    q, slots, cu = randn((m, 4, dim), dtype, 2), torch.zeros(1, dtype=torch.int32, device="cuda"), offsets([m])
+    ws = paro.make_workspace(paro.paro_attention_prompt_cached_workspace_bytes(c, 1, m, 4))
+    k, v = (x.clone() for x in cached_rows(c, 0, 0))
+    for at in (n - 1, n - 20):  # seen by the last rows alone
+        page, row = int(c.table[0, at // 16]), at % 16
+        c.v[0, page, :, row] = NAN
+        y = torch.full_like(q, 3.0)
+        paro.paro_attention_prompt_cached(c, 0, q, slots, cu, y, workspace=ws)
+        clean = m - (n - at)
+        check_rows(y[:clean], q[:clean], k[:n - m + clean], v[:n - m + clean], default_scale(dim))
+        assert bool(torch.isnan(y[clean:]).all())
+    c.v[0, int(c.table[0, 40]), :, 3, 9] = NAN
+    paro.paro_attention_prompt_cached(c, 0, q, slots, cu, y, workspace=ws)
+    assert bool(torch.isnan(y[:, :, 9]).all()) and not torch.isnan(y[:clean, :, :9]).any()
+
+
 def run_decode(lengths, heads, kv_heads, dim, page, dtype, seed=0, order=None, extra=2, layers=1, layer=0):
     c = filled_cache(paro, lengths, page, kv_heads, dim, dtype, seed, extra=extra, layers=layers)
     order = list(range(len(lengths))) if order is None else order
@@ -443,3 +492,10 @@ def test_binding_refuses():
                  (c, 0, q[:, :3], s, y[:, :3], ws), (c, 0, q.bfloat16(), s, y, ws), (c, 0, q, s.long(), y, ws)]:
         with pytest.raises(paro.ParoError):
             paro.paro_attention_decode(*args)
+    c = paro.KVCache.empty(1, 200, 2, 16, 64, 2, 100, f)
+    need = paro.paro_attention_prompt_cached_workspace_bytes(c, 1, 4, 4)
+    ws = paro.make_workspace(need)
+    paro.paro_attention_prompt_cached(c, 0, q, s[:1], cu, y, workspace=ws)
+    for bad in (ws[:need - 16], ws.cpu(), ws[::2]):
+        with pytest.raises(paro.ParoError):
+            paro.paro_attention_prompt_cached(c, 0, q, s[:1], cu, y, workspace=bad)

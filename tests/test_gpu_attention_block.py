@@ -251,7 +251,9 @@ def test_one_workspace_for_linears_attention_and_pages():
     x = torch.from_numpy(np.ascontiguousarray(synth.make_x(971, 0, rows, 1024, dt)).view(np.int16)).cuda()
     x = x.view(cache.dtype)
     need = max(paro.paro_w4a16_linear_workspace_bytes(lin, rows), paro.paro_kv_workspace_bytes(cache),
-               max(paro.paro_attention_decode_workspace_bytes(cache, r, 8) for r in (1, 2)))
+               max(paro.paro_attention_decode_workspace_bytes(cache, r, 8) for r in (1, 2)),
+               paro.paro_attention_prompt_cached_workspace_bytes(cache, 1, 2, 8))
+    assert paro.paro_attention_prompt_cached_workspace_bytes(cache, 1, 2, 8) > 0
     shared, alone = paro.make_workspace(need), paro.make_workspace(need)
     want, got = e(rows, 16384), e(rows, 16384)
     paro.paro_w4a16_linear(lin, x, want, alone)
@@ -266,6 +268,9 @@ def test_one_workspace_for_linears_attention_and_pages():
         a = e(rows, 8, dim)
         paro.paro_attention_decode(cache, 0, q, ints([1, 3]), a, shared)
         paro.paro_attention_decode(cache, 0, q[:1], ints([3]), e(1, 8, dim), shared)
+        chunk = e(2, 8, dim)
+        paro.paro_attention_prompt_cached(cache, 0, q, ints([1]), offsets([2]), chunk, workspace=shared)
+        check_rows(chunk, q, k[:2500], -k[:2500], default_scale(dim))
         paro.paro_w4a16_linear(lin, x, got, shared)
         assert torch.equal(got, want)
         paro.paro_kv_fork(cache, ints([1]), ints([0]), granted[:1], shared)
@@ -275,3 +280,28 @@ def test_one_workspace_for_linears_attention_and_pages():
         assert torch.equal(got, want)
         for r, (lo, n) in enumerate(((0, 2500), (2500, 1800))):
             check_rows(a[r:r + 1], q[r:r + 1], k[lo:lo + n], -k[lo:lo + n], default_scale(dim))
+
+
+def test_captured_split_chunk_follows_the_lengths():
+    """Few rows, their keys split over workgroups, in a graph: replays see the lengths of the moment."""
+    cache = paro.KVCache.empty(1, 250, 2, 16, 64, 2, 250, torch.float16)
+    cache.k.normal_()
+    cache.v.normal_()
+    cache.table[1] = torch.randperm(250, device="cuda").to(torch.int32)
+    cache.refs.fill_(1)
+    q = torch.randn((6, 8, 64), device="cuda").half()
+    y, want, s, cu = torch.empty_like(q), torch.empty_like(q), ints([1]), offsets([6])
+    need = paro.paro_attention_prompt_cached_workspace_bytes(cache, 1, 6, 8)
+    ws, other = paro.make_workspace(need), paro.make_workspace(need)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        paro.paro_attention_prompt_cached(cache, 0, q, s, cu, y, workspace=ws)
+    for n in (4000, 6, 0, 700, 3, 513, 512, 3999, 4000):
+        cache.lengths[1] = n
+        y.fill_(float("nan"))
+        g.replay()
+        paro.paro_attention_prompt_cached(cache, 0, q, s, cu, want, workspace=other)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), n
+    k, v = (x[0, cache.table[1].long()].transpose(1, 2).reshape(4000, 2, 64) for x in (cache.k, cache.v))
+    check_rows(y, q, k, v, default_scale(64))
