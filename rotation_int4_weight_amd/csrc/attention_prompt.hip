@@ -1,7 +1,7 @@
 // attention_prompt.hip - attention over prompts (paro_attention_prompt over
 // packed K and V, paro_attention_prompt_cached over the cache's pages).
 //
-// A workgroup takes BM rows of one key-value head, a row being a (token,
+// A workgroup takes 128 rows of one key-value head, a row being a (token,
 // query head of the group) pair, so that the heads that share K and V share
 // their tiles, short prompts fill a tile and the diagonal wastes little.  K
 // and V stream through LDS in tiles of 64 keys (two buffers, loaded straight
@@ -37,9 +37,9 @@
 // to 1046 TFLOP/s (1222 for a library GEMM of 8192^3); counters: MFMA busy
 // 53 % of the cycles, no LDS bank conflict, 157 MB read from HBM for 100 MB of
 // input.  Interleaving the next tile's scores with the weights by hand took
-// the same time at a lower clock.  With one wave per SIMD (up to 1024 tokens,
-// 25 us) a tile takes 3500 cycles: scores 1160, weights 940, values 790, the
-// next loads' issue and the barrier 580.
+// the same time at a lower clock.  With one wave per SIMD a tile takes 3500
+// cycles: scores 1160, weights 940, values 790, the next loads' issue and the
+// barrier 580 (1024 tokens: 25 us so, 22 with two, see kHalvesKeys).
 #include <float.h>
 #include <math.h>
 
@@ -74,6 +74,16 @@ constexpr int kFewTiles = 96;
 // 32.
 constexpr int kPartKeys = 512;
 constexpr int64_t kCus = 256;
+// Workgroups of 128 rows have eight waves, in two halves that take the key
+// tiles in turn, where there is about one of them per CU: alone there, four
+// waves wait for their own results most of the time.  Four waves and eight, us:
+// 1024 rows over 9024 cached keys (256 workgroups) 217 and 157, 500 over 8500
+// (120) 201 and 140, 16 x 64 over 4064 (256) 128 and 101, but 1500 over 5500
+// (368) 141 and 155.  A causal prompt's workgroups end at different times, so
+// there up to two per CU: 2048 tokens (512) 49.4 and 47.0, 2 x 1000 34.4 and
+// 30.4, 2 x 2000 with 16 heads over 16 58.5 and 46; 2500 (624) 63 and 70.  Short
+// sequences have no tiles to share: 2 x 700 20.6 and 21.1, 4 x 400 18.3 and 22.9.
+constexpr int64_t kHalvesKeys = 768;
 
 template <int DT>
 __device__ __forceinline__ f32x16 mfma32x32x16(const u32x4 &a, const u32x4 &b, const f32x16 &c) {
@@ -311,8 +321,9 @@ struct Loader {
                             : min(KEYS, r.n_k - j0);
     return left > 0 ? (uint32_t)((left - 1) * (CACHED ? DIM : token) * 2 + DIM * 2) : 0u;
   }
-  // the tile at key j0 (after look_up of it), and the look-up of the next one
-  __device__ __forceinline__ void load(const AttentionArgs &a, const Rows &r, int j0, char *to_k, char *to_v, int wave) {
+  // the tile at key j0 (after look_up of it), and the look-up of the one at key next
+  __device__ __forceinline__ void load(const AttentionArgs &a, const Rows &r, int j0, int next, char *to_k, char *to_v,
+                                       int wave) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass does not know the buffer type
 #pragma unroll
     for (int b = 0; b < kBuffers; ++b) {
@@ -328,7 +339,7 @@ struct Loader {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr)(to_v + to), 16, CACHED ? k_off[n] : v_off[n], 0, 0, 0);
       }
     }
-    if constexpr (CACHED) look_up(a, r, j0 + KEYS, wave);
+    if constexpr (CACHED) look_up(a, r, next, wave);
 #endif
   }
   // K or V alone by asm loads (kLoads of them)
@@ -479,17 +490,19 @@ __device__ __forceinline__ void join_waves(const AttentionArgs &a, const Rows &r
 template <int DT, int DIM, bool CACHED, int NW, bool SPLIT, bool PARTS>
 __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionArgs a, int row_tiles,
                                                                       uint32_t *counters, float *sums) {
-  constexpr int BM = SPLIT ? 32 : 32 * NW, KS = DIM / 16, DB = DIM / 32;
+  constexpr bool HALVES = !SPLIT && NW == 8;  // waves 0..3 and 4..7 take tiles in turn
+  constexpr int BM = SPLIT ? 32 : 128, KS = DIM / 16, DB = DIM / 32;
   constexpr int KEYS = SPLIT ? 32 : kKeys, KB = KEYS / 32;
   constexpr int kTileBytes = KEYS * DIM * 2;
   constexpr int kBuffers = SPLIT ? 1 : 2;  // of K, then of V
-  constexpr int kJoinBytes = SPLIT ? NW * 32 * (DIM + 4) * 4 : 0, kAllBytes = (SPLIT ? NW : 1) * 2 * kBuffers * kTileBytes;
+  constexpr int kJoinBytes = SPLIT ? NW * 32 * (DIM + 4) * 4 : 0, kAllBytes = (SPLIT ? NW : NW / 4) * 2 * kBuffers * kTileBytes;
   __shared__ __align__(1024) char all_lds[kJoinBytes > kAllBytes ? kJoinBytes : kAllBytes];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
   const int h = lane >> 5, col = lane & 31;
-  char *const lds = all_lds + (SPLIT ? wave * 2 * kTileBytes : 0);
-  const int stride = SPLIT ? NW * KEYS : KEYS;  // between this wave's tiles
-  const int share = SPLIT ? 0 : wave;                                            // of a tile's loads
+  const int half = HALVES ? wave / 4 : 0;
+  char *const lds = all_lds + (SPLIT ? wave * 2 : half * 4) * kTileBytes;
+  const int stride = SPLIT ? NW * KEYS : NW / 4 * KEYS;  // between this wave's tiles
+  const int share = SPLIT ? 0 : wave - 4 * half;          // of a tile's loads and rows
   // key-value heads next to each other in the launch order: workgroups go to
   // the XCDs in turn, so with 8 heads each XCD's L2 holds one head's K and V;
   // the longest tiles (a sequence's last) first
@@ -498,7 +511,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
   Rows r;
   if (!find_tile<CACHED, BM>(a, t, r)) return;
   const int rows = r.n_q * a.group;  // rows of the sequence and key-value head
-  const int base = r.index * BM + (SPLIT ? 0 : wave * 32);
+  const int base = r.index * BM + 32 * share;
   const int mine = min(base + col, rows - 1);  // rows past the end repeat the last one and are not stored
   const int token = mine / a.group, head = kvh * a.group + mine % a.group;
   const int shift = r.n_k - r.n_q;
@@ -511,7 +524,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
   const int wave_least = seen_by(min(base, rows - 1)), wave_most = seen_by(min(base + 31, rows - 1));
   const int most = __builtin_amdgcn_readfirstlane(seen_by(min((r.index + 1) * BM, rows) - 1));
   // this workgroup's part of the keys, and this wave's first tile
-  int begin = SPLIT ? wave * KEYS : 0, end = most, keys = 0;
+  int begin = SPLIT ? wave * KEYS : half * KEYS, end = most, keys = 0;
   if constexpr (PARTS) {
     const int splits = (int)gridDim.z, index = (int)blockIdx.z;
     keys = max(kPartKeys, ((most + splits - 1) / splits + stride - 1) / stride * stride);
@@ -554,7 +567,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
     for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
   float m = -INFINITY, l = 0.f;
 
-  Loader<DIM, CACHED, SPLIT ? 1 : NW, KEYS> loader;
+  Loader<DIM, CACHED, SPLIT ? 1 : 4, KEYS> loader;
   if (begin < end) {
     loader.init(a, r, kvh, begin, share, lane);
     if constexpr (SPLIT) {
@@ -562,7 +575,7 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
       loader.template load_one<true>(a, r, begin, lds + kTileBytes);
       if constexpr (CACHED) loader.look_up(a, r, begin + stride, share);
     } else {
-      loader.load(a, r, begin, lds, lds + 2 * kTileBytes, share);
+      loader.load(a, r, begin, begin + stride, lds, lds + 2 * kTileBytes, share);
     }
   }
   const auto step = [&](int j0, auto which) __attribute__((always_inline)) {
@@ -573,7 +586,9 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
     } else {
       // this tile has landed, and every wave is done with the other buffer
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      if (more) loader.load(a, r, j0 + stride, lds + (buf ^ 1) * kTileBytes, lds + (2 + (buf ^ 1)) * kTileBytes, share);
+      if (more)
+        loader.load(a, r, j0 + stride, j0 + 2 * stride, lds + (buf ^ 1) * kTileBytes,
+                    lds + (2 + (buf ^ 1)) * kTileBytes, share);
     }
     if (!SPLIT && j0 >= wave_most) return;  // no row of this wave sees the tile
     const char *tile = lds + buf * kTileBytes;
@@ -659,9 +674,10 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
   if constexpr (SPLIT) {
     for (int j0 = begin; j0 < end; j0 += stride) step(j0, std::integral_constant<int, 0>());
   } else {
-    for (int j0 = 0; j0 < most; j0 += 2 * kKeys) {
-      step(j0, std::integral_constant<int, 0>());
-      if (j0 + kKeys < most) step(j0 + kKeys, std::integral_constant<int, 1>());
+    // (with halves both take as many steps, since they meet at each one's barrier)
+    for (int j0 = 0; j0 < most; j0 += 2 * stride) {
+      step(j0 + begin, std::integral_constant<int, 0>());
+      if (j0 + stride < most) step(j0 + stride + begin, std::integral_constant<int, 1>());
     }
   }
 
@@ -681,6 +697,34 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
     join_waves<DT, DIM, CACHED, NW, PARTS>(a, r, kvh, base, rows, wave_least, wave_most, o, m * scale2, l, reinterpret_cast<float *>(all_lds),
                                      part);
     return;
+  }
+  if constexpr (HALVES) {
+    // the second half's sums come to the first, lane for lane
+    __syncthreads();
+    float *const at = reinterpret_cast<float *>(all_lds) + share * (DIM / 2 + 2) * 64;
+    if (half) {
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<f32x4 *>(at + ((4 * db + i / 4) * 64 + lane) * 4) =
+              f32x4{o[db][i], o[db][i + 1], o[db][i + 2], o[db][i + 3]};
+      at[DIM / 2 * 64 + lane] = m * scale2;
+      at[(DIM / 2 + 1) * 64 + lane] = l;
+    }
+    __syncthreads();
+    if (half) return;
+    const float m1 = at[DIM / 2 * 64 + lane], m0 = m * scale2, top = fmaxf(m0, m1);
+    const float k0 = m0 == top ? 1.f : __builtin_amdgcn_exp2f(m0 - top), k1 = m1 == top ? 1.f : __builtin_amdgcn_exp2f(m1 - top);
+    l = l * k0 + at[(DIM / 2 + 1) * 64 + lane] * k1;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const f32x4 x = *reinterpret_cast<const f32x4 *>(at + ((4 * db + i / 4) * 64 + lane) * 4);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[db][i + c] = o[db][i + c] * k0 + x[c] * k1;
+      }
   }
   const bool stored = base + col < rows;
   const float inv = seen > 0 ? 1.f / l : 0.f;
@@ -719,8 +763,7 @@ int64_t row_tiles(int64_t q_tokens, int64_t sequences, int group, int rows) {
 
 template <int DT, int DIM, bool CACHED>
 hipError_t launch_typed(const AttentionArgs &a, int splits, uint32_t *counters, float *sums, hipStream_t st) {
-  constexpr int NW = 4;
-  const int64_t tiles = row_tiles(a.q_tokens, a.sequences, a.group, 32 * NW);
+  const int64_t tiles = row_tiles(a.q_tokens, a.sequences, a.group, 128);
   if (tiles * a.kv_heads <= kFewTiles && (CACHED || a.k_tokens > kKeys)) {
     constexpr int SW = 8;
     const int64_t small = row_tiles(a.q_tokens, a.sequences, a.group, 32);
@@ -734,10 +777,16 @@ hipError_t launch_typed(const AttentionArgs &a, int splits, uint32_t *counters, 
     }
     hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, SW, true, false>), grid, block, 0, st, a, (int)small,
                        counters, sums);
-  } else {
-    hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, NW, false, false>), dim3((unsigned)(tiles * a.kv_heads)),
-                       dim3(64 * NW), 0, st, a, (int)tiles, counters, sums);
+    return hipGetLastError();
   }
+  const dim3 grid((unsigned)(tiles * a.kv_heads));
+  const bool few = row_tiles(a.q_tokens, 0, a.group, 128) * a.kv_heads <= (CACHED || !a.causal ? 1 : 2) * kCus;
+  if (few && (CACHED || a.k_tokens >= a.sequences * kHalvesKeys))
+    hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, 8, false, false>), grid, dim3(512), 0, st, a,
+                       (int)tiles, nullptr, nullptr);
+  else
+    hipLaunchKernelGGL((prompt_attention_kernel<DT, DIM, CACHED, 4, false, false>), grid, dim3(256), 0, st, a,
+                       (int)tiles, nullptr, nullptr);
   return hipGetLastError();
 }
 

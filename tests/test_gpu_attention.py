@@ -66,6 +66,15 @@ def test_prompt_many_row_tiles(dim, dtype, causal):
     run_prompt([150, 200, 3], [333, 70, 3], 56, 8, dim, dtype, causal=causal, seed=12)
 
 
+@pytest.mark.parametrize("dim,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+@pytest.mark.parametrize("q_counts,k_counts,causal", [([800], [800], True), ([769, 900], [769, 900], True),
+                                                      ([600, 65, 1], [640, 1500, 300], True), ([800], [833], False),
+                                                      ([900], [780], True)])
+def test_prompt_keys_in_halves(q_counts, k_counts, causal, dim, dtype):
+    """About one workgroup of 128 rows per CU and long sequences: its waves take the key tiles in two halves."""
+    run_prompt(q_counts, k_counts, 16, 8, dim, dtype, causal=causal, seed=21)
+
+
 @pytest.mark.parametrize("layout", ["fused", "heads_first"])
 def test_prompt_strides_many_row_tiles(layout):
     n, heads, kv_heads, dim, dtype = 340, 64, 16, 64, torch.bfloat16
@@ -155,7 +164,7 @@ def test_prompt_bad_values_reach_the_rows_that_see_them():
     assert not inf.any() and not nan.any()
 
 
-@pytest.mark.parametrize("n,heads,kv_heads", [(300, 4, 1), (300, 64, 16)])
+@pytest.mark.parametrize("n,heads,kv_heads", [(300, 4, 1), (300, 64, 16), (800, 16, 8)])
 def test_prompt_bad_value_beside_and_before_masked_ones(n, heads, kv_heads):
     """Every tile and wave that a bad value can share with rows that may not see it: one at a time, moved along a tile."""
     dtype, dim = torch.bfloat16, 64
@@ -312,6 +321,21 @@ def test_chunk_layers_empty_and_foreign_slots():
         k, v = cached_rows(c, 2, s)
         check_rows(y[a:b], q[a:b], k, v, default_scale(128))
     assert bool((y[93:] == 0).all())  # no keys
+
+
+@pytest.mark.parametrize("dim,page,dtype", [(64, 16, torch.bfloat16), (128, 64, torch.float16), (128, 16, torch.bfloat16)])
+def test_chunk_keys_in_halves(dim, page, dtype):
+    lengths, new = [300, 90, 0, 1217, 64, 1], [200, 90, 3, 64, 30, 1]
+    c = filled_cache(paro, lengths, page, 8, dim, dtype, 4)
+    q = randn((sum(new), 56, dim), dtype, 5, 1.5)
+    y = torch.full_like(q, NAN)
+    slots = torch.arange(len(new), dtype=torch.int32, device="cuda")
+    paro.paro_attention_prompt_cached(c, 0, q, slots, offsets(new), y)
+    at = 0
+    for s, n in enumerate(new):
+        k, v = cached_rows(c, 0, s)
+        check_rows(y[at:at + n], q[at:at + n], k, v, default_scale(dim))
+        at += n
 
 
 def run_split_chunk(lengths, new, heads, kv_heads, dim, page, dtype, causal=True, layers=1, layer=0):
