@@ -60,12 +60,15 @@ typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
 
 constexpr int kKeys = 64;  // keys per tile
 // With at most this many workgroups of 128 rows the keys are split between the
-// waves of smaller ones (see the SPLIT kernel).  Whole and split: 64 rows over
-// 8064 cached keys (24 workgroups) 189 and 50 us, 256 rows over 8256 (72) 195
-// and 62, a prompt of 256 (72) 9.9 and 9.4; a prompt of 512 (136) 14.5 and
-// 18.1, 1024 rows over 9024 (264) 214 and 225.  A prompt of one key tile has
-// nothing to split (17 tokens: 5.8 us, 6.5 split).
-constexpr int kFewTiles = 96;
+// waves of smaller ones (see the SPLIT kernel).  Whole and split, us: 64 rows
+// over 8064 cached keys (24 workgroups) 189 and 50, 256 over 8256 (72) 195 and
+// 62; eight waves in halves (see kHalvesKeys) and split: 500 over 8500 (128) 139
+// and 107, 400 over 1400 (104) 28 and 26, but 600 over 8600 (152) 142 and 155, and 8 x 30
+// over 60 (120) 6.7 and 8.3 (lengths are not known on the host).
+// A causal prompt's rows see half the keys: 256 (72) whole and split 9.9 and
+// 9.4, 512 (136) 14.5 and 16.2.  One of one key tile has nothing to split (17
+// tokens: 5.8 us, 6.5 split).
+constexpr int few_tiles(bool cached) { return cached ? 128 : 96; }
 // With a workspace the parts of few rows' keys fill the 256 CUs once (one
 // workgroup of the SPLIT kernel fits a CU), no part shorter than this: it is
 // two tiles per wave, and joining costs 2 to 3 us (4 rows over 1000 keys, one
@@ -77,9 +80,8 @@ constexpr int64_t kCus = 256;
 // Workgroups of 128 rows have eight waves, in two halves that take the key
 // tiles in turn, where there is about one of them per CU: alone there, four
 // waves wait for their own results most of the time.  Four waves and eight, us:
-// 1024 rows over 9024 cached keys (256 workgroups) 217 and 157, 500 over 8500
-// (120) 201 and 140, 16 x 64 over 4064 (256) 128 and 101, but 1500 over 5500
-// (368) 141 and 155.  A causal prompt's workgroups end at different times, so
+// 1024 rows over 9024 cached keys (256 workgroups) 217 and 157, 16 x 64 over
+// 4064 (256) 128 and 101, but 1500 over 5500 (368) 141 and 155.  A causal prompt's workgroups end at different times, so
 // there up to two per CU: 2048 tokens (512) 49.4 and 47.0, 2 x 1000 34.4 and
 // 30.4, 2 x 2000 with 16 heads over 16 58.5 and 46; 2500 (624) 63 and 70.  Short
 // sequences have no tiles to share: 2 x 700 20.6 and 21.1, 4 x 400 18.3 and 22.9.
@@ -764,7 +766,7 @@ int64_t row_tiles(int64_t q_tokens, int64_t sequences, int group, int rows) {
 template <int DT, int DIM, bool CACHED>
 hipError_t launch_typed(const AttentionArgs &a, int splits, uint32_t *counters, float *sums, hipStream_t st) {
   const int64_t tiles = row_tiles(a.q_tokens, a.sequences, a.group, 128);
-  if (tiles * a.kv_heads <= kFewTiles && (CACHED || a.k_tokens > kKeys)) {
+  if (tiles * a.kv_heads <= few_tiles(CACHED) && (CACHED || a.k_tokens > kKeys)) {
     constexpr int SW = 8;
     const int64_t small = row_tiles(a.q_tokens, a.sequences, a.group, 32);
     const dim3 grid((unsigned)(small * a.kv_heads), 1, (unsigned)splits), block(64 * SW);
@@ -803,7 +805,7 @@ hipError_t launch(const AttentionArgs &a, int splits, uint32_t *counters, float 
 
 int attention_prompt_splits(int64_t q_tokens, int64_t sequences, int q_heads, int kv_heads, int64_t max_len) {
   const int group = q_heads / kv_heads;
-  if (row_tiles(q_tokens, sequences, group, 128) * kv_heads > kFewTiles) return 1;
+  if (row_tiles(q_tokens, sequences, group, 128) * kv_heads > few_tiles(true)) return 1;
   const int64_t items = row_tiles(q_tokens, sequences, group, 32) * kv_heads;
   return (int)std::max<int64_t>(1, std::min(kCus / items, (max_len + kPartKeys - 1) / kPartKeys));
 }

@@ -324,10 +324,12 @@ def test_chunk_layers_empty_and_foreign_slots():
 
 
 @pytest.mark.parametrize("dim,page,dtype", [(64, 16, torch.bfloat16), (128, 64, torch.float16), (128, 16, torch.bfloat16)])
-def test_chunk_keys_in_halves(dim, page, dtype):
-    lengths, new = [300, 90, 0, 1217, 64, 1], [200, 90, 3, 64, 30, 1]
-    c = filled_cache(paro, lengths, page, 8, dim, dtype, 4)
-    q = randn((sum(new), 56, dim), dtype, 5, 1.5)
+@pytest.mark.parametrize("lengths,new,heads,kv_heads", [([300, 90, 0, 1217, 64, 1], [200, 90, 3, 64, 30, 1], 56, 8),
+                                                        ([290, 400, 5], [280, 270, 9], 64, 16)])
+def test_chunk_many_row_tiles(lengths, new, heads, kv_heads, dim, page, dtype):
+    """About one workgroup of 128 rows per CU (eight waves, keys in two halves), and more (four waves)."""
+    c = filled_cache(paro, lengths, page, kv_heads, dim, dtype, 4)
+    q = randn((sum(new), heads, dim), dtype, 5, 1.5)
     y = torch.full_like(q, NAN)
     slots = torch.arange(len(new), dtype=torch.int32, device="cuda")
     paro.paro_attention_prompt_cached(c, 0, q, slots, offsets(new), y)
