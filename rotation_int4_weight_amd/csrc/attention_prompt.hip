@@ -63,11 +63,11 @@ constexpr int kKeys = 64;  // keys per tile
 // waves of smaller ones (see the SPLIT kernel).  Whole and split, us: 64 rows
 // over 8064 cached keys (24 workgroups) 189 and 50, 256 over 8256 (72) 195 and
 // 62; eight waves in halves (see kHalvesKeys) and split: 500 over 8500 (128) 139
-// and 107, 400 over 1400 (104) 28 and 26, but 600 over 8600 (152) 142 and 155, and 8 x 30
-// over 60 (120) 6.7 and 8.3 (lengths are not known on the host).
-// A causal prompt's rows see half the keys: 256 (72) whole and split 9.9 and
-// 9.4, 512 (136) 14.5 and 16.2.  One of one key tile has nothing to split (17
-// tokens: 5.8 us, 6.5 split).
+// and 107, 400 over 1400 (104) 28 and 26, but 600 over 8600 (152) 142 and 155,
+// and 8 x 30 over 60 (120) 6.7 and 8.3 (lengths are not known on the host).  A
+// causal prompt's rows see half the keys: 256 (72) whole and split 9.9 and 9.4,
+// 512 (136) 14.5 and 16.2.  One of one key tile has nothing to split (17 tokens:
+// 5.8 us, 6.5 split).
 constexpr int few_tiles(bool cached) { return cached ? 128 : 96; }
 // With a workspace the parts of few rows' keys fill the 256 CUs once (one
 // workgroup of the SPLIT kernel fits a CU), no part shorter than this: it is
@@ -81,10 +81,11 @@ constexpr int64_t kCus = 256;
 // tiles in turn, where there is about one of them per CU: alone there, four
 // waves wait for their own results most of the time.  Four waves and eight, us:
 // 1024 rows over 9024 cached keys (256 workgroups) 217 and 157, 16 x 64 over
-// 4064 (256) 128 and 101, but 1500 over 5500 (368) 141 and 155.  A causal prompt's workgroups end at different times, so
-// there up to two per CU: 2048 tokens (512) 49.4 and 47.0, 2 x 1000 34.4 and
-// 30.4, 2 x 2000 with 16 heads over 16 58.5 and 46; 2500 (624) 63 and 70.  Short
-// sequences have no tiles to share: 2 x 700 20.6 and 21.1, 4 x 400 18.3 and 22.9.
+// 4064 (256) 128 and 101, but 1500 over 5500 (368) 141 and 155.  A causal
+// prompt's workgroups end at different times, so there up to two per CU: 2048
+// tokens (512) 49.4 and 47.0, 2 x 1000 34.4 and 30.4, 2 x 2000 with 16 heads over
+// 16 58.5 and 46; 2500 (624) 63 and 70.  Short sequences have no tiles to share:
+// 2 x 700 20.6 and 21.1, 4 x 400 18.3 and 22.9.
 constexpr int64_t kHalvesKeys = 768;
 
 template <int DT>
