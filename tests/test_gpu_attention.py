@@ -525,3 +525,43 @@ def test_binding_refuses():
     for bad in (ws[:need - 16], ws.cpu(), ws[::2]):
         with pytest.raises(paro.ParoError):
             paro.paro_attention_prompt_cached(c, 0, q, s[:1], cu, y, workspace=bad)
+
+
+@pytest.mark.parametrize("heads", [(256, 1), (256, 256), (255, 85)])
+def test_most_heads(heads):
+    run_prompt([5, 40], [5, 40], *heads, 64, torch.float16, seed=31)
+    run_decode([70, 3], *heads, 64, 16, torch.bfloat16, seed=32)
+    lengths, new = [90, 20], [3, 20]
+    c = filled_cache(paro, lengths, 16, heads[1], 64, torch.float16, 33)
+    q = randn((sum(new), heads[0], 64), torch.float16, 34)
+    y = torch.full_like(q, NAN)
+    paro.paro_attention_prompt_cached(c, 0, q, torch.arange(2, dtype=torch.int32, device="cuda"), offsets(new), y)
+    for s, (a, b) in enumerate(((0, 3), (3, 23))):
+        check_rows(y[a:b], q[a:b], *cached_rows(c, 0, s), default_scale(64))
+
+
+def test_most_sequences_and_rows():
+    """16384 sequences (one key each: a row's output is its value) and 32768 decode rows over three slots."""
+    n, dt = 16384, torch.bfloat16
+    q, k, v = randn((n, 2, 64), dt, 1), randn((n, 1, 64), dt, 2), randn((n, 1, 64), dt, 3)
+    y = torch.full_like(q, NAN)
+    cu = torch.arange(n + 1, dtype=torch.int64, device="cuda")
+    paro.paro_attention_prompt(q, k, v, cu, cu, y)
+    assert torch.equal(y, v.expand(n, 2, 64))
+    with pytest.raises(paro.ParoError):
+        more = torch.arange(n + 2, dtype=torch.int64, device="cuda").clamp(max=n)
+        paro.paro_attention_prompt(q, k, v, more, more, y)
+    rows = 2 * n
+    c = filled_cache(paro, [33, 1, 100], 16, 1, 64, dt, 4)
+    q = randn((rows, 2, 64), dt, 5)
+    y = torch.full_like(q, NAN)
+    slots = torch.arange(rows, dtype=torch.int32, device="cuda") % 3
+    ws = paro.make_workspace(paro.paro_attention_decode_workspace_bytes(c, rows, 2))
+    paro.paro_attention_decode(c, 0, q, slots, y, ws)
+    assert not torch.isnan(y).any()
+    for r in (0, 1, 2, 12345, 20000, rows - 2, rows - 1):
+        check_rows(y[r:r + 1], q[r:r + 1], *cached_rows(c, 0, r % 3), default_scale(64))
+    assert torch.equal(y[1::3], cached_rows(c, 0, 1)[1].expand(y[1::3].shape[0], 2, 64))
+    with pytest.raises(paro.ParoError):
+        paro.paro_attention_decode(c, 0, q.repeat(2, 1, 1)[:rows + 1], slots.repeat(2)[:rows + 1],
+                                   y.repeat(2, 1, 1)[:rows + 1], ws)
