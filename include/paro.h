@@ -616,13 +616,15 @@ size_t paro_attention_decode_workspace_bytes(const paro_kv_cache *cache, int64_t
  * paro_attention_shape) become the newest positions of slot slots[i], i.e.
  * lengths[slots[i]] - (cu[i+1] - cu[i]) and up, which paro_kv_reserve has
  * granted before.  cu: DEVICE int64 [n + 1], or NULL for one row per entry
- * (tokens == n).  n <= 16384.  Rows whose position or page does not exist
- * are skipped; of entries that name the same slot the first one counts and
- * the others are skipped.  Nothing else of the cache is written.
+ * (tokens == n).  granted: DEVICE int32 [n], what paro_kv_reserve gave for the
+ * same entries, or NULL: an entry with 0 is skipped (its rows would take the
+ * place of older ones).  n <= 16384.  Rows whose position or page does not
+ * exist are skipped; of entries that name the same slot the first one counts
+ * and the others are skipped.  Nothing else of the cache is written.
  */
 int paro_kv_append(const paro_kv_cache *cache, int layer, const void *k, int64_t k_token, int64_t k_head,
                    const void *v, int64_t v_token, int64_t v_head, const int32_t *slots, const int64_t *cu,
-                   int64_t n, int64_t tokens, void *stream);
+                   const int32_t *granted, int64_t n, int64_t tokens, void *stream);
 /*
  * Room for grow[i] >= 0 new positions in slot slots[i], i < n <= 4096
  * (DEVICE int32 arrays): lengths grow, missing pages are taken from the free

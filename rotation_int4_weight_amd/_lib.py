@@ -136,7 +136,7 @@ def load(path: str | None = None):
     lib.paro_attention_decode.argtypes = [P, I32, P, P, P, I64, P, P, SZ, P]
     lib.paro_attention_decode_workspace_bytes.argtypes = [P, I64, I32]
     lib.paro_attention_decode_workspace_bytes.restype = SZ
-    lib.paro_kv_append.argtypes = [P, I32, P, I64, I64, P, I64, I64, P, P, I64, I64, P]
+    lib.paro_kv_append.argtypes = [P, I32, P, I64, I64, P, I64, I64, P, P, P, I64, I64, P]
     lib.paro_kv_reserve.argtypes = [P, P, P, I64, P, P, SZ, P]
     lib.paro_kv_fork.argtypes = [P, P, P, I64, P, P, SZ, P]
     lib.paro_kv_free.argtypes = [P, P, I64, P]
@@ -603,9 +603,10 @@ def paro_attention_decode(cache: KVCache, layer: int, q, slots, y, workspace, sc
                    slots.data_ptr(), n, y.data_ptr(), _ptr(workspace), ws_bytes), what)
 
 
-def paro_kv_append(cache: KVCache, layer: int, k, v, slots, cu=None, stream=None) -> None:
+def paro_kv_append(cache: KVCache, layer: int, k, v, slots, cu=None, stream=None, granted=None) -> None:
     """k, v: (tokens, kv_heads, head_dim) of the cache's dtype become the newest positions of the slots: rows
-    cu[i]..cu[i + 1] of slot slots[i] (int32), one row per slot if cu (int64) is None."""
+    cu[i]..cu[i + 1] of slot slots[i] (int32), one row per slot if cu (int64) is None; granted: paro_kv_reserve's,
+    whose refused entries are then skipped."""
     import torch
     what, dt, dev = "paro_kv_append", cache.dtype, cache.device
     ks, vs = _rows(k, dt, dev, what, "k"), _rows(v, dt, dev, what, "v")
@@ -616,8 +617,10 @@ def paro_kv_append(cache: KVCache, layer: int, k, v, slots, cu=None, stream=None
     n = slots.shape[0]
     if cu is not None:
         _index(cu, torch.int64, n + 1, dev, what, "cu")
+    if granted is not None:
+        _index(granted, torch.int32, n, dev, what, "granted")
     _check(_launch(load().paro_kv_append, dev, stream, cache.ref, layer, k.data_ptr(), ks[0], ks[1], v.data_ptr(),
-                   vs[0], vs[1], slots.data_ptr(), _ptr(cu), n, rows), what)
+                   vs[0], vs[1], slots.data_ptr(), _ptr(cu), _ptr(granted), n, rows), what)
 
 
 def paro_kv_workspace_bytes(cache: KVCache) -> int:

@@ -69,7 +69,7 @@ hipError_t launch_attention_decode(const AttentionArgs &a, const DecodeAttention
 
 hipError_t launch_kv_append(const KvLayer &kv, int kv_heads, int head_dim, const uint16_t *k, int64_t k_token,
                             int64_t k_head, const uint16_t *v, int64_t v_token, int64_t v_head, const int32_t *slots,
-                            const int64_t *cu, int n, int64_t tokens, hipStream_t st);
+                            const int64_t *cu, const int32_t *granted, int n, int64_t tokens, hipStream_t st);
 
 // Page bookkeeping.  work: kv_work_ints(c) int32.
 size_t kv_work_ints(const paro_kv_cache &c);

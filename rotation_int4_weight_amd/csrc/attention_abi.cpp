@@ -377,8 +377,8 @@ int paro_attention_decode(const paro_kv_cache *c, int layer, const paro_attentio
 }
 
 int paro_kv_append(const paro_kv_cache *c, int layer, const void *k, int64_t k_token, int64_t k_head, const void *v,
-                   int64_t v_token, int64_t v_head, const int32_t *slots, const int64_t *cu, int64_t n, int64_t tokens,
-                   void *stream) {
+                   int64_t v_token, int64_t v_head, const int32_t *slots, const int64_t *cu, const int32_t *granted,
+                   int64_t n, int64_t tokens, void *stream) {
   int rc = check_cache(c, true);
   if (!rc) rc = check_layer(c, layer);
   if (!rc) rc = check_rows(n, "n", paro::kMaxSequences);
@@ -393,14 +393,15 @@ int paro_kv_append(const paro_kv_cache *c, int layer, const void *k, int64_t k_t
     return rc;
   if (!k || !v || !slots) return fail(PARO_ERR_NULL, "k, v and slots are required");
   if (!aligned(k, 16) || !aligned(v, 16)) return fail(PARO_ERR_ALIGN, "k and v must be 16-byte aligned");
-  if (!aligned(slots, 4) || !aligned(cu, 8))
-    return fail(PARO_ERR_ALIGN, "slots must be 4-byte aligned, cu 8-byte aligned");
+  if (!aligned(slots, 4) || !aligned(cu, 8) || !aligned(granted, 4))
+    return fail(PARO_ERR_ALIGN, "slots and granted must be 4-byte aligned, cu 8-byte aligned");
   const size_t pb = pool_bytes(c), kb = extent(tokens, c->kv_heads, c->head_dim, k_token, k_head),
                vb = extent(tokens, c->kv_heads, c->head_dim, v_token, v_head);
   if (overlap(k, kb, c->k, pb) || overlap(k, kb, c->v, pb) || overlap(v, vb, c->k, pb) || overlap(v, vb, c->v, pb))
     return fail(PARO_ERR_SHAPE, "k or v overlaps the cache");
   hipError_t e = paro::launch_kv_append(kv_layer(c, layer), c->kv_heads, c->head_dim, (const uint16_t *)k, k_token,
-                                        k_head, (const uint16_t *)v, v_token, v_head, slots, cu, (int)n, tokens,
+                                        k_head, (const uint16_t *)v, v_token, v_head, slots, cu, granted,
+                                        (int)n, tokens,
                                         (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "kv append launch");
   return ok();

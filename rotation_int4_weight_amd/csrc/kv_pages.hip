@@ -382,11 +382,12 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(Pool p, int3
 
 // A wave writes one row of K and of V.  Its sequence is found by a 64-way
 // search of the offsets; a row whose entry is not the first to name its slot,
-// or whose position or page does not exist, is skipped.
+// or was refused its room, or whose position or page does not exist, is skipped.
 __global__ void __launch_bounds__(256) append_kernel(KvLayer kv, int kv_heads, int dim_shift, const uint16_t *__restrict__ k,
                                                      int64_t k_token, int64_t k_head, const uint16_t *__restrict__ v,
                                                      int64_t v_token, int64_t v_head, const int32_t *__restrict__ slots,
-                                                     const int64_t *__restrict__ cu, int n, int64_t tokens) {
+                                                     const int64_t *__restrict__ cu, const int32_t *__restrict__ granted, int n,
+                                                     int64_t tokens) {
   const int64_t row = (int64_t)blockIdx.x * 4 + wave_id();
   if (row >= tokens) return;
   const int lane = lane_id();
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(256) append_kernel(KvLayer kv, int kv_heads, i
     if (row < low || row >= high) return;
   }
   const int s = slots[i];
-  if (s < 0 || s >= kv.slots) return;
+  if (s < 0 || s >= kv.slots || (granted && granted[i] == 0)) return;
   bool earlier = false;
 #pragma unroll 8
   for (int j = lane; j < i; j += 64) earlier |= slots[j] == s;
@@ -509,9 +510,10 @@ hipError_t launch_kv_compact(const paro_kv_cache &c, int32_t *used, int32_t *wor
 
 hipError_t launch_kv_append(const KvLayer &kv, int kv_heads, int head_dim, const uint16_t *k, int64_t k_token,
                             int64_t k_head, const uint16_t *v, int64_t v_token, int64_t v_head, const int32_t *slots,
-                            const int64_t *cu, int n, int64_t tokens, hipStream_t st) {
+                            const int64_t *cu, const int32_t *granted, int n, int64_t tokens, hipStream_t st) {
   hipLaunchKernelGGL(append_kernel, dim3((unsigned)((tokens + 3) / 4)), dim3(256), 0, st, kv, kv_heads,
-                     __builtin_ctz((unsigned)head_dim), k, k_token, k_head, v, v_token, v_head, slots, cu, n, tokens);
+                     __builtin_ctz((unsigned)head_dim), k, k_token, k_head, v, v_token, v_head, slots, cu, granted,
+                     n, tokens);
   return hipGetLastError();
 }
 

@@ -45,9 +45,9 @@ def decode(c=None, layer=0, s=None, q=Q, slots=LIST, rows=0, y=Y, ws=WS, nb=BIG)
                                              rows, y, ws, nb, None)
 
 
-def append(c=None, layer=0, k=K, kt=256, kh=128, v=V, vt=256, vh=128, slots=LIST, cu=CU, n=1, tokens=0):
-    return _lib.load().paro_kv_append(ctypes.byref(c or cache()), layer, k, kt, kh, v, vt, vh, slots, cu, n, tokens,
-                                      None)
+def append(c=None, layer=0, k=K, kt=256, kh=128, v=V, vt=256, vh=128, slots=LIST, cu=CU, granted=None, n=1, tokens=0):
+    return _lib.load().paro_kv_append(ctypes.byref(c or cache()), layer, k, kt, kh, v, vt, vh, slots, cu, granted, n,
+                                      tokens, None)
 
 
 def plan(name, c=None, a=LIST, b=CU, n=1, out=OUT, ws=WS, nb=BIG):
@@ -166,6 +166,7 @@ def test_append_arguments():
         assert append(tokens=2, **{name: None}) == NULL
     assert append(tokens=2, k=K + 8) == ALIGN and append(tokens=2, cu=CU + 4) == ALIGN and append(tokens=2, kt=3) == SHAPE
     assert append(tokens=2, k=A + 64) == SHAPE and append(tokens=2, v=A + STEP + 64) == SHAPE
+    assert append(tokens=1, granted=OUT + 2) == ALIGN
 
 
 def test_bookkeeping_arguments():

@@ -53,7 +53,7 @@ class Block:
         flat = [b[name].view(x.shape[0], -1) for name in "qkv"]
         paro.paro_w4a16_linear_prepared_multi(self.dev[:3], self.hl[:3], x, flat, self.ws)
         paro.paro_kv_reserve(self.cache, slots, grow, b["granted"][:n], self.kv_ws)
-        paro.paro_kv_append(self.cache, self.layer, b["k"], b["v"], slots, cu)
+        paro.paro_kv_append(self.cache, self.layer, b["k"], b["v"], slots, cu, granted=b["granted"][:n])
         if prompt == "packed":
             paro.paro_attention_prompt(b["q"], b["k"], b["v"], cu, cu, b["a"])
         elif prompt == "cached":

@@ -285,6 +285,28 @@ def test_append(page, kv_heads, dim, dtype):
     p.same()
 
 
+def test_append_skips_what_reserve_refused():
+    """Three slots, two of which share a page, and one free page left: the refused entries' rows go nowhere."""
+    c = paro.KVCache.empty(1, 3, 1, 16, 64, 4, 4, torch.float16)
+    ws = torch.empty(paro.paro_kv_workspace_bytes(c), dtype=torch.uint8, device="cuda")
+    got = ints([-1, -1, -1])
+    paro.paro_kv_reserve(c, ints([0, 2]), ints([10, 16]), got[:2], ws)
+    paro.paro_kv_fork(c, ints([0]), ints([1]), got[:1], ws)
+    c.k.normal_()
+    c.v.normal_()
+    k0, v0 = c.k.clone(), c.v.clone()
+    rows = torch.randn((5, 1, 64), device="cuda").half()
+    # slot 2 takes the last free page; slot 0's copy and slot 9 are refused
+    slots, cu = ints([2, 0, 9]), torch.tensor([0, 2, 4, 5], dtype=torch.int64, device="cuda")
+    paro.paro_kv_reserve(c, slots, ints([2, 2, 1]), got, ws)
+    paro.paro_kv_append(c, 0, rows, -rows, slots, cu, granted=got)
+    assert got.tolist() == [1, 0, 0] and c.lengths.tolist() == [10, 10, 18, 0]
+    page = int(c.table[2, 1])
+    assert torch.equal(c.k[0, page, 0, :2], rows[:2, 0]) and torch.equal(c.v[0, page, 0, :2], -rows[:2, 0])
+    k0[0, page, 0, :2], v0[0, page, 0, :2] = rows[:2, 0], -rows[:2, 0]
+    assert torch.equal(c.k, k0) and torch.equal(c.v, v0)
+
+
 @pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 300, 4096])
 def test_append_finds_its_sequence(n):
     """Offsets with many empty sequences: each row lands in its own slot."""
