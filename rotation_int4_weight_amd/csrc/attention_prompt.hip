@@ -195,11 +195,15 @@ __device__ __forceinline__ const uint16_t *v_row(const AttentionArgs &a, const R
 
 // Whether V holds a value that is not finite among the keys that a wave's rows
 // had in their tiles (up to the end of the tile with key most - 1) and that not
-// all of them see (from key least on).
+// all of them see (from key least on).  A tile's rows past the sequence's end
+// are zeros only as far as they lie behind its last row: where packed rows
+// overlap (a token stride under DIM), they hold parts of the last rows, at most
+// DIM / 8 of them, so those are searched too.
 template <int DT, int DIM, bool CACHED>
 __device__ __forceinline__ bool masked_not_finite(const AttentionArgs &a, const Rows &r, int kvh, int least, int most) {
   constexpr uint32_t kInf = DT == kF16 ? 0x7c00u : 0x7f80u;
-  const int end = min(r.n_k, (most + kKeys - 1) / kKeys * kKeys);
+  const int tiles_end = (most + kKeys - 1) / kKeys * kKeys, end = min(r.n_k, tiles_end);
+  if (!CACHED && a.v_token < DIM && tiles_end > r.n_k) least = max(0, min(least, r.n_k - DIM / 8));
   bool bad = false;
   for (int j = least; j < end; ++j) {
     const uint16_t *v = v_row<DIM, CACHED>(a, r, kvh, j);
