@@ -1,7 +1,9 @@
 """Calls at the edges of what the attention entry points allow, on every form
-of the kernels: views whose rows overlap."""
+of the kernels: views whose rows overlap, strides at their limit, scales of
+either sign."""
 import pytest
 
+import _shares as sh
 from _attention import check_rows, default_scale, offsets, randn
 
 torch = pytest.importorskip("torch")
@@ -9,6 +11,7 @@ paro = pytest.importorskip("rotation_int4_weight_amd")
 
 pytestmark = pytest.mark.gpu
 
+TYPES = [torch.float16, torch.bfloat16]
 NAN = float("nan")
 
 # form: (query rows, keys, query heads, key-value heads)
@@ -79,3 +82,61 @@ def test_a_bad_value_in_overlapping_value_rows_stays_in_its_channel(form, dim, s
     assert not torch.isnan(y).any()
     part = slice(max(0, n_q - 70), n_q)
     check_rows(y[part], q[part], k, clean, default_scale(dim), causal)
+
+
+# ---- scales ----
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("form", FORMS)
+def test_negative_scales(form, dim, dtype):
+    n_q, n, heads, kv_heads = FORMS[form]
+    for pattern in ("blocks", "rising", "falling"):
+        lev = sh.levels(n, pattern, n)
+        q = sh.queries(n_q, heads, dim, dtype, "cuda")
+        for p in range(sh.windows(n, dim)):
+            k, v = sh.keys_and_values(lev, kv_heads, dim, p, sign=-1.0, device="cuda")
+            sh.check(attend(form, q, k.to(dtype), v.to(dtype), -sh.LOG2), lev, v)
+
+
+# ---- strides ----
+
+@pytest.mark.parametrize("dim,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+@pytest.mark.parametrize("layout", ["fused", "heads_first", "broadcast"])
+@pytest.mark.parametrize("form", PACKED)
+def test_strided_keys_and_values(form, layout, dim, dtype):
+    n_q, n, heads, kv_heads = PACKED[form]
+    if layout == "fused":
+        rows = torch.zeros((n, heads + 2 * kv_heads, dim), dtype=dtype, device="cuda")
+        q, k, v = rows[:, :heads], rows[:, heads:heads + kv_heads], rows[:, heads + kv_heads:]
+    elif layout == "heads_first":
+        q, k, v = (torch.zeros((h, n, dim), dtype=dtype, device="cuda").transpose(0, 1)
+                   for h in (heads, kv_heads, kv_heads))
+    else:  # one head of keys and values seen as all
+        q = torch.zeros((n, heads, dim), dtype=dtype, device="cuda")
+        k, v = (torch.zeros((n, 1, dim), dtype=dtype, device="cuda") for _ in range(2))
+    q[:, :, 0] = 1.0
+    for pattern in ("blocks", "rising"):
+        lev = sh.levels(n, pattern, n)
+        for p in range(sh.windows(n, dim)):
+            kk, vv = sh.keys_and_values(lev, k.shape[1], dim, p, device="cuda")
+            k.copy_(kk)
+            v.copy_(vv)
+            y = attend(form, q, k.expand(n, kv_heads, dim), v.expand(n, kv_heads, dim), sh.LOG2)
+            sh.check(y, lev, vv.expand(n, kv_heads, dim))
+
+
+@pytest.mark.parametrize("form", PACKED)
+def test_keys_and_values_a_full_stride_apart(form):
+    """The longest token stride, 2^24 elements: a tile's last row lies 2 GB behind its first."""
+    n_q, n, heads, kv_heads = PACKED[form]
+    dim, dtype, token = 64, torch.bfloat16, 1 << 24
+    store = torch.empty((n - 1) * token + 2 * kv_heads * dim, dtype=dtype, device="cuda")
+    k, v = (store[i * kv_heads * dim:].as_strided((n, kv_heads, dim), (token, dim, 1)) for i in (0, 1))
+    lev = sh.levels(n, "blocks", n)
+    q = sh.queries(n_q, heads, dim, dtype, "cuda")
+    for p in range(sh.windows(n, dim)):
+        kk, vv = sh.keys_and_values(lev, kv_heads, dim, p, device="cuda")
+        k.copy_(kk)
+        v.copy_(vv)
+        sh.check(attend(form, q, k, v, sh.LOG2), lev, vv)
