@@ -40,7 +40,6 @@
 // the same time at a lower clock.  With one wave per SIMD a tile takes 3500
 // cycles: scores 1160, weights 940, values 790, the next loads' issue and the
 // barrier 580 (1024 tokens: 25 us so, 22 with two, see kHalvesKeys).
-#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -552,7 +551,8 @@ __global__ void __launch_bounds__(64 * NW, 2) prompt_attention_kernel(AttentionA
       for (int c = 0; c < 4; ++c) q[s][c] ^= flip;
     }
   }
-  const float scale2 = fmaxf(fabsf(a.scale) * 1.44269504088896340736f, FLT_MIN);
+  // not zero (0 times the -infinity of a masked score is NaN), but so small that no finite product matters
+  const float scale2 = fmaxf(fabsf(a.scale) * 1.44269504088896340736f, 0x1p-149f);
 
   // LDS addresses: K fragment s at k_at[s] (+ 32 rows), V^T fragment (db, half) at v_at (+ 16 rows per step)
   uint32_t k_at[KS], v_at[DB][2];

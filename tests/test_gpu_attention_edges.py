@@ -1,6 +1,6 @@
 """Calls at the edges of what the attention entry points allow, on every form
 of the kernels: views whose rows overlap, strides at their limit, scales of
-either sign."""
+either sign and of zero."""
 import pytest
 
 import _shares as sh
@@ -97,6 +97,20 @@ def test_negative_scales(form, dim, dtype):
         for p in range(sh.windows(n, dim)):
             k, v = sh.keys_and_values(lev, kv_heads, dim, p, sign=-1.0, device="cuda")
             sh.check(attend(form, q, k.to(dtype), v.to(dtype), -sh.LOG2), lev, v)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-44, -1e-44])
+@pytest.mark.parametrize("form", FORMS)
+def test_a_scale_of_zero_weighs_all_keys_alike(form, scale):
+    """Products q . k up to 12 * 2^124, whose scaled scores are 0 (or under 2^-17): all keys weigh the same."""
+    n_q, n, heads, kv_heads = FORMS[form]
+    dim, dtype = 64, torch.bfloat16
+    flat = sh.levels(n, "flat")
+    q = sh.queries(n_q, heads, dim, dtype, "cuda")
+    for p in range(sh.windows(n, dim)):
+        k, v = sh.keys_and_values(flat, kv_heads, dim, p, device="cuda")
+        k[:, :, 0] = (sh.levels(n, "blocks", n).float() * 2.0 ** 124).cuda()[:, None]
+        sh.check(attend(form, q, k.to(dtype), v.to(dtype), scale), flat, v)
 
 
 # ---- strides ----
