@@ -519,7 +519,7 @@ size_t paro_mxfp4_linear_prepared_workspace_bytes(const paro_w4_layer *layer, in
 typedef struct {
   int32_t q_heads, kv_heads, head_dim;
   int32_t causal;                 /* 0: every row sees every key of its sequence */
-  float scale;                    /* finite; usually 1 / sqrt(head_dim)          */
+  float scale;                    /* at most 2^127 in size; usually 1 / sqrt(head_dim) */
   int64_t q_token, q_head;        /* strides in elements: row r, head h of q     */
   int64_t k_token, k_head;        /*   starts at q + r * q_token + h * q_head    */
   int64_t v_token, v_head;        /* k and v strides: packed prompts only        */

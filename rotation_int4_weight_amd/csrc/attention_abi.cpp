@@ -110,7 +110,8 @@ int check_heads(const paro_attention_shape *s) {
   if (s->kv_heads < 1 || s->q_heads < 1 || s->q_heads > kMaxHeads || s->q_heads % s->kv_heads)
     return fail(PARO_ERR_SHAPE, "q_heads=%d must be a multiple of kv_heads=%d in 1..%d", s->q_heads, s->kv_heads,
                 kMaxHeads);
-  if (!std::isfinite(s->scale)) return fail(PARO_ERR_SHAPE, "scale must be finite");
+  // the kernels work in base 2: an infinite scale * log2(e) would make NaN of a score of 0
+  if (!(std::fabs(s->scale) <= 0x1p127f)) return fail(PARO_ERR_SHAPE, "scale must be finite and at most 2^127 in size");
   return PARO_OK;
 }
 

@@ -219,3 +219,12 @@ def test_binding_refuses_host_tensors_and_mismatches():
                  lambda: paro.paro_attention_decode(c, 0, q, s, q[:2], ws)):
         with pytest.raises(paro.ParoError):
             call()
+
+
+@pytest.mark.parametrize("scale,status", [(2.0 ** 127, 0), (-2.0 ** 127, 0), (0.0, 0), (2.0 ** 127 * 1.001, SHAPE),
+                                          (-3e38, SHAPE), (float("inf"), SHAPE), (-float("inf"), SHAPE),
+                                          (float("nan"), SHAPE)])
+def test_scales_that_overflow_in_base_two_are_refused(scale, status):
+    """2^127 log2(e) still fits fp32; no call here has rows, so none is launched."""
+    s = shape(scale=scale)
+    assert prompt(s) == status and cached(s=s) == status and decode(s=s) == status
