@@ -511,7 +511,8 @@ size_t paro_mxfp4_linear_prepared_workspace_bytes(const paro_w4_layer *layer, in
  * rounded to the activation dtype for the matrix cores (half a step each;
  * fp16 ones below 2^-21 of the row's largest, 2^-29 in paro_attention_decode,
  * fall into its subnormals), their sum is that of the unrounded ones, and y is
- * rounded once.
+ * rounded once; where that would carry a finite fp16 value past the type it is
+ * the largest finite one.
  * GPU limits: head_dim 64 or 128, q_heads a multiple of kv_heads and at most
  * 256, strides non-negative multiples of 8 elements below 2^40, tensors
  * 16-byte aligned.

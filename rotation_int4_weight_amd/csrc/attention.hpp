@@ -44,6 +44,15 @@ struct AttentionArgs {
   KvLayer kv;            // cache forms
 };
 
+// A finite output stays finite in fp16: rounded weights may carry a sum of
+// values of 65504 past the type by up to 2^-11.  Infinities and NaN stay.
+constexpr float kMaxF16 = 65504.f;
+template <bool FP16>
+__device__ __forceinline__ float within_type(float x) {
+  if constexpr (!FP16) return x;
+  return __builtin_fabsf(x) < __builtin_inff() ? __builtin_amdgcn_fmed3f(x, -kMaxF16, kMaxF16) : x;
+}
+
 // Prompts: K and V packed (cached = false) or in the cache's pages.  Over the
 // cache, few rows may have their keys split over `splits` workgroups (at most
 // attention_prompt_splits; then there are fewer than kDecodeCounters of them).

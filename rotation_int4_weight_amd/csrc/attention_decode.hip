@@ -186,6 +186,14 @@ __device__ __forceinline__ void add_part(f32x4 &o, float &m, float &sum, const f
   m = mn;
 }
 
+// four outputs in the type
+template <int DT>
+__device__ __forceinline__ u32x2 pack_row(const f32x4 &o, float inv) {
+  constexpr bool F = DT == kF16;
+  return u32x2{pack2<DT>(within_type<F>(o[0] * inv), within_type<F>(o[1] * inv)),
+               pack2<DT>(within_type<F>(o[2] * inv), within_type<F>(o[3] * inv))};
+}
+
 template <int DT, int DIM>
 __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs a, DecodeAttentionPlan plan,
                                                                   uint32_t *__restrict__ counters,
@@ -303,7 +311,7 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
     }
     if (parts == 1) {
       const float inv = len > 0 ? 1.f / sum : 0.f;
-      const u32x2 y = {pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
+      const u32x2 y = pack_row<DT>(o, inv);
       *reinterpret_cast<u32x2 *>(a.y + row * a.y_token + (int64_t)(head0 + h) * a.y_head + ch) =
           len > 0 ? y : u32x2{0, 0};
     } else {
@@ -367,7 +375,7 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
     }
     if (h >= heads) continue;
     const float inv = 1.f / sum;
-    const u32x2 y = {pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
+    const u32x2 y = pack_row<DT>(o, inv);
     *reinterpret_cast<u32x2 *>(a.y + row * a.y_token + (int64_t)(head0 + h) * a.y_head + ch) = y;
   }
   if (threadIdx.x == 0) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

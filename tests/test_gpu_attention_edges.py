@@ -1,6 +1,6 @@
 """Calls at the edges of what the attention entry points allow, on every form
 of the kernels: views whose rows overlap, strides at their limit, scales of
-either sign and of zero."""
+either sign and of zero, values at the end of fp16."""
 import pytest
 
 import _shares as sh
@@ -111,6 +111,39 @@ def test_a_scale_of_zero_weighs_all_keys_alike(form, scale):
         k, v = sh.keys_and_values(flat, kv_heads, dim, p, device="cuda")
         k[:, :, 0] = (sh.levels(n, "blocks", n).float() * 2.0 ** 124).cuda()[:, None]
         sh.check(attend(form, q, k.to(dtype), v.to(dtype), scale), flat, v)
+
+
+# ---- values at the end of the type ----
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("form", FORMS)
+def test_largest_fp16_values_do_not_become_infinities(form, dim, sign):
+    """All values are the largest finite one, so y is it too; the weights' rounding may not carry it past the type.
+    One key a little above all others, so that a weight that is not a power of two leads."""
+    n_q, n, heads, kv_heads = FORMS[form]
+    big = torch.finfo(torch.float16).max
+    v = torch.full((n, kv_heads, dim), sign * big, dtype=torch.float16, device="cuda")
+    q = sh.queries(n_q, heads, dim, torch.float16, "cuda")
+    # 6 to 9 powers of two above, different for every row and head
+    q[:, :, 0] = 1.0 + torch.arange(n_q * heads, device="cuda").view(n_q, heads) % 512 / 1024
+    for at in {70, n - 40, n // 2} if n_q < n else {70}:
+        k = torch.zeros((n, kv_heads, dim), dtype=torch.float16, device="cuda")
+        k[at % n, :, 0] = 6.25
+        y = attend(form, q, k, v, sh.LOG2).double()
+        # half a step for the weights, half for y
+        assert bool(((y * sign <= big) & (y * sign >= big * (1 - 2.0 ** -10))).all()), (at, float((y * sign).max()))
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_infinite_fp16_values_stay_infinite(form):
+    n_q, n, heads, kv_heads = FORMS[form]
+    q, k, v = (randn((m, h, 64), torch.float16, i) for i, (m, h) in
+               enumerate(((n_q, heads), (n, kv_heads), (n, kv_heads))))
+    v[0, :, 3], v[0, :, 9] = float("inf"), -float("inf")
+    y = attend(form, q, k, v, 0.01)
+    assert bool((y[:, :, 3] == float("inf")).all()) and bool((y[:, :, 9] == -float("inf")).all())
+    assert int(torch.isinf(y).sum()) == 2 * n_q * heads and not torch.isnan(y).any()
 
 
 # ---- strides ----
