@@ -261,7 +261,10 @@ __device__ __forceinline__ void row_by_wave(const AttentionArgs &a, const Rows &
 // its own loads: for builtin loads the compiler makes every transposing LDS
 // read wait for all that are in flight.  There is no output register, the
 // tile loop waits by itself, and the wait states cover a descriptor or m0
-// written just before.
+// written just before.  m0 is named as written: the compiler keeps its own
+// value there from one builtin load into LDS to the next.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is a reserved register, which it warns of
 __device__ __forceinline__ void load_lds(const uint16_t *base, uint32_t bytes, char *lds, uint32_t off) {
   const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr)lds);
   const uint64_t b = (uint64_t)base;
@@ -269,8 +272,9 @@ __device__ __forceinline__ void load_lds(const uint16_t *base, uint32_t bytes, c
                    (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32) & 0xffffu),
                    (uint32_t)__builtin_amdgcn_readfirstlane(bytes), (uint32_t)kRawBufferWord3};
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(r)
-               : "memory");
+               : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // All but the last n of this wave's vector-memory operations have completed.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
