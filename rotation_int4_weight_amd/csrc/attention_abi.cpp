@@ -165,8 +165,9 @@ int check_cache_and_shape(const paro_kv_cache *c, int layer, const paro_attentio
   return PARO_OK;
 }
 
+// (k and v: where the call has them)
 bool overlaps_cache(const paro_kv_cache *c, const void *p, size_t bytes) {
-  return overlap(p, bytes, c->k, pool_bytes(c)) || overlap(p, bytes, c->v, pool_bytes(c)) ||
+  return (c->k && overlap(p, bytes, c->k, pool_bytes(c))) || (c->v && overlap(p, bytes, c->v, pool_bytes(c))) ||
          overlap(p, bytes, c->table, (size_t)c->slots * c->max_pages * 4) ||
          overlap(p, bytes, c->lengths, (size_t)c->slots * 4) || overlap(p, bytes, c->refs, (size_t)c->num_pages * 4);
 }
@@ -227,9 +228,7 @@ int check_list(const paro_kv_cache *c, const void *p, int64_t n, const void *wor
   if (!p) return fail(PARO_ERR_NULL, "%s is required", what);
   if (!aligned(p, 4)) return fail(PARO_ERR_ALIGN, "%s must be 4-byte aligned", what);
   const size_t b = (size_t)n * 4;
-  if (overlap(p, b, c->refs, (size_t)c->num_pages * 4) || overlap(p, b, c->lengths, (size_t)c->slots * 4) ||
-      overlap(p, b, c->table, (size_t)c->slots * c->max_pages * 4) ||
-      (workspace && overlap(p, b, workspace, paro_kv_workspace_bytes(c))))
+  if (overlaps_cache(c, p, b) || (workspace && overlap(p, b, workspace, paro_kv_workspace_bytes(c))))
     return fail(PARO_ERR_SHAPE, "%s overlaps the cache or the workspace", what);
   return PARO_OK;
 }
@@ -400,6 +399,9 @@ int paro_kv_append(const paro_kv_cache *c, int layer, const void *k, int64_t k_t
                vb = extent(tokens, c->kv_heads, c->head_dim, v_token, v_head);
   if (overlap(k, kb, c->k, pb) || overlap(k, kb, c->v, pb) || overlap(v, vb, c->k, pb) || overlap(v, vb, c->v, pb))
     return fail(PARO_ERR_SHAPE, "k or v overlaps the cache");
+  if (overlaps_cache(c, slots, (size_t)n * 4) || (cu && overlaps_cache(c, cu, (size_t)(n + 1) * 8)) ||
+      (granted && overlaps_cache(c, granted, (size_t)n * 4)))
+    return fail(PARO_ERR_SHAPE, "slots, cu or granted overlaps the cache");
   hipError_t e = paro::launch_kv_append(kv_layer(c, layer), c->kv_heads, c->head_dim, (const uint16_t *)k, k_token,
                                         k_head, (const uint16_t *)v, v_token, v_head, slots, cu, granted,
                                         (int)n, tokens,

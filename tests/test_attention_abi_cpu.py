@@ -228,3 +228,18 @@ def test_scales_that_overflow_in_base_two_are_refused(scale, status):
     """2^127 log2(e) still fits fp32; no call here has rows, so none is launched."""
     s = shape(scale=scale)
     assert prompt(s) == status and cached(s=s) == status and decode(s=s) == status
+
+
+def test_lists_inside_the_cache_are_refused():
+    """Lists that a call would overwrite, or read while it writes them: over K, V or the tables."""
+    inside = (A + 64, A + STEP + 64, A + 2 * STEP, A + 3 * STEP, A + 4 * STEP)
+    for at in inside:
+        for name in ("paro_kv_reserve", "paro_kv_fork"):
+            assert plan(name, a=at) == SHAPE and plan(name, b=at) == SHAPE and plan(name, out=at) == SHAPE
+        assert free(a=at) == SHAPE and compact(used=at) == SHAPE
+        for name in ("slots", "cu", "granted"):
+            assert append(tokens=2, **{name: at}) == SHAPE
+        assert append(cu=None, n=2, tokens=2, slots=at) == SHAPE
+    # a cache without data serves fork and free; its tables are checked all the same
+    bare = cache(k=None, v=None)
+    assert plan("paro_kv_fork", bare, a=A + 3 * STEP) == SHAPE and free(bare, a=A + 2 * STEP) == SHAPE
