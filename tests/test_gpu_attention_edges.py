@@ -187,3 +187,49 @@ def test_keys_and_values_a_full_stride_apart(form):
         k.copy_(kk)
         v.copy_(vv)
         sh.check(attend(form, q, k, v, sh.LOG2), lev, vv)
+
+
+# ---- the largest sizes ----
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_most_packed_rows(dtype):
+    """2^21 query rows in 16384 sequences, 64 heads: q and y have 2^33 elements."""
+    count, n, heads, dim = 16384, 128, 64, 64
+    lev = sh.levels(n, "blocks", 1)
+    k, v = (x.to(dtype).repeat(count, 1, 1) for x in sh.keys_and_values(lev, 1, dim, 0, device="cuda"))
+    v[-n:] *= 0.5  # the last sequence has values of its own
+    q = sh.queries(count * n, heads, dim, dtype, "cuda")
+    y = torch.full_like(q, NAN)
+    cu = torch.arange(count + 1, device="cuda") * n
+    paro.paro_attention_prompt(q, k, v, cu, cu, y, scale=sh.LOG2)
+    for s in (0, 1, 8191, 8192, count - 2, count - 1):
+        sh.check(y[s * n:(s + 1) * n], lev, v[s * n:(s + 1) * n].float())
+    same = y[:-n].view(count - 1, n * heads * dim)
+    for part in same.split(1024):
+        assert torch.equal(part, same[:1].expand(part.shape[0], -1))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_longest_slot(dtype):
+    """2^20 pages of 256 positions (the same four pages again and again), all keys alike: y is the mean of the values,
+    with 2^28 keys and with 77 fewer."""
+    pages, page, dim, heads, kv_heads = 1 << 20, 256, 64, 8, 2
+    c = paro.KVCache.empty(1, 4, kv_heads, page, dim, 1, pages, dtype)
+    c.v.copy_(torch.tensor([1.0, 2.0, 4.0, -3.0]).view(1, 4, 1, 1, 1).expand_as(c.v))
+    c.table[0] = (torch.arange(pages, device="cuda") % 4).int()
+    slots = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dec = paro.make_workspace(paro.paro_attention_decode_workspace_bytes(c, 1, heads))
+    chunk = paro.make_workspace(paro.paro_attention_prompt_cached_workspace_bytes(c, 1, 3, heads))
+    for n in (pages * page, pages * page - 77):
+        c.lengths[0] = n
+        want = 1.0  # (1 + 2 + 4 - 3) / 4; 77 values of -3 fewer change it by under 2^-19
+        for rows in (1, 3):
+            q = randn((rows, heads, dim), dtype, rows)
+            y = torch.full_like(q, NAN)
+            if rows == 1:
+                paro.paro_attention_decode(c, 0, q, slots, y, dec)
+            else:
+                paro.paro_attention_prompt_cached(c, 0, q, slots, offsets([rows]), y, workspace=chunk)
+            # sums of up to 2^20 whole numbers a part, exact, then 2^8 parts; half a step of the type for y
+            off = (y.double() - want).abs()
+            assert float(off.max()) <= sh.HALF_STEP[dtype] + 2.0 ** -12, float(off.max())

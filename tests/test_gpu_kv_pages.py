@@ -375,3 +375,39 @@ def test_offsets_past_32_bits():
         used = ints([0])
         paro.paro_kv_compact(c, used, torch.empty(paro.paro_kv_workspace_bytes(c), dtype=torch.uint8, device="cuda"))
         assert used.tolist() == [1] and int(c.table[0, 0]) == 0
+
+
+def test_most_pages_and_slots():
+    """2^22 pages over 4096 slots: the last free ones are found, and 2048 holes are filled from the end."""
+    pages, slots, width = 1 << 22, 4096, 1024
+    c = paro.KVCache.empty(1, pages, 1, 16, 64, slots, width, torch.float16)
+    index = torch.arange(pages, dtype=torch.int32, device="cuda")
+    for x, salt in ((c.k, 0), (c.v, 1)):  # page p's first four bytes say p
+        x.view(torch.int32)[0, :, 0, 0, 0] = index ^ salt
+    c.table.copy_(index.view(slots, width))
+    c.table[-1, -5:] = -1
+    c.refs.fill_(1)
+    c.refs[-5:] = 0
+    c.lengths.fill_(width * 16)
+    c.lengths[-1] = (width - 5) * 16 - 3
+    ws = torch.empty(paro.paro_kv_workspace_bytes(c), dtype=torch.uint8, device="cuda")
+    got = ints([-1] * 3)
+    paro.paro_kv_reserve(c, ints([0, slots - 1, 5]), ints([1, 3 + 33, 0]), got, ws)  # slot 0 is full
+    assert got.tolist() == [0, 1, 1] and c.table[-1, -6:].tolist() == [pages - 6, pages - 5, pages - 4, pages - 3, -1, -1]
+    assert c.refs[-5:].tolist() == [1, 1, 1, 0, 0]
+    paro.paro_kv_free(c, ints([0, 7, 0]))
+    used = ints([0])
+    paro.paro_kv_compact(c, used, ws)
+    n = pages - 2 - 2 * width
+    assert used.tolist() == [n] and bool((c.refs[:n] == 1).all()) and not c.refs[n:].any()
+    want = index.view(slots, width).clone()
+    want[-1, -2:] = -1
+    holes = torch.cat([torch.arange(width), 7 * width + torch.arange(width)]).int().cuda()
+    moving = want >= n  # in ascending order, as the table is
+    want[moving] = holes
+    want[0] = want[7] = -1
+    assert torch.equal(c.table, want)
+    stamp = index[:n].clone()
+    stamp[holes.long()] = torch.arange(n, n + 2 * width, dtype=torch.int32, device="cuda")
+    for x, salt in ((c.k, 0), (c.v, 1)):
+        assert torch.equal(x.view(torch.int32)[0, :n, 0, 0, 0], stamp ^ salt)
