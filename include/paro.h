@@ -67,6 +67,10 @@
 extern "C" {
 #endif
 
+/* Raised when an entry point or struct that was there changes.  Entry points
+ * may be added without a new number: a library of version 5 may lack
+ * paro_attention_* and paro_kv_*, which a caller can tell by looking the symbol
+ * up (dlsym). */
 #define PARO_ABI_VERSION 5
 
 /* The _RANGE_MIN / _RANGE_MAX members of the two argument enums are not
@@ -512,7 +516,9 @@ size_t paro_mxfp4_linear_prepared_workspace_bytes(const paro_w4_layer *layer, in
  * fp16 ones below 2^-21 of the row's largest, 2^-29 in paro_attention_decode,
  * fall into its subnormals), their sum is that of the unrounded ones, and y is
  * rounded once; where that would carry a finite fp16 value past the type it is
- * the largest finite one.
+ * the largest finite one.  The sums are those of unnormalised weights, up to
+ * 2^8 each: bf16 values times the number of keys have to stay below 2^120, or y
+ * is not finite.
  * GPU limits: head_dim 64 or 128, q_heads a multiple of kv_heads and at most
  * 256, strides non-negative multiples of 8 elements below 2^40, tensors
  * 16-byte aligned.
@@ -630,7 +636,10 @@ int paro_kv_append(const paro_kv_cache *cache, int layer, const void *k, int64_t
  * Room for grow[i] >= 0 new positions in slot slots[i], i < n <= 4096
  * (DEVICE int32 arrays): lengths grow, missing pages are taken from the free
  * ones in ascending order, and a last page that is shared and not full is
- * replaced by a copy of it in all layers (copy on write).
+ * replaced by a copy of it in all layers (copy on write).  Shared means more
+ * than one reference before the call: where all that hold a page grow in one
+ * call, each gets (and needs) a copy, the last one too, and the page is free
+ * afterwards.
  * granted[i] (DEVICE int32 [n], written): 1, or 0 with the slot left as it
  * was: its slot or growth is out of range, it would exceed max_pages, an
  * earlier entry names the same slot, or the pages that it and the entries
