@@ -1,6 +1,7 @@
 """Calls at the edges of what the attention entry points allow, on every form
 of the kernels: views whose rows overlap, strides at their limit, scales of
-either sign and of zero, values at the end of fp16."""
+either sign and of zero, values at the end of fp16, rows of no sequence, the
+largest sizes."""
 import pytest
 
 import _shares as sh
@@ -187,6 +188,36 @@ def test_keys_and_values_a_full_stride_apart(form):
         k.copy_(kk)
         v.copy_(vv)
         sh.check(attend(form, q, k, v, sh.LOG2), lev, vv)
+
+
+# ---- rows of no sequence ----
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("form", [f for f in CACHED if not f.startswith("decode")])
+def test_rows_before_between_and_behind_the_sequences_stay(form, dtype):
+    """Over the cache; the offsets leave out the first five rows and the last nine, and one sequence is empty."""
+    n_q, n, heads, kv_heads = CACHED[form]
+    dim, page, first, behind = 64, 32, 5, 9
+    m = -(-n // page)
+    c = paro.KVCache.empty(1, m, kv_heads, page, dim, 2, m, dtype)
+    lev = sh.levels(n, "blocks", n)
+    k, v = sh.keys_and_values(lev, kv_heads, dim, 0, device="cuda")
+    at = torch.arange(n, device="cuda")
+    c.table[1] = torch.arange(m - 1, -1, -1, device="cuda").int()
+    c.lengths[1] = n
+    where = c.table[1].long()[at // page]
+    c.k[0, where, :, at % page], c.v[0, where, :, at % page] = k.to(dtype), v.to(dtype)
+    rows = first + n_q + behind
+    q = sh.queries(rows, heads, dim, dtype, "cuda")
+    y = torch.full_like(q, 3.0)
+    cu = torch.tensor([first, first, first + n_q], device="cuda")
+    slots = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    need = paro.paro_attention_prompt_cached_workspace_bytes(c, 2, rows, heads)
+    ws = paro.make_workspace(need) if form == "cached parts" else None
+    assert ws is None or need > 0
+    paro.paro_attention_prompt_cached(c, 0, q, slots, cu, y, scale=sh.LOG2, workspace=ws)
+    assert bool((y[:first] == 3).all()) and bool((y[first + n_q:] == 3).all())
+    sh.check(y[first:first + n_q], lev, v)
 
 
 # ---- the largest sizes ----
