@@ -388,7 +388,10 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
 // 512; one row of 32768: 27.2 and 30.4), so the parts fill the 256 CUs once.
 // Between one and two workgroups per CU two parts even out the second round
 // (40 rows of 4096: 124.6 us against 140.3); from two on, whole rows (64 rows
-// of 4096: 187 us, 194 in two parts).
+// of 4096: 187 us, 194 in two parts).  The rule looks at the number of rows, not
+// at their lengths (they are on the device): 63 rows of 500 beside one of 131072
+// take 1360 us, which eight workgroups spend on the long row, 667 MB that the
+// whole card would read in 120; without the long row 23.5 us.
 DecodeAttentionPlan plan_attention_decode(int64_t rows, int q_heads, int kv_heads, int64_t max_len) {
   DecodeAttentionPlan p;
   p.head_tiles = (q_heads / kv_heads + 15) / 16;
