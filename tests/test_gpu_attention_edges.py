@@ -1,7 +1,7 @@
 """Calls at the edges of what the attention entry points allow, on every form
 of the kernels: views whose rows overlap, strides at their limit, scales of
-either sign and of zero, values at the end of fp16, rows of no sequence, the
-largest sizes."""
+either sign and of zero, values at the end of fp16 or not finite, two calls at
+once, rows of no sequence, the largest sizes."""
 import pytest
 
 import _shares as sh
@@ -188,6 +188,63 @@ def test_keys_and_values_a_full_stride_apart(form):
         k.copy_(kk)
         v.copy_(vv)
         sh.check(attend(form, q, k, v, sh.LOG2), lev, vv)
+
+
+# ---- values that are not finite, behind the diagonal ----
+
+@pytest.mark.parametrize("bad", [NAN, float("inf"), "lowest"])
+@pytest.mark.parametrize("form", [f for f in FORMS if not f.startswith("decode")])
+def test_masked_bad_keys_and_values_do_not_reach_a_row(form, bad):
+    """The last third of the query rows has keys and values that are not finite (or the type's lowest): the rows before
+    count their own keys as if there were no others."""
+    n_q, n, heads, kv_heads = FORMS[form]
+    dim, dtype = 64, torch.float16
+    bad = torch.finfo(dtype).min if bad == "lowest" else bad
+    clean = n_q - max(1, n_q // 3)  # rows that see only good keys
+    good = n - n_q + clean
+    lev = sh.levels(good, "blocks", n)
+    q = sh.queries(n_q, heads, dim, dtype, "cuda")
+    for p in range(sh.windows(good, dim)):
+        k, v = (torch.full((n, kv_heads, dim), bad, dtype=dtype, device="cuda") for _ in range(2))
+        kk, vv = sh.keys_and_values(lev, kv_heads, dim, p, device="cuda")
+        k[:good], v[:good] = kk.to(dtype), vv.to(dtype)
+        sh.check(attend(form, q, k, v, sh.LOG2)[:clean], lev, vv)
+
+
+# ---- two at once ----
+
+def test_chunks_in_parts_on_two_streams():
+    """Two calls over one cache at the same time, each with a workspace of its own; the bits are those of single calls."""
+    dim, heads, kv_heads, page, lengths = 128, 8, 2, 16, [3000, 4500]
+    m = [-(-n // page) for n in lengths]
+    c = paro.KVCache.empty(1, sum(m), kv_heads, page, dim, 2, max(m), torch.bfloat16)
+    c.k.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    c.v.normal_(generator=torch.Generator(device="cuda").manual_seed(2))
+    c.table[0, :m[0]] = torch.arange(m[0], device="cuda").int()
+    c.table[1, :m[1]] = torch.arange(m[0], sum(m), device="cuda").int()
+    c.lengths.copy_(torch.tensor(lengths))
+    calls = []
+    for i, rows in enumerate((6, 9)):
+        need = paro.paro_attention_prompt_cached_workspace_bytes(c, 1, rows, heads)
+        assert need > 0
+        q = randn((rows, heads, dim), c.dtype, i)
+        calls.append((torch.cuda.Stream(), q, torch.tensor([i], dtype=torch.int32, device="cuda"), offsets([rows]),
+                      torch.empty_like(q), paro.make_workspace(need)))
+    want = []
+    for _, q, s, cu, y, ws in calls:
+        paro.paro_attention_prompt_cached(c, 0, q, s, cu, y, workspace=ws)
+        torch.cuda.synchronize()
+        want.append(y.clone())
+    for _ in range(10):
+        for call in calls:
+            call[4].fill_(NAN)
+        torch.cuda.synchronize()
+        for st, q, s, cu, y, ws in calls:
+            for _ in range(4):
+                paro.paro_attention_prompt_cached(c, 0, q, s, cu, y, stream=st, workspace=ws)
+        torch.cuda.synchronize()
+        for call, w in zip(calls, want):
+            assert torch.equal(call[4], w)
 
 
 # ---- rows of no sequence ----
