@@ -522,7 +522,8 @@ def bench_mxfp4(args, paro, synth, np, torch, dev):
 
 ATTENTION_METRIC = "Attention between the q/k/v and the output projections: prompt TFLOP/s, decode cache GB/s, % of roofline"
 KERNEL_FILES["attention"] = ("attention_prompt.hip", "attention.hpp", "common.hpp", "mfma.hpp")
-KERNEL_FILES["attention_decode"] = ("attention_decode.hip", "kv_pages.hip", "attention.hpp", "common.hpp", "mfma.hpp")
+KERNEL_FILES["attention_decode"] = ("attention_decode.hip", "kv_pages.hip", "attention.hpp", "attention_join.hpp",
+                                    "kv_rows.hpp", "common.hpp", "mfma.hpp")
 HEAD_DIM = 128  # the Llama-3-8B heads: q_proj has 32 of them, k_proj and v_proj 8
 
 

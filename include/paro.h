@@ -69,8 +69,9 @@ extern "C" {
 
 /* Raised when an entry point or struct that was there changes.  Entry points
  * may be added without a new number: a library of version 5 may lack
- * paro_attention_* and paro_kv_*, which a caller can tell by looking the symbol
- * up (dlsym). */
+ * paro_attention_*, paro_kv_* and paro_rotary*, which a caller can tell by
+ * looking the symbol up (dlsym).  One without paro_kv_read refuses caches in
+ * four bits (PARO_ERR_DTYPE). */
 #define PARO_ABI_VERSION 5
 
 /* The _RANGE_MIN / _RANGE_MAX members of the two argument enums are not
@@ -81,6 +82,8 @@ typedef enum {
   PARO_F16 = 0,  /* IEEE binary16 */
   PARO_BF16 = 1, /* bfloat16      */
   PARO_F32 = 2,  /* IEEE binary32 */
+  PARO_KV4_F16 = 16,  /* paro_kv_cache.dt only: four bits for rows in F16  */
+  PARO_KV4_BF16 = 17, /* paro_kv_cache.dt only: four bits for rows in BF16 */
   PARO_DTYPE_RANGE_MIN = -2147483647 - 1,
   PARO_DTYPE_RANGE_MAX = 2147483647
 } paro_dtype;
@@ -534,6 +537,70 @@ typedef struct {
 } paro_attention_shape;
 
 /*
+ * Rotary positions, between the q/k/v projections and the cache: each head's
+ * first rot_dim channels turn in pairs by angles that grow with the position,
+ *   (y_a, y_b) = magnitude * (x_a cos t - x_b sin t, x_b cos t + x_a sin t),
+ *   t = positions[row] * freqs[i]
+ * for pair i < rot_dim / 2 of channels (a, b) = (i, i + rot_dim / 2), or
+ * (2i, 2i + 1) where `interleaved`; the other channels are copied.  With
+ * `inverse` by -t: the gradient of the loss with respect to x from that with
+ * respect to y (the map is linear, and its transpose turns back).
+ * The angle is taken and brought within one turn in 64 bits (far positions
+ * keep their fraction), sine and cosine are those of a 32-bit number of turns,
+ * products and sums are fp32, and y is rounded once.
+ *   x, y : [tokens][heads][head_dim] dt in {F16, BF16, F32} with the strides of
+ *          `shape`, 16-byte aligned; y may be x with the same strides (in
+ *          place), else they must not overlap.  y's rows and heads must not
+ *          overlap each other.  The q and the k heads of a fused q/k/v buffer
+ *          are one call.
+ *   positions : DEVICE int32 [tokens], any values.
+ *   freqs     : DEVICE double [rot_dim / 2], 8-byte aligned: radians per
+ *               position, for example from paro_rotary_frequencies.
+ * heads 1..256, head_dim a multiple of 8 up to 512, rot_dim even, 2..head_dim,
+ * tokens <= 2^21, strides multiples of 8 elements in 0..2^40.
+ */
+typedef struct {
+  int32_t heads, head_dim, rot_dim;
+  int32_t interleaved, inverse;
+  float magnitude;            /* finite; usually 1 */
+  int64_t x_token, x_head, y_token, y_head;  /* strides in elements */
+} paro_rotary_shape;
+int paro_rotary(const paro_rotary_shape *shape, const void *x, paro_dtype dt, const int32_t *positions,
+                const double *freqs, int64_t tokens, void *y, void *stream);
+/*
+ * The frequencies of a model's positions, on the HOST:
+ *   f_i = base^(-2i / rot_dim), i < rot_dim / 2,
+ * scaled to contexts that are `factor` times the trained `context`:
+ *   NONE   as they are.
+ *   LINEAR f_i / factor.
+ *   BASE   with base * factor^(rot_dim / (rot_dim - 2)) as the base: the
+ *          fastest pair stays, the slowest is divided by factor.
+ *   BANDS  by the turns n_i = context * f_i / (2 pi) over the trained context:
+ *          n_i >= high as they are, n_i <= low divided by factor, between the
+ *          two with the share (n_i - low) / (high - low) of the first.
+ *   RAMP   by the pair's index: kept up to the pair that makes `high` turns
+ *          over the trained context, divided by factor from the one that makes
+ *          `low`, with a linear share between (its ends rounded outwards to
+ *          whole pairs); *magnitude is 0.1 ln(factor) + 1.
+ * magnitude (may be NULL) is 1 but for RAMP.  context is used by BANDS and RAMP,
+ * low and high too (0 < low < high; usually 1 and 4, and 1 and 32).
+ * base > 1, factor >= 1, rot_dim even and in 2..512 (BASE: from 4).
+ * PARO_ERR_NULL, _SHAPE (sizes and numbers), _UNSUPPORTED (kind).
+ */
+typedef enum {
+  PARO_ROTARY_NONE = 0,
+  PARO_ROTARY_LINEAR = 1,
+  PARO_ROTARY_BASE = 2,
+  PARO_ROTARY_BANDS = 3,
+  PARO_ROTARY_RAMP = 4
+} paro_rotary_kind;
+typedef struct {
+  int32_t kind;  /* a paro_rotary_kind */
+  double base, factor, context, low, high;
+} paro_rotary_scaling;
+int paro_rotary_frequencies(const paro_rotary_scaling *scaling, int rot_dim, double *freqs, float *magnitude);
+
+/*
  * A paged key-value cache: host struct of sizes and DEVICE pointers.  Pages
  * hold page_size (16, 32, 64, 128 or 256) positions of one sequence, for all
  * kv_heads and all layers of a model; the same page index serves K, V and
@@ -548,6 +615,28 @@ typedef struct {
  * an invalid state yields wrong numbers, never an out-of-bounds access.
  * Calls on one cache follow each other (stream order, or the caller's
  * events); calls that only read it (the attention ones) may overlap.
+ *
+ * A cache in four bits (dt PARO_KV4_F16 or PARO_KV4_BF16: for rows, queries
+ * and outputs in F16 or BF16) holds each row of a head as 4-bit codes with a
+ * scale and a lowest value for every 64 channels:
+ *   low   = the least of the 64 values x
+ *   scale = (the greatest - low) / 15, rounded to fp32 and then to the row's type
+ *   code  = the whole number nearest to (x - low) / scale (a tie: the even
+ *           one), at most 15; 0 where scale is 0
+ * and stands for low + scale * code.  A group that holds a value that is not
+ * finite is stored as NaN (scale and low).  72 bytes for 128 channels: 9/16 of a
+ * byte per value where the 16-bit cache has 2.  Taken by paro_kv_append (rows
+ * are quantised as they are written), paro_kv_read, paro_attention_decode and
+ * the page calls; paro_attention_prompt_cached refuses it (PARO_ERR_UNSUPPORTED:
+ * read the slots back and call paro_attention_prompt).
+ * Layout: k and v are bytes [layers][num_pages][kv_heads][page_size * head_dim
+ * * 9 / 16].  A page of a head (P positions, D channels) is its codes and then
+ * the pairs {scale, low} [P][D / 64][2] in the rows' type, the codes in the
+ * order in which the matrix cores take them:
+ *   K: [P][4][D / 32] 32-bit words; word (p, g, t) holds channels 32 t + 8 g +
+ *      (0, 2, 4, 6, 1, 3, 5, 7) of position p, lowest bits first (the AWQ order)
+ *   V: [P / 4][16][D / 64][4] 16-bit words; word (j, r, u, i) holds channels
+ *      64 u + 4 r + (0, 1, 2, 3) of position 4 j + i, lowest bits first
  * GPU limits: slots <= 4096, num_pages <= 2^22, max_pages <= 2^20 and
  * max_pages * page_size <= 2^30, layers <= 1024, kv_heads <= 256; k and v
  * 16-byte aligned, refs, table and lengths 4-byte aligned.
@@ -556,8 +645,9 @@ typedef struct {
   int32_t layers, kv_heads, head_dim, page_size;
   int64_t num_pages;
   int32_t slots, max_pages;
-  paro_dtype dt;        /* PARO_F16 or PARO_BF16                              */
-  void *k, *v;          /* [layers][num_pages][kv_heads][page_size][head_dim] */
+  paro_dtype dt;        /* PARO_F16, PARO_BF16, PARO_KV4_F16 or PARO_KV4_BF16 */
+  void *k, *v;          /* [layers][num_pages][kv_heads][page_size][head_dim],
+                           or as above in four bits                           */
   int32_t *refs;        /* [num_pages]                                        */
   int32_t *table;       /* [slots][max_pages]                                 */
   int32_t *lengths;     /* [slots] positions held                             */
@@ -610,6 +700,10 @@ size_t paro_attention_prompt_cached_workspace_bytes(const paro_kv_cache *cache, 
  *   another.  Calls that overlap in time need separate ones.  The split of the length depends on rows, q_heads and the cache's
  *   sizes and on each length alone, and parts are joined in order: a
  *   repeated call gives identical bits.
+ * Over a cache in four bits q and y are in the rows' type; scores are fp32 sums
+ * over codes and pairs, queries are taken as fp16 times a power of two of their
+ * row's (values below 2^-39 of the row's largest are lost), and what is rounded
+ * to fp16, for either type, is the weights times the scales.
  * rows <= 32768.
  */
 int paro_attention_decode(const paro_kv_cache *cache, int layer, const paro_attention_shape *shape, const void *q,
@@ -619,7 +713,7 @@ size_t paro_attention_decode_workspace_bytes(const paro_kv_cache *cache, int64_t
 
 /*
  * New K and V rows into the pages of one layer: rows cu[i]..cu[i+1] of k and
- * v [tokens][kv_heads][head_dim] (cache dtype, strides in elements as in
+ * v [tokens][kv_heads][head_dim] (the rows' dtype: F16 or BF16 after the cache's; strides in elements as in
  * paro_attention_shape) become the newest positions of slot slots[i], i.e.
  * lengths[slots[i]] - (cu[i+1] - cu[i]) and up, which paro_kv_reserve has
  * granted before.  cu: DEVICE int64 [n + 1], or NULL for one row per entry
@@ -632,6 +726,23 @@ size_t paro_attention_decode_workspace_bytes(const paro_kv_cache *cache, int64_t
 int paro_kv_append(const paro_kv_cache *cache, int layer, const void *k, int64_t k_token, int64_t k_head,
                    const void *v, int64_t v_token, int64_t v_head, const int32_t *slots, const int64_t *cu,
                    const int32_t *granted, int64_t n, int64_t tokens, void *stream);
+/*
+ * Rows of one layer out of the pages: rows cu[i]..cu[i+1] of k and v [tokens]
+ * [kv_heads][head_dim] (out_dt: the rows' type, F16 or BF16 after the cache's
+ * dt, or F32; strides in elements) are set to positions first[i] and up of slot
+ * slots[i].  first: DEVICE int32 [n], or NULL for the newest positions, as
+ * paro_kv_append has them.  cu: DEVICE int64 [n + 1], or NULL for one row per
+ * entry (tokens == n); entries are clamped as there.  n <= 16384.  From a cache
+ * in 16 bits the values are copied, from one in four bits they are those that
+ * the codes stand for, low + scale * code rounded to fp32 and then to out_dt.
+ * Rows whose position the slot does not hold (or that it has no valid page for)
+ * are set to zero; rows outside every entry are left as they were.  k and v
+ * must overlap neither each other, the cache nor the lists, and their rows and
+ * heads not one another.  k or v may be NULL (not written).
+ */
+int paro_kv_read(const paro_kv_cache *cache, int layer, void *k, int64_t k_token, int64_t k_head, void *v,
+                 int64_t v_token, int64_t v_head, paro_dtype out_dt, const int32_t *slots, const int64_t *cu,
+                 const int32_t *first, int64_t n, int64_t tokens, void *stream);
 /*
  * Room for grow[i] >= 0 new positions in slot slots[i], i < n <= 4096
  * (DEVICE int32 arrays): lengths grow, missing pages are taken from the free

@@ -26,7 +26,8 @@ from ._lib import (BF16, EXPORTS, F16, F32, PATH_AUTO, PATH_DECODE_FUSED, PATH_D
                    KVCache, paro_attention_prompt, paro_attention_prompt_cached,
                    paro_attention_prompt_cached_workspace_bytes, paro_attention_decode,
                    paro_attention_decode_workspace_bytes, paro_kv_append, paro_kv_reserve, paro_kv_fork,
-                   paro_kv_free, paro_kv_compact, paro_kv_workspace_bytes)
+                   paro_kv_free, paro_kv_compact, paro_kv_workspace_bytes, KV4_BF16, KV4_F16, paro_kv_read,
+                   paro_rotary, paro_rotary_frequencies)
 
 __all__ = ["BF16", "EXPORTS", "F16", "F32", "PATH_AUTO", "PATH_DECODE_FUSED", "PATH_DECODE_SPLIT",
            "PATH_PREFILL", "DeviceLayer", "ParoError", "load", "make_workspace", "paro_abi_version",
@@ -46,4 +47,5 @@ __all__ = ["BF16", "EXPORTS", "F16", "F32", "PATH_AUTO", "PATH_DECODE_FUSED", "P
            "KVCache", "paro_attention_prompt", "paro_attention_prompt_cached",
            "paro_attention_prompt_cached_workspace_bytes", "paro_attention_decode",
            "paro_attention_decode_workspace_bytes", "paro_kv_append", "paro_kv_reserve", "paro_kv_fork",
-           "paro_kv_free", "paro_kv_compact", "paro_kv_workspace_bytes"]
+           "paro_kv_free", "paro_kv_compact", "paro_kv_workspace_bytes", "KV4_BF16", "KV4_F16", "paro_kv_read",
+           "paro_rotary", "paro_rotary_frequencies"]

@@ -16,6 +16,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("PARO_LIB") or os.path.join(PKG, "libparo.so")
 
 F16, BF16, F32 = 0, 1, 2
+KV4_F16, KV4_BF16 = 16, 17  # caches in four bits, for rows in fp16 or bf16
 PATH_AUTO, PATH_DECODE_FUSED, PATH_DECODE_SPLIT, PATH_PREFILL = 0, 1, 2, 3
 STATUS = {0: "PARO_OK", 1: "PARO_ERR_NULL", 2: "PARO_ERR_SHAPE", 3: "PARO_ERR_DTYPE",
           4: "PARO_ERR_ALIGN", 5: "PARO_ERR_UNSUPPORTED", 6: "PARO_ERR_PAIRS",
@@ -38,8 +39,8 @@ EXPORTS = ("paro_scale_rotate", "paro_w4_unpack_dequant", "paro_w4a16_linear",
            "paro_w4a16_linear_choose_path", "paro_validate_layer", "paro_last_error",
            "paro_abi_version", "paro_attention_prompt", "paro_attention_prompt_cached",
            "paro_attention_prompt_cached_workspace_bytes", "paro_attention_decode", "paro_attention_decode_workspace_bytes", "paro_kv_append",
-           "paro_kv_reserve", "paro_kv_fork", "paro_kv_free", "paro_kv_compact",
-           "paro_kv_workspace_bytes")
+           "paro_kv_read", "paro_kv_reserve", "paro_kv_fork", "paro_kv_free", "paro_kv_compact",
+           "paro_kv_workspace_bytes", "paro_rotary", "paro_rotary_frequencies")
 
 
 class ParoError(RuntimeError):
@@ -72,6 +73,18 @@ class ParoKvCacheC(ctypes.Structure):
                 ("max_pages", ctypes.c_int32), ("dt", ctypes.c_int), ("k", ctypes.c_void_p),
                 ("v", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("table", ctypes.c_void_p),
                 ("lengths", ctypes.c_void_p)]
+
+
+class ParoRotaryShapeC(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("y_token", ctypes.c_int64), ("y_head", ctypes.c_int64)]
+
+
+class ParoRotaryScalingC(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("context", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double)]
 
 
 _lib = None
@@ -137,6 +150,9 @@ def load(path: str | None = None):
     lib.paro_attention_decode_workspace_bytes.argtypes = [P, I64, I32]
     lib.paro_attention_decode_workspace_bytes.restype = SZ
     lib.paro_kv_append.argtypes = [P, I32, P, I64, I64, P, I64, I64, P, P, P, I64, I64, P]
+    lib.paro_kv_read.argtypes = [P, I32, P, I64, I64, P, I64, I64, I32, P, P, P, I64, I64, P]
+    lib.paro_rotary.argtypes = [P, P, I32, P, P, I64, P, P]
+    lib.paro_rotary_frequencies.argtypes = [P, I32, P, P]
     lib.paro_kv_reserve.argtypes = [P, P, P, I64, P, P, SZ, P]
     lib.paro_kv_fork.argtypes = [P, P, P, I64, P, P, SZ, P]
     lib.paro_kv_free.argtypes = [P, P, I64, P]
@@ -156,7 +172,8 @@ def load(path: str | None = None):
                  "paro_w4a16_linear_choose_path",
                  "paro_validate_layer", "paro_abi_version", "paro_attention_prompt",
                  "paro_attention_prompt_cached", "paro_attention_decode", "paro_kv_append", "paro_kv_reserve",
-                 "paro_kv_fork", "paro_kv_free", "paro_kv_compact"):
+                 "paro_kv_fork", "paro_kv_free", "paro_kv_compact", "paro_kv_read", "paro_rotary",
+                 "paro_rotary_frequencies"):
         getattr(lib, name).restype = I32
     if path == LIB_PATH:
         _lib = lib
@@ -463,13 +480,18 @@ class KVCache:
 
     k, v: (layers, pages, kv_heads, page_size, head_dim) fp16/bf16; refs: (pages,), table: (slots, max_pages),
     lengths: (slots,), int32; contiguous, on one device.  KVCache.empty() makes them.
+    In four bits k and v are uint8 of (layers, pages, kv_heads, page_size, 9 * head_dim // 16), the bytes of each
+    head's page (include/paro.h gives their order), and dtype, fp16 or bf16, is that of the rows, queries and outputs.
     """
 
-    def __init__(self, k, v, refs, table, lengths):
+    def __init__(self, k, v, refs, table, lengths, dtype=None):
         import torch
         what = "KVCache"
         _need(k.dim() == 5 and v.shape == k.shape, 2, what, "k and v: (layers, pages, kv_heads, page_size, head_dim)")
-        _need(k.dtype in (torch.float16, torch.bfloat16) and v.dtype == k.dtype, 3, what, "k and v: fp16 or bf16")
+        four = k.dtype == torch.uint8
+        dtype = k.dtype if dtype is None else dtype
+        _need(dtype in (torch.float16, torch.bfloat16) and v.dtype == k.dtype and (four or k.dtype == dtype), 3, what,
+              "k and v: fp16 or bf16, or uint8 with dtype fp16 or bf16")
         _need(refs.shape == (k.shape[1],) and table.dim() == 2 and lengths.shape == (table.shape[0],), 2, what,
               "refs (pages,), table (slots, max_pages), lengths (slots,)")
         _need(all(t.dtype == torch.int32 for t in (refs, table, lengths)), 3, what, "refs, table and lengths: int32")
@@ -477,20 +499,28 @@ class KVCache:
               "contiguous tensors on one device")
         self.k, self.v, self.refs, self.table, self.lengths = k, v, refs, table, lengths
         layers, pages, kv_heads, page_size, head_dim = k.shape
-        self.c = ParoKvCacheC(layers, kv_heads, head_dim, page_size, pages, table.shape[0], table.shape[1], _dt(k),
-                              k.data_ptr(), v.data_ptr(), refs.data_ptr(), table.data_ptr(), lengths.data_ptr())
+        if four:
+            _need(head_dim in (36, 72), 2, what, "four bits: 36 bytes for 64 channels or 72 for 128")
+            head_dim = head_dim * 16 // 9
+        self.dtype, self.device, self.bits = dtype, k.device, 4 if four else 16
+        dt = F16 if dtype == torch.float16 else BF16
+        self.c = ParoKvCacheC(layers, kv_heads, head_dim, page_size, pages, table.shape[0], table.shape[1],
+                              KV4_F16 + dt if four else dt, k.data_ptr(), v.data_ptr(), refs.data_ptr(),
+                              table.data_ptr(), lengths.data_ptr())
         self.ref = ctypes.byref(self.c)
-        self.dtype, self.device = k.dtype, k.device
 
     @classmethod
-    def empty(cls, layers, pages, kv_heads, page_size, head_dim, slots, max_pages, dtype, device="cuda"):
-        """A cache with all slots empty and all pages free."""
+    def empty(cls, layers, pages, kv_heads, page_size, head_dim, slots, max_pages, dtype, device="cuda", bits=16):
+        """A cache with all slots empty and all pages free; bits: 16, or 4 for rows of dtype held in four bits."""
         import torch
-        shape = (layers, pages, kv_heads, page_size, head_dim)
-        return cls(torch.zeros(shape, dtype=dtype, device=device), torch.zeros(shape, dtype=dtype, device=device),
+        _need(bits in (4, 16), 5, "KVCache.empty", "bits: 4 or 16")
+        _need(bits == 16 or head_dim in (64, 128), 5, "KVCache.empty", "four bits: heads of 64 or 128 channels")
+        shape = (layers, pages, kv_heads, page_size, head_dim if bits == 16 else head_dim * 9 // 16)
+        held = dtype if bits == 16 else torch.uint8
+        return cls(torch.zeros(shape, dtype=held, device=device), torch.zeros(shape, dtype=held, device=device),
                    torch.zeros(pages, dtype=torch.int32, device=device),
                    torch.full((slots, max_pages), -1, dtype=torch.int32, device=device),
-                   torch.zeros(slots, dtype=torch.int32, device=device))
+                   torch.zeros(slots, dtype=torch.int32, device=device), dtype=dtype)
 
 
 def _need(good, status: int, what: str, msg: str):
@@ -623,6 +653,29 @@ def paro_kv_append(cache: KVCache, layer: int, k, v, slots, cu=None, stream=None
                    vs[0], vs[1], slots.data_ptr(), _ptr(cu), _ptr(granted), n, rows), what)
 
 
+def paro_kv_read(cache: KVCache, layer: int, k, v, slots, cu=None, first=None, stream=None) -> None:
+    """k, v: (tokens, kv_heads, head_dim) of the cache's dtype or fp32 (either may be None) are set to what the slots
+    hold: rows cu[i]..cu[i + 1] (one row per slot if cu is None) to positions first[i] and up (int32 (n,)), or to the
+    newest ones if first is None; rows beyond what a slot holds are zero."""
+    import torch
+    what, dev = "paro_kv_read", cache.device
+    outs = [t for t in (k, v) if t is not None]
+    _need(outs, 1, what, "k or v is required")
+    out, shape = outs[0].dtype, outs[0].shape
+    _need(out in (cache.dtype, torch.float32), 3, what, f"k and v: {cache.dtype} or fp32")
+    ks, vs = (_rows(t, out, dev, what, name) if t is not None else (0, 0) for t, name in ((k, "k"), (v, "v")))
+    if any(t.shape != shape for t in outs) or shape[1:] != (cache.c.kv_heads, cache.c.head_dim):
+        raise ParoError(2, what, f"k and v: (tokens, {cache.c.kv_heads}, {cache.c.head_dim})")
+    _index(slots, torch.int32, None, dev, what, "slots")
+    n = slots.shape[0]
+    if cu is not None:
+        _index(cu, torch.int64, n + 1, dev, what, "cu")
+    if first is not None:
+        _index(first, torch.int32, n, dev, what, "first")
+    _check(_launch(load().paro_kv_read, dev, stream, cache.ref, layer, _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1],
+                   _dt(outs[0]), slots.data_ptr(), _ptr(cu), _ptr(first), n, shape[0]), what)
+
+
 def paro_kv_workspace_bytes(cache: KVCache) -> int:
     """Workspace bytes of paro_kv_reserve, paro_kv_fork and paro_kv_compact."""
     return int(load().paro_kv_workspace_bytes(cache.ref))
@@ -665,3 +718,42 @@ def paro_kv_compact(cache: KVCache, used, workspace, stream=None) -> None:
     _index(used, torch.int32, 1, dev, what, "used")
     _check(_launch(load().paro_kv_compact, dev, stream, cache.ref, used.data_ptr(), _ptr(workspace),
                    _scratch(workspace, dev, what)), what)
+
+
+# ---- rotary positions ----
+
+ROTARY = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
+
+
+def paro_rotary_frequencies(rot_dim: int, base: float = 10000.0, kind: str = "none", factor: float = 1.0,
+                            context: float = 0.0, low: float | None = None, high: float | None = None, device="cuda"):
+    """(freqs, magnitude): the angle per position of each pair of channels, float64 (rot_dim // 2,) on `device`, and
+    what multiplies cosine and sine.  kind: "none", "linear", "base", "bands" or "ramp" (include/paro.h gives their
+    formulas), stretching a trained `context` by `factor`; low, high: 1 and 4 ("bands") or 1 and 32 ("ramp") if None."""
+    import torch
+    what = "paro_rotary_frequencies"
+    _need(kind in ROTARY, 5, what, f"kind: one of {', '.join(ROTARY)}")
+    s = ParoRotaryScalingC(ROTARY[kind], base, factor, context, 1.0 if low is None else low,
+                           (32.0 if kind == "ramp" else 4.0) if high is None else high)
+    out, magnitude = (ctypes.c_double * max(1, rot_dim // 2))(), ctypes.c_float()
+    _check(load().paro_rotary_frequencies(ctypes.byref(s), rot_dim, out, ctypes.byref(magnitude)), what)
+    return torch.tensor(list(out), dtype=torch.float64, device=device), magnitude.value
+
+
+def paro_rotary(x, positions, freqs, y, interleaved: bool = False, inverse: bool = False, magnitude: float = 1.0,
+                stream=None) -> None:
+    """x, y: (tokens, heads, head_dim) fp16/bf16/fp32 views, y may be x; positions: int32 (tokens,); freqs: float64
+    (rot_dim // 2,), radians per position: channel pairs (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved, turn by
+    positions * freqs (inverse: back, which is the gradient), the channels from rot_dim on are copied."""
+    import torch
+    what, dt, dev = "paro_rotary", x.dtype, x.device
+    xs, ys = _rows(x, dt, dev, what, "x"), _rows(y, dt, dev, what, "y")
+    _need(dt in (torch.float16, torch.bfloat16, torch.float32), 3, what, "fp16, bf16 or fp32")
+    _need(y.shape == x.shape, 2, what, "y like x")
+    tokens, heads, d = x.shape
+    _index(positions, torch.int32, tokens, dev, what, "positions")
+    _index(freqs, torch.float64, None, dev, what, "freqs")
+    s = ParoRotaryShapeC(heads, d, 2 * freqs.shape[0], bool(interleaved), bool(inverse), magnitude, xs[0], xs[1],
+                         ys[0], ys[1])
+    _check(_launch(load().paro_rotary, dev, stream, ctypes.byref(s), x.data_ptr(), _dt(x), positions.data_ptr(),
+                   freqs.data_ptr(), tokens, y.data_ptr()), what)

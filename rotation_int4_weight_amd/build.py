@@ -23,7 +23,8 @@ LIB = os.path.join(PKG, "libparo.so")
 ARCH = "gfx950"
 
 SOURCES = ["paro_abi.cpp", "scale_rotate.hip", "unpack_dequant.hip", "decode.hip", "prefill.hip", "quantize.hip", "rotate_backward.hip", "mxfp4.hip", "noalloc.hip",
-           "attention_abi.cpp", "attention_prompt.hip", "attention_decode.hip", "kv_pages.hip"]
+           "attention_abi.cpp", "attention_prompt.hip", "attention_decode.hip", "attention_decode4.hip",
+           "kv_pages.hip", "kv4_rows.hip", "rotary_abi.cpp", "rotary.hip"]
 
 # Packed-FP32 instructions are switched off for all device code: hipcc would
 # otherwise form v_pk_{add,mul,fma}_f32 from scalar float code.

@@ -14,12 +14,24 @@ constexpr int kMaxSlots = 4096;      // the planning kernels keep per-slot table
 constexpr int kMaxSequences = 16384;  // with 256 heads and the most rows, under 2^32 threads a launch
 constexpr int kMaxDecodeRows = 32768;  // a grid dimension
 
+// Caches in four bits (include/paro.h gives the layout): 64 channels share a
+// scale and a lowest value.
+constexpr int kKv4Group = 64;
+inline bool kv4(int dt) { return dt == PARO_KV4_F16 || dt == PARO_KV4_BF16; }
+// the type of the rows, queries and outputs of a cache
+inline int kv_row_dtype(int dt) { return dt == PARO_KV4_F16 ? PARO_F16 : dt == PARO_KV4_BF16 ? PARO_BF16 : dt; }
+// 16-bit units of a page of K (or V) of one layer: elements, or codes and pairs
+inline int64_t kv_page_units(const paro_kv_cache &c) {
+  const int64_t n = (int64_t)c.kv_heads * c.page_size * c.head_dim;
+  return kv4(c.dt) ? n * 9 / 32 : n;
+}
+
 // One layer of a paged cache as the kernels see it.
 struct KvLayer {
-  uint16_t *k, *v;         // the layer's pages [num_pages][kv_heads][page_size][head_dim]
+  uint16_t *k, *v;         // the layer's pages [num_pages][kv_heads][page_size][head_dim], or in four bits
   const int32_t *table;    // [slots][max_pages]
   const int32_t *lengths;  // [slots]
-  int64_t page_stride;     // elements per page: kv_heads * page_size * head_dim
+  int64_t page_stride;     // 16-bit units per page (kv_page_units)
   int num_pages, max_pages, slots;
   int page_shift;          // log2(page_size)
   // positions that a slot holds (0 for one outside the cache)
@@ -76,9 +88,32 @@ size_t attention_decode_partial_bytes(const DecodeAttentionPlan &p, int64_t rows
 hipError_t launch_attention_decode(const AttentionArgs &a, const DecodeAttentionPlan &p, uint32_t *counters,
                                    float *partials, hipStream_t st);
 
+// The same over a cache in four bits (the plan and the workspace are the same).
+hipError_t launch_attention_decode4(const AttentionArgs &a, const DecodeAttentionPlan &p, uint32_t *counters,
+                                    float *partials, hipStream_t st);
+
 hipError_t launch_kv_append(const KvLayer &kv, int kv_heads, int head_dim, const uint16_t *k, int64_t k_token,
                             int64_t k_head, const uint16_t *v, int64_t v_token, int64_t v_head, const int32_t *slots,
                             const int64_t *cu, const int32_t *granted, int n, int64_t tokens, hipStream_t st);
+
+// The same into a cache in four bits; dt: the rows' type.
+hipError_t launch_kv_append4(const KvLayer &kv, int kv_heads, int head_dim, int dt, const uint16_t *k,
+                             int64_t k_token, int64_t k_head, const uint16_t *v, int64_t v_token, int64_t v_head,
+                             const int32_t *slots, const int64_t *cu, const int32_t *granted, int n, int64_t tokens,
+                             hipStream_t st);
+// Rows out of the pages; k or v may be null.  four: the cache is in four bits.
+struct KvReadArgs {
+  KvLayer kv;
+  int kv_heads, head_dim, dt, out_dt;  // dt: the rows' type; out_dt: dt or kF32
+  bool four;
+  void *k, *v;
+  int64_t k_token, k_head, v_token, v_head;  // elements
+  const int32_t *slots, *first;              // first may be null
+  const int64_t *cu;                         // may be null
+  int n;
+  int64_t tokens;
+};
+hipError_t launch_kv_read(const KvReadArgs &a, hipStream_t st);
 
 // Page bookkeeping.  work: kv_work_ints(c) int32.
 size_t kv_work_ints(const paro_kv_cache &c);

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include "abi.hpp"
 #include "attention.hpp"
@@ -44,8 +45,10 @@ int check_head_dim(int d) {
 
 int32_t *kv_work(void *workspace) { return (int32_t *)((char *)workspace + kCounterBytes); }
 
-int64_t page_elements(const paro_kv_cache *c) { return (int64_t)c->kv_heads * c->page_size * c->head_dim; }
-size_t pool_bytes(const paro_kv_cache *c) { return (size_t)c->layers * c->num_pages * page_elements(c) * 2; }
+size_t pool_bytes(const paro_kv_cache *c) {
+  return (size_t)c->layers * c->num_pages * paro::kv_page_units(*c) * 2;
+}
+paro_dtype row_dtype(const paro_kv_cache *c) { return (paro_dtype)paro::kv_row_dtype(c->dt); }
 
 // Sizes and tables; `data`: K and V are needed too.
 int check_cache(const paro_kv_cache *c, bool data) {
@@ -65,7 +68,8 @@ int check_cache(const paro_kv_cache *c, bool data) {
   if (c->max_pages < 1 || c->max_pages > kMaxTable || (int64_t)c->max_pages * c->page_size > kMaxLength)
     return fail(PARO_ERR_SHAPE, "max_pages=%d must be in 1..%lld and max_pages * page_size at most %lld", c->max_pages,
                 (long long)kMaxTable, (long long)kMaxLength);
-  if (!act_dtype(c->dt)) return fail(PARO_ERR_DTYPE, "cache dtype %d must be F16 or BF16", (int)c->dt);
+  if (!act_dtype(c->dt) && !paro::kv4(c->dt))
+    return fail(PARO_ERR_DTYPE, "cache dtype %d must be F16, BF16, KV4_F16 or KV4_BF16", (int)c->dt);
   if (!c->refs || !c->table || !c->lengths) return fail(PARO_ERR_NULL, "refs, table and lengths are required");
   if (!aligned(c->refs, 4) || !aligned(c->table, 4) || !aligned(c->lengths, 4))
     return fail(PARO_ERR_ALIGN, "refs, table and lengths must be 4-byte aligned");
@@ -90,12 +94,12 @@ int check_layer(const paro_kv_cache *c, int layer) {
 
 paro::KvLayer kv_layer(const paro_kv_cache *c, int layer) {
   paro::KvLayer kv;
-  const int64_t at = (int64_t)layer * c->num_pages * page_elements(c);
+  const int64_t at = (int64_t)layer * c->num_pages * paro::kv_page_units(*c);
   kv.k = (uint16_t *)c->k + at;
   kv.v = (uint16_t *)c->v + at;
   kv.table = c->table;
   kv.lengths = c->lengths;
-  kv.page_stride = page_elements(c);
+  kv.page_stride = paro::kv_page_units(*c);
   kv.num_pages = (int)c->num_pages;
   kv.max_pages = c->max_pages;
   kv.slots = c->slots;
@@ -122,20 +126,17 @@ int check_stride(int64_t s, const char *what) {
 }
 
 // Bytes from the first to past the last element of a strided tensor.
-size_t extent(int64_t rows, int heads, int dim, int64_t token, int64_t head) {
-  return rows <= 0 ? 0 : (size_t)((rows - 1) * token + (heads - 1) * head + dim) * 2;
+size_t extent(int64_t rows, int heads, int dim, int64_t token, int64_t head, size_t size = 2) {
+  return rows <= 0 ? 0 : (size_t)((rows - 1) * token + (heads - 1) * head + dim) * size;
 }
 
-// y's rows and heads lie apart from each other.
-int check_output_strides(const paro_attention_shape *s, int64_t rows) {
-  const int64_t d = s->head_dim;
-  const bool heads_inside = (s->q_heads == 1 || s->y_head >= d) &&
-                            (rows <= 1 || s->y_token >= (s->q_heads - 1) * s->y_head + d);
-  const bool rows_inside = (rows <= 1 || s->y_token >= d) &&
-                           (s->q_heads == 1 || s->y_head >= (rows - 1) * s->y_token + d);
+// An output's rows and heads lie apart from each other.
+int check_output_strides(const char *what, int heads, int64_t d, int64_t rows, int64_t token, int64_t head) {
+  const bool heads_inside = (heads == 1 || head >= d) && (rows <= 1 || token >= (heads - 1) * head + d);
+  const bool rows_inside = (rows <= 1 || token >= d) && (heads == 1 || head >= (rows - 1) * token + d);
   if (!heads_inside && !rows_inside)
-    return fail(PARO_ERR_SHAPE, "y strides (token %lld, head %lld) make rows or heads overlap", (long long)s->y_token,
-                (long long)s->y_head);
+    return fail(PARO_ERR_SHAPE, "%s strides (token %lld, head %lld) make rows or heads overlap", what,
+                (long long)token, (long long)head);
   return PARO_OK;
 }
 
@@ -144,7 +145,7 @@ int check_qy(const paro_attention_shape *s, const void *q, const void *y, int64_
   if (!rc) rc = check_stride(s->q_head, "q_head");
   if (!rc) rc = check_stride(s->y_token, "y_token");
   if (!rc) rc = check_stride(s->y_head, "y_head");
-  if (!rc) rc = check_output_strides(s, rows);
+  if (!rc) rc = check_output_strides("y", s->q_heads, s->head_dim, rows, s->y_token, s->y_head);
   if (rc) return rc;
   if (!q || !y) return fail(PARO_ERR_NULL, "q and y are required");
   if (!aligned(q, 16) || !aligned(y, 16)) return fail(PARO_ERR_ALIGN, "q and y must be 16-byte aligned");
@@ -279,7 +280,7 @@ int paro_attention_prompt(const paro_attention_shape *s, const void *q, const vo
 
 size_t paro_attention_prompt_cached_workspace_bytes(const paro_kv_cache *c, int64_t sequences, int64_t q_tokens,
                                                     int q_heads) {
-  if (check_cache(c, false) || sequences <= 0 || sequences > paro::kMaxSequences || q_tokens <= 0 ||
+  if (check_cache(c, false) || paro::kv4(c->dt) || sequences <= 0 || sequences > paro::kMaxSequences || q_tokens <= 0 ||
       q_tokens > kMaxRows || q_heads < 1 || q_heads > kMaxHeads || q_heads % c->kv_heads)
     return 0;
   const int splits = paro::attention_prompt_splits(q_tokens, sequences, q_heads, c->kv_heads,
@@ -293,6 +294,9 @@ int paro_attention_prompt_cached(const paro_kv_cache *c, int layer, const paro_a
                                  const int32_t *slots, const int64_t *cu_q, int64_t sequences, int64_t q_tokens,
                                  void *y, void *workspace, size_t workspace_bytes, void *stream) {
   int rc = check_cache_and_shape(c, layer, s);
+  if (!rc && paro::kv4(c->dt))
+    return fail(PARO_ERR_UNSUPPORTED, "a cache in four bits: read the slots back (paro_kv_read) and call "
+                                      "paro_attention_prompt");
   if (!rc) rc = check_rows(q_tokens, "q_tokens", kMaxRows);
   if (!rc) rc = check_rows(sequences, "sequences", paro::kMaxSequences);
   if (rc) return rc;
@@ -316,7 +320,7 @@ int paro_attention_prompt_cached(const paro_kv_cache *c, int layer, const paro_a
         overlap(workspace, need, slots, (size_t)sequences * 4) || overlaps_cache(c, workspace, need))
       return fail(PARO_ERR_SHAPE, "the workspace overlaps q, y, cu_q, slots or the cache");
   }
-  paro::AttentionArgs a = attention_args(s, q, y, c->dt);
+  paro::AttentionArgs a = attention_args(s, q, y, row_dtype(c));
   a.cu_q = cu_q;
   a.slots = slots;
   a.sequences = (int)sequences;
@@ -362,16 +366,16 @@ int paro_attention_decode(const paro_kv_cache *c, int layer, const paro_attentio
       overlap(workspace, need, q, extent(rows, s->q_heads, s->head_dim, s->q_token, s->q_head)) ||
       overlap(workspace, need, slots, (size_t)rows * 4) || overlaps_cache(c, workspace, need))
     return fail(PARO_ERR_SHAPE, "the workspace overlaps q, y, slots or the cache");
-  paro::AttentionArgs a = attention_args(s, q, y, c->dt);
+  paro::AttentionArgs a = attention_args(s, q, y, row_dtype(c));
   a.slots = slots;
   a.sequences = (int)rows;
   a.q_tokens = rows;
   a.kv = kv_layer(c, layer);
   const paro::DecodeAttentionPlan p =
       paro::plan_attention_decode(rows, s->q_heads, c->kv_heads, (int64_t)c->max_pages * c->page_size);
-  hipError_t e = paro::launch_attention_decode(a, p, (uint32_t *)workspace,
-                                               (float *)((char *)workspace + kCounterBytes),
-                                               (hipStream_t)stream);
+  const auto launch = paro::kv4(c->dt) ? paro::launch_attention_decode4 : paro::launch_attention_decode;
+  hipError_t e =
+      launch(a, p, (uint32_t *)workspace, (float *)((char *)workspace + kCounterBytes), (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "decode attention launch");
   return ok();
 }
@@ -402,11 +406,78 @@ int paro_kv_append(const paro_kv_cache *c, int layer, const void *k, int64_t k_t
   if (overlaps_cache(c, slots, (size_t)n * 4) || (cu && overlaps_cache(c, cu, (size_t)(n + 1) * 8)) ||
       (granted && overlaps_cache(c, granted, (size_t)n * 4)))
     return fail(PARO_ERR_SHAPE, "slots, cu or granted overlaps the cache");
-  hipError_t e = paro::launch_kv_append(kv_layer(c, layer), c->kv_heads, c->head_dim, (const uint16_t *)k, k_token,
-                                        k_head, (const uint16_t *)v, v_token, v_head, slots, cu, granted,
-                                        (int)n, tokens,
-                                        (hipStream_t)stream);
+  const paro::KvLayer kv = kv_layer(c, layer);
+  const uint16_t *k16 = (const uint16_t *)k, *v16 = (const uint16_t *)v;
+  hipError_t e = paro::kv4(c->dt)
+                     ? paro::launch_kv_append4(kv, c->kv_heads, c->head_dim, (int)row_dtype(c), k16, k_token, k_head,
+                                               v16, v_token, v_head, slots, cu, granted, (int)n, tokens,
+                                               (hipStream_t)stream)
+                     : paro::launch_kv_append(kv, c->kv_heads, c->head_dim, k16, k_token, k_head, v16, v_token, v_head,
+                                              slots, cu, granted, (int)n, tokens, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "kv append launch");
+  return ok();
+}
+
+int paro_kv_read(const paro_kv_cache *c, int layer, void *k, int64_t k_token, int64_t k_head, void *v,
+                 int64_t v_token, int64_t v_head, paro_dtype out_dt, const int32_t *slots, const int64_t *cu,
+                 const int32_t *first, int64_t n, int64_t tokens, void *stream) {
+  int rc = check_cache(c, true);
+  if (!rc) rc = check_layer(c, layer);
+  if (!rc) rc = check_rows(n, "n", paro::kMaxSequences);
+  if (!rc) rc = check_rows(tokens, "tokens", kMaxRows);
+  if (rc) return rc;
+  if (out_dt != PARO_F32 && out_dt != row_dtype(c))
+    return fail(PARO_ERR_DTYPE, "out dtype %d must be the rows' (%d) or F32", (int)out_dt, (int)row_dtype(c));
+  if (!cu && tokens != n)
+    return fail(PARO_ERR_SHAPE, "without cu there is one row per entry: tokens=%lld, n=%lld", (long long)tokens,
+                (long long)n);
+  if (tokens == 0 || n == 0 || (!k && !v)) return ok();
+  if ((rc = check_stride(k_token, "k_token")) || (rc = check_stride(k_head, "k_head")) ||
+      (rc = check_stride(v_token, "v_token")) || (rc = check_stride(v_head, "v_head")) ||
+      (k && (rc = check_output_strides("k", c->kv_heads, c->head_dim, tokens, k_token, k_head))) ||
+      (v && (rc = check_output_strides("v", c->kv_heads, c->head_dim, tokens, v_token, v_head))))
+    return rc;
+  if (!slots) return fail(PARO_ERR_NULL, "slots is required");
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(PARO_ERR_ALIGN, "k and v must be 16-byte aligned");
+  if (!aligned(slots, 4) || !aligned(cu, 8) || !aligned(first, 4))
+    return fail(PARO_ERR_ALIGN, "slots and first must be 4-byte aligned, cu 8-byte aligned");
+  const size_t size = out_dt == PARO_F32 ? 4 : 2;
+  const size_t kb = k ? extent(tokens, c->kv_heads, c->head_dim, k_token, k_head, size) : 0,
+               vb = v ? extent(tokens, c->kv_heads, c->head_dim, v_token, v_head, size) : 0;
+  if (overlaps_cache(c, k, kb) || overlaps_cache(c, v, vb)) return fail(PARO_ERR_SHAPE, "k or v overlaps the cache");
+  if (overlap(k, kb, v, vb)) {
+    // views of one buffer: K's and V's heads side by side in every row of the same stride
+    const uint64_t step = (uint64_t)k_token * size, kr = extent(1, c->kv_heads, c->head_dim, 0, k_head, size),
+                   vr = extent(1, c->kv_heads, c->head_dim, 0, v_head, size);
+    const uintptr_t a = (uintptr_t)k, b = (uintptr_t)v;
+    const uint64_t gap = step ? (b >= a ? (b - a) % step : (step - (a - b) % step) % step) : 0;
+    if (k_token != v_token || gap < kr || gap + vr > step) return fail(PARO_ERR_SHAPE, "k and v overlap");
+  }
+  for (const auto &out : {std::pair<const void *, size_t>(k, kb), std::pair<const void *, size_t>(v, vb)})
+    if (overlap(out.first, out.second, slots, (size_t)n * 4) ||
+        (cu && overlap(out.first, out.second, cu, (size_t)(n + 1) * 8)) ||
+        (first && overlap(out.first, out.second, first, (size_t)n * 4)))
+      return fail(PARO_ERR_SHAPE, "k or v overlaps slots, cu or first");
+  paro::KvReadArgs a = {};
+  a.kv = kv_layer(c, layer);
+  a.kv_heads = c->kv_heads;
+  a.head_dim = c->head_dim;
+  a.dt = (int)row_dtype(c);
+  a.out_dt = (int)out_dt;
+  a.four = paro::kv4(c->dt);
+  a.k = k;
+  a.v = v;
+  a.k_token = k_token;
+  a.k_head = k_head;
+  a.v_token = v_token;
+  a.v_head = v_head;
+  a.slots = slots;
+  a.first = first;
+  a.cu = cu;
+  a.n = (int)n;
+  a.tokens = tokens;
+  hipError_t e = paro::launch_kv_read(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "kv read launch");
   return ok();
 }
 

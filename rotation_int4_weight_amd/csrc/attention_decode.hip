@@ -32,15 +32,15 @@
 #include <algorithm>
 
 #include "attention.hpp"
+#include "attention_join.hpp"
 #include "common.hpp"
 #include "mfma.hpp"
 
 namespace paro {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = kDecodeWaves;
 constexpr int kStep = 32;           // keys per wave and step
-constexpr int kCoherent = 16;       // SC1: device-scope loads and stores of the parts
 constexpr int kUnit = kStep * kWaves;  // keys per workgroup and step
 // Rows up to this length are not cut: joining parts costs 2 to 3 us (stores, a
 // counter and loads through the coherent levels), one step about 1 us (whole
@@ -97,23 +97,6 @@ __device__ __forceinline__ void load_tile(Tile<DIM> &t, const uint16_t *__restri
       }
     }
   }
-}
-
-__device__ __forceinline__ float max_over_groups(float x) {
-  uint32_t u = __float_as_uint(x);
-  auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
-  u = __float_as_uint(x);
-  auto q = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
-}
-__device__ __forceinline__ float sum_over_groups(float x) {
-  uint32_t u = __float_as_uint(x);
-  auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
-  u = __float_as_uint(x);
-  auto q = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
 template <int DIM>
@@ -177,33 +160,12 @@ __device__ __forceinline__ void step(State<DIM> &st, Tile<DIM> &t, const u32x4 (
   }
 }
 
-// (o, m, sum) joined with another part's, both relative to their maxima
-__device__ __forceinline__ void add_part(f32x4 &o, float &m, float &sum, const f32x4 &po, float pm, float psum) {
-  const float mn = fmaxf(m, pm), ref = mn == -INFINITY ? 0.f : mn;
-  const float ka = __builtin_amdgcn_exp2f(m - ref), kb = __builtin_amdgcn_exp2f(pm - ref);
-  o = o * ka + po * kb;
-  sum = sum * ka + psum * kb;
-  m = mn;
-}
-
-// four outputs in the type
-template <int DT>
-__device__ __forceinline__ u32x2 pack_row(const f32x4 &o, float inv) {
-  constexpr bool F = DT == kF16;
-  return u32x2{pack2<DT>(within_type<F>(o[0] * inv), within_type<F>(o[1] * inv)),
-               pack2<DT>(within_type<F>(o[2] * inv), within_type<F>(o[3] * inv))};
-}
-
 template <int DT, int DIM>
 __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs a, DecodeAttentionPlan plan,
                                                                   uint32_t *__restrict__ counters,
                                                                   float *__restrict__ partials) {
   constexpr int E = DIM / 16;
-  constexpr int RS = DIM + 4;  // LDS row: the four words over keep rows on different banks
-  __shared__ __align__(16) float so[kWaves][16][RS];
-  __shared__ float sm[kWaves][16], sl[kWaves][16];
-  __shared__ float jm[16], jl[16];
-  __shared__ int s_last;
+  __shared__ DecodeJoin<DIM> lds;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
   // The part is the slowest index: workgroups go to the XCDs in turn, and with
   // it the fastest those that have work (short rows have one part) would sit on
@@ -274,8 +236,8 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
   {
     const int h = lane & 15, g = lane >> 4;
     if (g == 0) {
-      sm[wave][h] = st.m;
-      sl[wave][h] = l;
+      lds.m[wave][h] = st.m;
+      lds.l[wave][h] = l;
     }
     if (h < heads) {
 #pragma unroll
@@ -283,102 +245,11 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
 #pragma unroll
         for (int j = 0; j < E; j += 4) {
           f32x4 x = {st.o[j][i], st.o[j + 1][i], st.o[j + 2][i], st.o[j + 3][i]};
-          *reinterpret_cast<f32x4 *>(&so[wave][h][(4 * g + i) * E + j]) = x;
+          *reinterpret_cast<f32x4 *>(&lds.o[wave][h][(4 * g + i) * E + j]) = x;
         }
     }
   }
-  __syncthreads();
-  // thread: head t / (DIM / 4), four channels; heads in passes
-  constexpr int kPerHead = DIM / 4, kHeadsPerPass = 256 / kPerHead;
-  const int hp = a.group < 16 ? a.group : 16;  // heads of a part's slot in the workspace
-  const int64_t item = (row * a.kv_heads + kvh) * plan.head_tiles + tile;
-  const int slot_floats = hp * (DIM + 4);  // per head: DIM sums, maximum, sum, 2 unused
-  const int ch = ((int)threadIdx.x % kPerHead) * 4;
-  const __amdgpu_buffer_rsrc_t rs =  // not used with one part
-      raw_rsrc(partials + item * plan.splits * slot_floats, (uint32_t)(plan.splits * slot_floats * 4));
-  for (int h = (int)threadIdx.x / kPerHead; h < heads; h += kHeadsPerPass) {
-    float m = sm[0][h];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sm[w][h]);
-    const float ref = m == -INFINITY ? 0.f : m;
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    float sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float k = __builtin_amdgcn_exp2f(sm[w][h] - ref);
-      sum += k * sl[w][h];
-      o += k * *reinterpret_cast<const f32x4 *>(&so[w][h][ch]);
-    }
-    if (parts == 1) {
-      const float inv = len > 0 ? 1.f / sum : 0.f;
-      const u32x2 y = pack_row<DT>(o, inv);
-      *reinterpret_cast<u32x2 *>(a.y + row * a.y_token + (int64_t)(head0 + h) * a.y_head + ch) =
-          len > 0 ? y : u32x2{0, 0};
-    } else {
-      const uint32_t at = (uint32_t)(split * slot_floats + h * (DIM + 4)) * 4u;
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), rs, at + ch * 4, 0, kCoherent);
-      if (ch == 0) {
-        const u32x2 ml = {__float_as_uint(m), __float_as_uint(sum)};
-        __builtin_amdgcn_raw_buffer_store_b64(ml, rs, at + DIM * 4, 0, kCoherent);
-      }
-    }
-  }
-  if (parts == 1) return;
-  // ---- join the parts: the last workgroup to arrive, in their order ----
-  __builtin_amdgcn_s_waitcnt(0);  // this thread's part has been stored
-  __syncthreads();
-  uint32_t *cnt = counters + item;
-  if (threadIdx.x == 0) {
-    const uint32_t old = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    s_last = old == (uint32_t)(parts - 1);
-  }
-  __syncthreads();
-  if (!s_last) return;
-  // DIM / 4 threads per head leave room for `lanes` of them per output: each
-  // takes every lanes-th part, eight loads in flight together
-  const int lanes = max(1, kHeadsPerPass / heads);
-  const int sub = (int)threadIdx.x / kPerHead;
-  float *const jo = &so[0][0][0];  // [sub][RS], after the waves' use of so
-  for (int h0 = 0; h0 < heads; h0 += kHeadsPerPass) {
-    const int h = lanes > 1 ? sub / lanes : h0 + sub, first = lanes > 1 ? sub % lanes : 0;
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, sum = 0.f;
-    if (h < heads) {
-      constexpr int kBatch = 8;
-      for (int p0 = first; p0 < parts; p0 += kBatch * lanes) {
-        f32x4 x[kBatch];
-        u32x2 ml[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const uint32_t at = (uint32_t)(min(p0 + u * lanes, parts - 1) * slot_floats + h * (DIM + 4)) * 4u;
-          x[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at + ch * 4, 0, kCoherent));
-          ml[u] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, at + DIM * 4, 0, kCoherent));
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u)
-          if (p0 + u * lanes < parts) add_part(o, m, sum, x[u], __uint_as_float(ml[u][0]), __uint_as_float(ml[u][1]));
-      }
-    }
-    if (lanes > 1) {  // then heads <= kHeadsPerPass / 2: this loop runs once
-      __syncthreads();
-      if (h < heads) {
-        *reinterpret_cast<f32x4 *>(jo + sub * RS + ch) = o;
-        if (ch == 0) {
-          jm[sub] = m;
-          jl[sub] = sum;
-        }
-      }
-      __syncthreads();
-      if (first != 0) continue;
-      for (int u = 1; u < lanes && h < heads; ++u)
-        add_part(o, m, sum, *reinterpret_cast<const f32x4 *>(jo + (sub + u) * RS + ch), jm[sub + u], jl[sub + u]);
-    }
-    if (h >= heads) continue;
-    const float inv = 1.f / sum;
-    const u32x2 y = pack_row<DT>(o, inv);
-    *reinterpret_cast<u32x2 *>(a.y + row * a.y_token + (int64_t)(head0 + h) * a.y_head + ch) = y;
-  }
-  if (threadIdx.x == 0) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  join_parts<DT, DIM>(a, plan, lds, counters, partials, row, kvh, tile, heads, split, parts, len);
 }
 
 }  // namespace

@@ -21,6 +21,7 @@
 
 #include "attention.hpp"
 #include "common.hpp"
+#include "kv_rows.hpp"
 
 namespace paro {
 namespace {
@@ -401,39 +402,14 @@ __global__ void __launch_bounds__(256) append_kernel(KvLayer kv, int kv_heads, i
   const int64_t row = (int64_t)blockIdx.x * 4 + wave_id();
   if (row >= tokens) return;
   const int lane = lane_id();
-  int i = (int)row;
-  int64_t low = row, high = row + 1;
-  if (cu) {
-    // the last entry with cu[i] <= row: narrow [a, b) to one by 64-way steps
-    int a = 0, b = n;
-    while (b - a > 1) {
-      const int step = (b - a + 63) / 64;
-      const int at = a + lane * step;
-      const uint64_t le = __ballot(at < b && cu[at < b ? at : a] <= row);
-      if (!(le & 1)) return;  // before the first sequence
-      const int last = 63 - __clzll(le);
-      a += last * step;
-      b = min(b, a + step);
-    }
-    i = a;
-    low = cu[i];
-    high = cu[i + 1];
-    if (low < 0) low = 0;
-    if (high > tokens) high = tokens;
-    if (row < low || row >= high) return;
-  }
-  const int s = slots[i];
-  if (s < 0 || s >= kv.slots || (granted && granted[i] == 0)) return;
-  bool earlier = false;
-#pragma unroll 8
-  for (int j = lane; j < i; j += 64) earlier |= slots[j] == s;
-  if (__any(earlier)) return;
-  const int most = kv.max_pages << kv.page_shift;
-  const int len = min(kv.lengths[s], most);
-  const int64_t pos = (int64_t)len - (high - row);
-  if (pos < 0 || len <= 0) return;
-  const int page = kv.table[(int64_t)s * kv.max_pages + (pos >> kv.page_shift)];
-  if (page < 0 || page >= kv.num_pages) return;
+  Entry e;
+  if (!entry_of(cu, n, row, tokens, lane, e)) return;
+  const int s = slots[e.i];
+  if (s < 0 || s >= kv.slots || (granted && granted[e.i] == 0) || named_before(slots, e.i, lane)) return;
+  const int64_t pos = newest_position(kv, s, e, row);
+  if (pos < 0) return;
+  const int page = page_at(kv, s, pos);
+  if (page < 0) return;
   const int dim = 1 << dim_shift;
   const int64_t base = (int64_t)page * kv.page_stride + ((pos & ((1 << kv.page_shift) - 1)) << dim_shift);
   const int64_t head_stride = (int64_t)dim << kv.page_shift;
@@ -461,7 +437,7 @@ Pool pool_of(const paro_kv_cache &c) {
 // used: compaction's; null for copies that leave their sources in place
 hipError_t launch_copies(const paro_kv_cache &c, const Work &w, int64_t most_copies, const int32_t *used,
                          hipStream_t st) {
-  const int64_t page_bytes = (int64_t)c.kv_heads * c.page_size * c.head_dim * 2;
+  const int64_t page_bytes = kv_page_units(c) * 2;
   const int64_t items = most_copies * c.layers * 2 * ((page_bytes + kPiece - 1) / kPiece);
   const dim3 grid((unsigned)std::min<int64_t>(std::max<int64_t>(items, used ? c.slots : 1), 2048)), block(256);
   if (used)
