@@ -88,8 +88,21 @@ size_t attention_decode_partial_bytes(const DecodeAttentionPlan &p, int64_t rows
 hipError_t launch_attention_decode(const AttentionArgs &a, const DecodeAttentionPlan &p, uint32_t *counters,
                                    float *partials, hipStream_t st);
 
-// The same over a cache in four bits (the plan and the workspace are the same).
-hipError_t launch_attention_decode4(const AttentionArgs &a, const DecodeAttentionPlan &p, uint32_t *counters,
+// The same over a cache in four bits: the keys of all rows together are dealt
+// out to the workgroups that the card holds at once, a counter and two slots for
+// parts each.
+constexpr int kMaxDealtRows = 1024;
+template <int DIM>
+constexpr int kDecode4Resident = DIM == 64 ? 2 : 2;  // workgroups per CU
+constexpr int kDecode4Counters = 256 * 4;
+struct Decode4Plan {
+  int head_tiles;  // as above
+  int workgroups;
+  bool dealt;      // false: a workgroup per row, key-value head and head tile
+};
+Decode4Plan plan_attention_decode4(int64_t rows, int q_heads, int kv_heads, int head_dim, int64_t max_len);
+size_t attention_decode4_partial_bytes(const Decode4Plan &p, int q_heads, int kv_heads, int head_dim);
+hipError_t launch_attention_decode4(const AttentionArgs &a, const Decode4Plan &p, uint32_t *counters,
                                     float *partials, hipStream_t st);
 
 hipError_t launch_kv_append(const KvLayer &kv, int kv_heads, int head_dim, const uint16_t *k, int64_t k_token,

@@ -30,7 +30,9 @@ constexpr int64_t kMaxPool = int64_t(1) << 22;
 constexpr int64_t kMaxTable = int64_t(1) << 20;
 constexpr int64_t kMaxLength = int64_t(1) << 30;
 constexpr int kMaxLayers = 1024;
-static_assert((size_t)paro::kDecodeCounters * 4 <= paro::kCounterBytes, "the join's counters fit the counter area");
+static_assert((size_t)paro::kDecodeCounters * 4 <= paro::kCounterBytes &&
+                  (size_t)paro::kDecode4Counters * 4 <= paro::kCounterBytes,
+              "the joins' counters fit the counter area");
 
 int page_shift(int page_size) {
   for (int s = 4; s <= 8; ++s)
@@ -341,8 +343,13 @@ size_t paro_attention_decode_workspace_bytes(const paro_kv_cache *c, int64_t row
   if (check_cache(c, false) || rows <= 0 || rows > paro::kMaxDecodeRows || q_heads < 1 || q_heads > kMaxHeads ||
       q_heads % c->kv_heads)
     return 0;
-  const paro::DecodeAttentionPlan p =
-      paro::plan_attention_decode(rows, q_heads, c->kv_heads, (int64_t)c->max_pages * c->page_size);
+  const int64_t most = (int64_t)c->max_pages * c->page_size;
+  if (paro::kv4(c->dt))
+    return kCounterBytes +
+           paro::attention_decode4_partial_bytes(
+               paro::plan_attention_decode4(rows, q_heads, c->kv_heads, c->head_dim, most), q_heads, c->kv_heads,
+               c->head_dim);
+  const paro::DecodeAttentionPlan p = paro::plan_attention_decode(rows, q_heads, c->kv_heads, most);
   return kCounterBytes + paro::attention_decode_partial_bytes(p, rows, c->kv_heads, c->head_dim);
 }
 
@@ -371,11 +378,16 @@ int paro_attention_decode(const paro_kv_cache *c, int layer, const paro_attentio
   a.sequences = (int)rows;
   a.q_tokens = rows;
   a.kv = kv_layer(c, layer);
-  const paro::DecodeAttentionPlan p =
-      paro::plan_attention_decode(rows, s->q_heads, c->kv_heads, (int64_t)c->max_pages * c->page_size);
-  const auto launch = paro::kv4(c->dt) ? paro::launch_attention_decode4 : paro::launch_attention_decode;
+  const int64_t most = (int64_t)c->max_pages * c->page_size;
+  uint32_t *counters = (uint32_t *)workspace;
+  float *partials = (float *)((char *)workspace + kCounterBytes);
   hipError_t e =
-      launch(a, p, (uint32_t *)workspace, (float *)((char *)workspace + kCounterBytes), (hipStream_t)stream);
+      paro::kv4(c->dt)
+          ? paro::launch_attention_decode4(
+                a, paro::plan_attention_decode4(rows, s->q_heads, c->kv_heads, c->head_dim, most), counters, partials,
+                (hipStream_t)stream)
+          : paro::launch_attention_decode(a, paro::plan_attention_decode(rows, s->q_heads, c->kv_heads, most), counters,
+                                          partials, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "decode attention launch");
   return ok();
 }

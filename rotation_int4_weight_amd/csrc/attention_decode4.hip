@@ -27,6 +27,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attention.hpp"
 #include "attention_join.hpp"
@@ -39,7 +40,11 @@ namespace {
 
 constexpr int kStep = 32;                    // keys per wave and step
 constexpr int kUnit = kStep * kDecodeWaves;  // keys per workgroup and step
-constexpr int kWhole = 3 * kUnit;            // rows up to this length are not cut
+constexpr int kWhole = 3;                    // units: where no row has more, shares hold whole rows
+constexpr int kOutputUnits = 3;              // what an output costs beside its steps, in steps
+constexpr int kTiles = 2;
+constexpr float kSlack = 3.f;                // a maximum moves when it rose by more than 2^kSlack
+constexpr int kTop = 12;                     // weights times scales stay under 2^(kTop + kSlack) in fp16
 constexpr int kLeastExponent = -126;         // of the values' scale
 
 template <int N>
@@ -47,65 +52,84 @@ struct Words {
   typedef uint32_t type __attribute__((ext_vector_type(N)));
 };
 
-// 32 keys of K and V: [16-key block]
+// 32 keys: a lane's codes of K and V, [16-key block], and one key's pairs: key
+// lane % 16 of K's first and second block (lanes 0.., 16..) and of V's.
 template <int DIM>
 struct Tile {
   typedef typename Words<DIM / 32>::type Codes;
   Codes k[2], v[2];
-  uint32_t pk, pv;  // this lane's pair of either
+  typename Words<DIM / 64>::type pairs;
 };
 
-// Byte offset, in a layer's K or V, of 16 consecutive positions (they lie in one
-// page): their codes, and their pairs.
+// Where a wave's keys lie: byte offsets, in a layer's K or V, of the codes of 16
+// consecutive positions (they lie in one page).  They are looked up for 32 steps
+// at a time, a lane for each 16-key block, so that no step waits for the table.
 template <int DIM>
-struct Pages {
-  const int32_t *table;
-  int64_t page_bytes, head_offset;
-  int last, num_pages, shift;
-  struct At {
-    int64_t codes, pairs;
-  };
-  __device__ __forceinline__ At at(int pos) const {
-    const int j = min(pos >> shift, last);
-    int page = table[j];
+struct Window {
+  uint32_t low, high;  // of this lane's block
+  __device__ __forceinline__ void look_up(const int32_t *__restrict__ table, int64_t page_bytes, int64_t head_offset,
+                                          int last, int num_pages, int shift, int pos, int lane) {
+    const int p = pos + kUnit * (lane >> 1) + 16 * (lane & 1);
+    int page = table[min(p >> shift, last)];
     page = page < 0 ? 0 : page >= num_pages ? num_pages - 1 : page;
-    const int64_t base = (int64_t)page * page_bytes + head_offset;
-    const int p = pos & ((1 << shift) - 1);
-    return At{base + p * Kv4<DIM>::kRow, base + Kv4<DIM>::pairs_at(1 << shift) + p * Kv4<DIM>::kGroups * 4};
+    const int64_t at = (int64_t)page * page_bytes + head_offset + (p & ((1 << shift) - 1)) * Kv4<DIM>::kRow;
+    low = (uint32_t)at;
+    high = (uint32_t)(at >> 32);
+  }
+  __device__ __forceinline__ int64_t block(int i) const {
+    const uint32_t l = __builtin_amdgcn_readlane(low, i), h = __builtin_amdgcn_readlane(high, i);
+    return (int64_t)((uint64_t)h << 32 | l);
   }
 };
 
+// The pairs of key lane % 16 for every lane, [block].
 template <int DIM>
-__device__ __forceinline__ void load_tile(Tile<DIM> &t, const char *__restrict__ k, const char *__restrict__ v,
-                                          const typename Pages<DIM>::At &a0, const typename Pages<DIM>::At &a1,
-                                          int lane) {
-  typedef typename Tile<DIM>::Codes Codes;
-  constexpr int G = Kv4<DIM>::kGroups, W = 16 * G;  // pair words of a block
-  const int ko = (lane & 15) * Kv4<DIM>::kRow + (lane >> 4) * (int)sizeof(Codes), vo = lane * (int)sizeof(Codes);
-  t.k[0] = *reinterpret_cast<const Codes *>(k + a0.codes + ko);
-  t.k[1] = *reinterpret_cast<const Codes *>(k + a1.codes + ko);
-  t.v[0] = *reinterpret_cast<const Codes *>(v + a0.codes + vo);
-  t.v[1] = *reinterpret_cast<const Codes *>(v + a1.codes + vo);
-  const int64_t pairs = ((lane / W) & 1 ? a1.pairs : a0.pairs) + (lane & (W - 1)) * 4;
-  t.pk = *reinterpret_cast<const uint32_t *>(k + pairs);
-  t.pv = *reinterpret_cast<const uint32_t *>(v + pairs);
+struct Pairs {
+  uint32_t k[2][DIM / 64], v[2][DIM / 64];
+};
+template <int DIM>
+__device__ __forceinline__ Pairs<DIM> spread(const typename Words<DIM / 64>::type &p) {
+  Pairs<DIM> out;
+#pragma unroll
+  for (int u = 0; u < DIM / 64; ++u) {
+    const auto half = __builtin_amdgcn_permlane32_swap(p[u], p[u], false, false);  // lanes 0..31, 32..63 twice
+    const auto k = __builtin_amdgcn_permlane16_swap(half[0], half[0], false, false);
+    const auto v = __builtin_amdgcn_permlane16_swap(half[1], half[1], false, false);
+    out.k[0][u] = k[0];
+    out.k[1][u] = k[1];
+    out.v[0][u] = v[0];
+    out.v[1][u] = v[1];
+  }
+  return out;
 }
 
-// {scale, low} of K and {scale * 2^(15 - ev), mid} of V for the 32 keys of a step
-template <int DIM>
-struct Shared {
-  f32x2 k[32 * Kv4<DIM>::kGroups], v[32 * Kv4<DIM>::kGroups];
-};
-
+// A lane's head in the second product is lane % 16; in the first one a lane has
+// key lane % 16 and the heads 4 g .. 4 g + 3, g = lane / 16.
 template <int DIM>
 struct State {
   static constexpr int G = DIM / 64;
-  // o[u][n][i]: the first sum of channel 64 u + 16 g + 4 i + n of the lane's head,
-  // times 2^(15 - ev - 24) (n odd: 2^(15 - ev - 20))
+  // o[u][n][i]: the first sum of channel 64 u + 16 g + 4 i + n of head lane % 16,
+  // times 2^(kTop - ev - 24) (n odd: 2^(kTop - ev - 20))
   f32x4 o[G][4];
-  float mids[G];  // this lane's share of the sum of weights times mid
-  float m, l;     // maximum of scores * log2 e, this lane's share of the sum of weights
-  int ev;         // 2^ev: over the scales of V
+  // of heads 4 g + i, over keys lane % 16 of each block: sums of weights times mid, and of weights
+  f32x4 mids[G], l;
+  f32x4 m;  // weights are exp2(score * log2 e - m), at most 2^kSlack
+  int ev;   // 2^ev: over the scales of V
+};
+
+// Weights of one u for the second product, [head][key], keys in the order in
+// which a lane takes them: 4 g .. 4 g + 3 of the first block, then of the second.
+constexpr int kWeightRow = 40;  // halves: rows of four lanes apart lie on different banks
+
+// A row's queries: their fp16 fragments (head lane % 16), and for heads 4 g + i
+// 2^-24 times their sums by group, and what makes scores * log2 e of a product: a
+// factor >= 0, times 2^rest where `more` (for the wave) says that it is not 1.
+template <int DIM>
+struct Query {
+  u32x4 w[DIM / 32];
+  f32x4 sum[DIM / 64], factor;
+  int rest[4];
+  bool more;
 };
 
 // codes of the even (bits 0..3, 8..11) or odd (4..7, 12..15) nibble of 16-bit
@@ -120,37 +144,34 @@ __device__ __forceinline__ uint32_t centred(uint32_t w, int n) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, nibbles(w, n)) - off);
 }
 
-// One step: 32 keys, `live` of them in the sequence (>= 32 but at its end).
+// The greatest of 16 lanes.
+__device__ __forceinline__ float max16(float x) {
+  const auto turn = [](float v, auto by) {
+    const int u = __builtin_bit_cast(int, v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(u, u, 0x120 + decltype(by)::value, 0xf, 0xf, false));
+  };
+  x = fmaxf(x, turn(x, std::integral_constant<int, 8>()));
+  x = fmaxf(x, turn(x, std::integral_constant<int, 4>()));
+  x = fmaxf(x, turn(x, std::integral_constant<int, 2>()));
+  return fmaxf(x, turn(x, std::integral_constant<int, 1>()));
+}
+
+__device__ __forceinline__ float sum16(float x) {
+  const auto turn = [](float v, auto by) {
+    const int u = __builtin_bit_cast(int, v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(u, u, 0x120 + decltype(by)::value, 0xf, 0xf, false));
+  };
+  x += turn(x, std::integral_constant<int, 8>());
+  x += turn(x, std::integral_constant<int, 4>());
+  x += turn(x, std::integral_constant<int, 2>());
+  return x + turn(x, std::integral_constant<int, 1>());
+}
+
+// The products of one step's 32 keys with the queries, times `factor` (and
+// 2^rest): x[b][i] of key 16 b + lane % 16 and head 4 g + i.
 template <int DT, int DIM>
-__device__ __forceinline__ void step(State<DIM> &st, Tile<DIM> &t, Shared<DIM> &lds, const u32x4 (&q)[DIM / 32],
-                                     const float (&qsum)[DIM / 64], float scale2, int shift, int live, int lane) {
-  constexpr int G = DIM / 64, W = 16 * G;
-  const int g = lane >> 4;
-  const bool end = live < kStep;  // what the page holds behind the end does not count
-  if (end && (lane & (2 * W - 1)) / G >= live) t.pk = t.pv = 0;
-  const float vs = act_to_f32<DT>(t.pv & 0xffffu), vlow = act_to_f32<DT>(t.pv >> 16);
-  const float size = fmaxf(vs, fabsf(vlow) * 0x1p-16f);
-  if (__any(size >= ldexpf(1.f, st.ev))) {  // seldom but in the first step
-    float most = size;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
-    int e;
-    (void)frexpf(most, &e);
-    e = max(st.ev, min(e, 128));
-#pragma unroll
-    for (int u = 0; u < G; ++u)
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st.o[u][n][i] = ldexpf(st.o[u][n][i], st.ev - e);
-    st.ev = e;
-  }
-  if (lane < 2 * W) {
-    lds.k[lane] = f32x2{act_to_f32<DT>(t.pk & 0xffffu), act_to_f32<DT>(t.pk >> 16)};
-    lds.v[lane] = f32x2{ldexpf(vs, 15 - st.ev), __builtin_fmaf(8.f, vs, vlow)};
-  }
-  wave_lds_sync();
-  float s[8];
+__device__ __forceinline__ void scores(f32x4 (&x)[2], const Tile<DIM> &t, const Pairs<DIM> &p, const Query<DIM> &q) {
+  constexpr int G = DIM / 64;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     f32x4 c[G];
@@ -158,206 +179,540 @@ __device__ __forceinline__ void step(State<DIM> &st, Tile<DIM> &t, Shared<DIM> &
     for (int u = 0; u < G; ++u) {
       c[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int x = 2 * u; x < 2 * u + 2; ++x) {
-        const uint32_t w = t.k[b][x];
+      for (int y = 2 * u; y < 2 * u + 2; ++y) {
+        const uint32_t w = t.k[b][y];
         const u32x4 a = {nibbles(w, 0), nibbles(w, 1), nibbles(w, 2), nibbles(w, 3)};
-        c[u] = mfma16x16x32<kF16>(a, q[x], c[u]);
+        c[u] = mfma16x16x32<kF16>(q.w[y], a, c[u]);
       }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float x = 0.f;
+      float s = 0.f;
 #pragma unroll
       for (int u = 0; u < G; ++u) {
-        const f32x2 p = lds.k[(16 * b + 4 * g + i) * G + u];
-        x = __builtin_fmaf(p[0], c[u][i], x);
-        x = __builtin_fmaf(p[1], qsum[u], x);
+        const float low = act_to_f32<DT>(p.k[b][u] >> 16);
+        s = u ? __builtin_fmaf(low, q.sum[u][i], s) : low * q.sum[u][i];
       }
-      s[4 * b + i] = ldexpf(x * scale2, shift);
+#pragma unroll
+      for (int u = 0; u < G; ++u) s = __builtin_fmaf(act_to_f32<DT>(p.k[b][u] & 0xffffu), c[u][i], s);
+      x[b][i] = s;
     }
   }
-  if (end) {
+}
+
+// The maxima rise: weights, sums and outputs so far are made relative to the new
+// ones.  keeps: 16 floats of the wave's.
+template <int DIM>
+__device__ __forceinline__ void raise(State<DIM> &st, const f32x4 (&x)[2], const Query<DIM> &q, float *keeps, int lane) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (16 * (u >> 2) + 4 * g + (u & 3) >= live) s[u] = -INFINITY;
+  for (int i = 0; i < 4; ++i) {
+    const float m = fmaxf(st.m[i], max16(fmaxf(x[0][i], x[1][i])) * q.factor[i]);
+    const float keep = m == st.m[i] ? 1.f : __builtin_amdgcn_exp2f(st.m[i] - m);
+    st.m[i] = m;
+    st.l[i] *= keep;
+#pragma unroll
+    for (int u = 0; u < DIM / 64; ++u) st.mids[u][i] *= keep;
+    if ((lane & 15) == 0) keeps[4 * (lane >> 4) + i] = keep;
   }
-  float top = s[0];
+  wave_lds_sync();
+  const float keep = keeps[lane & 15];
+  wave_lds_sync();
 #pragma unroll
-  for (int u = 1; u < 8; ++u) top = fmaxf(top, s[u]);
-  const float m = fmaxf(st.m, max_over_groups(top));
-  const float ref = m == -INFINITY ? 0.f : m;
-  const float keep = __builtin_amdgcn_exp2f(st.m - ref);
-  st.m = m;
-  float w[8];
-  float sum = 0.f;
+  for (int u = 0; u < DIM / 64; ++u)
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    w[u] = __builtin_amdgcn_exp2f(s[u] - ref);
-    sum += w[u];
-  }
-  st.l = st.l * keep + sum;
-  u32x4 p[G];
+    for (int n = 0; n < 4; ++n) st.o[u][n] *= keep;
+}
+
+// The exponent over 2^ev and the scales of V; size: the lane's greatest.
+__device__ __forceinline__ int exponent_over(int ev, float size) {
+  int e;
+  (void)frexpf(max16(size), &e);  // (the four groups of lanes have the same pairs)
+  return __builtin_amdgcn_readfirstlane(max(ev, min(e, 128)));
+}
+
+// Weights of the scores x, into the sums and, times the scales of V, into `lds`
+// (2^(kTop - ev) p s in fp16).  FRESH: the first step.
+template <int DT, int DIM, bool FRESH>
+__device__ __forceinline__ void weigh(State<DIM> &st, f32x4 (&x)[2], const Pairs<DIM> &pairs,
+                                      const Query<DIM> &q, uint16_t *lds, bool end, int live, int lane) {
+  constexpr int G = DIM / 64;
+  float vs[2][G], mid[2][G];
+  float size = 0.f;
 #pragma unroll
-  for (int u = 0; u < G; ++u) {
-    float mids = st.mids[u] * keep;
-    float r[8];
+  for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const f32x2 pair = lds.v[(16 * (j >> 2) + 4 * g + (j & 3)) * G + u];
-      r[j] = w[j] * pair[0];
-      mids = __builtin_fmaf(w[j], pair[1], mids);
+    for (int u = 0; u < G; ++u) {
+      const float scale = act_to_f32<DT>(pairs.v[b][u] & 0xffffu);
+      size = fmaxf(size, scale);
+      mid[b][u] = __builtin_fmaf(8.f, scale, act_to_f32<DT>(pairs.v[b][u] >> 16));
+      vs[b][u] = scale;
     }
-    st.mids[u] = mids;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) p[u][x] = pack2<kF16>(r[2 * x], r[2 * x + 1]);
-  }
-  if (__any(keep != 1.f)) {
+  if constexpr (FRESH) {
+    st.ev = exponent_over(st.ev, size);
+  } else if (__any(size >= ldexpf(1.f, st.ev))) {  // seldom
+    const int ev = exponent_over(st.ev, size);
 #pragma unroll
     for (int u = 0; u < G; ++u)
 #pragma unroll
-      for (int n = 0; n < 4; ++n) st.o[u][n] *= keep;
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.o[u][n][i] = ldexpf(st.o[u][n][i], st.ev - ev);
+    st.ev = ev;
   }
 #pragma unroll
-  for (int u = 0; u < G; ++u) {
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int u = 0; u < G; ++u) vs[b][u] = ldexpf(vs[b][u], kTop - st.ev);
+  if (q.more) {  // (uniform) a factor that one fp32 number does not hold
+    asm volatile("");
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[b][i] = ldexpf(x[b][i], q.rest[i]);
+  }
+  if (end) {  // (uniform) dead keys do not raise a maximum
+    asm volatile("");
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      if (16 * b + (lane & 15) >= live) x[b] = f32x4{-3e38f, -3e38f, -3e38f, -3e38f};
+  }
+  f32x4 w[2];
+  float top = -INFINITY;
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[b][i] = __builtin_fmaf(x[b][i], q.factor[i], -st.m[i]);
+      top = fmaxf(top, w[b][i]);
+    }
+  if (FRESH || __any(top > kSlack)) {
+    if constexpr (FRESH) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st.m[i] = max16(fmaxf(x[0][i], x[1][i])) * q.factor[i];
+    } else {
+      raise<DIM>(st, x, q, reinterpret_cast<float *>(lds), lane);
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[b][i] = __builtin_fmaf(x[b][i], q.factor[i], -st.m[i]);
+  }
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[b][i] = __builtin_amdgcn_exp2f(w[b][i]);
+  if (end) {
+    asm volatile("");
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      if (16 * b + (lane & 15) >= live) w[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  st.l += w[0] + w[1];
+  // key 16 b + 4 j + k of a block stands at 8 j + 4 b + k
+  uint16_t *to = lds + (4 * (lane >> 4)) * kWeightRow + 8 * (lane >> 2 & 3) + (lane & 3);
+#pragma unroll
+  for (int u = 0; u < G; ++u)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      st.mids[u] += w[b] * mid[b][u];
+      const f32x4 r = w[b] * vs[b][u];
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const uint32_t h = __builtin_bit_cast(uint32_t, f16x2{(_Float16)r[i], (_Float16)r[i + 1]});
+        to[(16 * u + i) * kWeightRow + 4 * b] = (uint16_t)h;
+        to[(16 * u + i + 1) * kWeightRow + 4 * b] = (uint16_t)(h >> 16);
+      }
+    }
+}
+
+// The second product.
+template <int DIM>
+__device__ __forceinline__ void add_values(State<DIM> &st, const typename Words<DIM / 32>::type (&codes)[2],
+                                           const uint16_t *lds, int lane) {
+#pragma unroll
+  for (int u = 0; u < DIM / 64; ++u) {
+    const u32x4 p = *reinterpret_cast<const u32x4 *>(lds + (16 * u + (lane & 15)) * kWeightRow + 8 * (lane >> 4));
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      const u32x4 a = {centred(t.v[0][2 * u], n), centred(t.v[0][2 * u + 1], n), centred(t.v[1][2 * u], n),
-                       centred(t.v[1][2 * u + 1], n)};
-      st.o[u][n] = mfma16x16x32<kF16>(a, p[u], st.o[u][n]);
+      const u32x4 a = {centred(codes[0][2 * u], n), centred(codes[0][2 * u + 1], n), centred(codes[1][2 * u], n),
+                       centred(codes[1][2 * u + 1], n)};
+      st.o[u][n] = mfma16x16x32<kF16>(a, p, st.o[u][n]);
     }
   }
-  wave_lds_sync();  // the pairs have been read
+}
+
+// Lane: head lane%16, channels 32 x + 8 g..; unused heads repeat the last one.
+template <int DIM>
+__device__ __forceinline__ void load_query(u32x4 (&raw)[DIM / 32], const AttentionArgs &a, int64_t row, int head0,
+                                           int heads, int lane) {
+  const uint16_t *qp =
+      a.q + row * a.q_token + (int64_t)(head0 + min(lane & 15, heads - 1)) * a.q_head + 8 * (lane >> 4);
+#pragma unroll
+  for (int x = 0; x < DIM / 32; ++x) raw[x] = *reinterpret_cast<const u32x4 *>(qp + 32 * x);
 }
 
 template <int DT, int DIM>
-__global__ void __launch_bounds__(256, 2) decode4_attention_kernel(AttentionArgs a, DecodeAttentionPlan plan,
-                                                                   uint32_t *__restrict__ counters,
-                                                                   float *__restrict__ partials) {
+__device__ __forceinline__ void open_query(Query<DIM> &q, const u32x4 (&raw)[DIM / 32], float scale, int heads,
+                                           int lane) {
   constexpr int G = DIM / 64, KS = DIM / 32;
-  __shared__ DecodeJoin<DIM> lds;
-  __shared__ __align__(16) Shared<DIM> pairs[kDecodeWaves];
-  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
-  // (the order of the workgroups as in attention_decode.hip)
-  const int split = blockIdx.z;
-  const int tile = (int)(blockIdx.x % plan.head_tiles), kvh = (int)(blockIdx.x / plan.head_tiles);
-  const int64_t row = blockIdx.y;
-  const int heads = min(16, a.group - 16 * tile);  // query heads of this workgroup
-  const int head0 = kvh * a.group + 16 * tile;
-  const int slot = a.slots[row];
-  // Q^T fragments: lane: head lane%16, channels 32 x + 8 g..; unused heads zero
-  u32x4 q[KS];
-  float qsum[G];
-  int shift;  // scores are 2^shift times the products' sums
-  {
-    const int h = lane & 15;
-    const uint16_t *qp = a.q + row * a.q_token + (int64_t)(head0 + min(h, heads - 1)) * a.q_head + 8 * (lane >> 4);
-    float most = 0.f;
+  float most = 0.f;
 #pragma unroll
-    for (int x = 0; x < KS; ++x) {
-      q[x] = *reinterpret_cast<const u32x4 *>(qp + 32 * x);
-      if (h >= heads) q[x] = u32x4{0, 0, 0, 0};
+  for (int x = 0; x < KS; ++x) {
+    q.w[x] = (lane & 15) < heads ? raw[x] : u32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(act_to_f32<DT>(q[x][j / 2] >> (16 * (j & 1)) & 0xffffu)));
-    }
-    most = max_over_groups(most);
-    int e = 0;
-    if (most < INFINITY) (void)frexpf(most, &e);  // most < 2^e
-#pragma unroll
-    for (int u = 0; u < G; ++u) qsum[u] = 0.f;
-#pragma unroll
-    for (int x = 0; x < KS; ++x)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float f0 = ldexpf(act_to_f32<DT>(q[x][j] & 0xffffu), 15 - e);
-        const float f1 = ldexpf(act_to_f32<DT>(q[x][j] >> 16), 15 - e);
-        qsum[x / 2] += f0 + f1;
-        const float part = j & 1 ? 0x1p-4f : 1.f;
-        q[x][j] = pack2<kF16>(f0 * part, f1 * part);
-      }
-#pragma unroll
-    for (int u = 0; u < G; ++u) qsum[u] = sum_over_groups(qsum[u]) * 0x1p-24f;
-    shift = 24 - 15 + e;
+    for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(act_to_f32<DT>(q.w[x][j / 2] >> (16 * (j & 1)) & 0xffffu)));
   }
-  const int len = a.kv.length(slot);
-  // equal parts of whole steps
-  const int part = len <= kWhole ? kWhole
-                                 : (int)((((int64_t)len + plan.splits - 1) / plan.splits + kUnit - 1) / kUnit * kUnit);
-  const int parts = max(1, (len + part - 1) / part);
-  if (split >= parts) return;
-  const int begin = split * part, end = min(len, begin + part);
-
-  State<DIM> st;
+  most = max_over_groups(most);
+  int e = 0;
+  if (most < INFINITY) (void)frexpf(most, &e);  // most < 2^e
+  const float sign = scale < 0.f ? -1.f : 1.f;
+  float sum[G];
+#pragma unroll
+  for (int u = 0; u < G; ++u) sum[u] = 0.f;
+#pragma unroll
+  for (int x = 0; x < KS; ++x)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float f0 = ldexpf(act_to_f32<DT>(q.w[x][j] & 0xffffu), 15 - e) * sign;
+      const float f1 = ldexpf(act_to_f32<DT>(q.w[x][j] >> 16), 15 - e) * sign;
+      sum[x / 2] += f0 + f1;
+      const float part = j & 1 ? 0x1p-4f : 1.f;
+      q.w[x][j] = pack2<kF16>(f0 * part, f1 * part);
+    }
+  // |scale| log2 e 2^shift: in one number where that is neither too large nor
+  // too small for one; the products then take 2^rest
+  const float scale2 = fabsf(scale) * 1.44269504088896340736f;
+  const int shift = 24 - 15 + e;
+  int es;
+  (void)frexpf(scale2, &es);
+  const int part = max(-100 - es, min(shift, 100 - es));
+  const int rest = scale2 > 0.f ? shift - part : 0;
+  const float factor = scale2 > 0.f ? ldexpf(scale2, part) : 0.f;
+  q.more = __any(rest != 0);
+  // from head lane % 16 to heads 4 g + i
 #pragma unroll
   for (int u = 0; u < G; ++u) {
-    st.mids[u] = 0.f;
+    const float all = sum_over_groups(sum[u]) * 0x1p-24f;
 #pragma unroll
-    for (int n = 0; n < 4; ++n) st.o[u][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < 4; ++i) q.sum[u][i] = __shfl(all, 4 * (lane >> 4) + i, 64);
   }
-  st.m = -INFINITY;
-  st.l = 0.f;
-  st.ev = kLeastExponent;
-  const float scale2 = a.scale * 1.44269504088896340736f;
-  if (begin + wave * kStep < end) {
-    Pages<DIM> pg;
-    pg.table = a.kv.table + (int64_t)slot * a.kv.max_pages;
-    pg.page_bytes = a.kv.page_stride * 2;
-    pg.head_offset = kvh * Kv4<DIM>::head_bytes(1 << a.kv.page_shift);
-    pg.last = (len - 1) >> a.kv.page_shift;
-    pg.num_pages = a.kv.num_pages;
-    pg.shift = a.kv.page_shift;
-    const char *k = (const char *)a.kv.k, *v = (const char *)a.kv.v;
-    int pos = begin + wave * kStep;
-    // two tiles in turn: one is worked on while the other is loaded
-    Tile<DIM> t0, t1;
-    load_tile<DIM>(t0, k, v, pg.at(pos), pg.at(pos + 16), lane);
-    typename Pages<DIM>::At n0 = pg.at(pos + kUnit), n1 = pg.at(pos + kUnit + 16);
-    while (true) {
-      if (pos + kUnit < end) load_tile<DIM>(t1, k, v, n0, n1, lane);
-      n0 = pg.at(pos + 2 * kUnit);
-      n1 = pg.at(pos + 2 * kUnit + 16);
-      step<DT, DIM>(st, t0, pairs[wave], q, qsum, scale2, shift, end - pos, lane);
-      pos += kUnit;
-      if (pos >= end) break;
-      if (pos + kUnit < end) load_tile<DIM>(t0, k, v, n0, n1, lane);
-      n0 = pg.at(pos + 2 * kUnit);
-      n1 = pg.at(pos + 2 * kUnit + 16);
-      step<DT, DIM>(st, t1, pairs[wave], q, qsum, scale2, shift, end - pos, lane);
-      pos += kUnit;
-      if (pos >= end) break;
-    }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    q.factor[i] = __shfl(factor, 4 * (lane >> 4) + i, 64);
+    q.rest[i] = __shfl(rest, 4 * (lane >> 4) + i, 64);
   }
-  // ---- join the waves ----
-  const float l = sum_over_groups(st.l);
-  float mids[G];
+}
+
+// How a call's work is dealt out (see plan_attention_decode4): rows one after
+// another, each row's outputs (key-value heads, head tiles) one after another, an
+// output being kOutputUnits for its start and end and a unit per kUnit keys (an
+// empty row has one).  A workgroup takes `share` units in a row; the steps of an
+// output begin kOutputUnits behind its first unit.
+__device__ __forceinline__ int units_of(int len) { return max(1, (len + kUnit - 1) / kUnit); }
+
+// The sum of the lanes up to this one.
+__device__ __forceinline__ int inclusive_sum(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);  // row_shr 1, 2, 4, 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // the row before's last lane
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // the first half's last lane
+  return x;
+}
+
+// a / b for 0 <= a, 0 < b
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+// The slots of an output's parts: a workgroup's second slot has what it began
+// and did not end, its first what it went on with.
+struct DealtParts {
+  int first;  // the workgroup with part 0
+  __device__ __forceinline__ int operator()(int p) const { return p ? 2 * (first + p) : 2 * first + 1; }
+};
+
+// A workgroup's piece of one output.
+struct Piece {
+  int row, slot, len;
+  int steps;           // of the row
+  int begin, end;      // the piece's keys
+  int kvh, heads, head0;
+  int64_t before;      // units before the row's, over the number of outputs
+  int64_t first;       // the output's first step
+  bool whole, none;    // none: only units that stand for an output's start
+};
+
+template <int DT, int DIM>
+__global__ void __launch_bounds__(256, kDecode4Resident<DIM>)
+decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict__ counters,
+                         float *__restrict__ partials) {
+  constexpr int G = DIM / 64;
+  __shared__ DecodeJoin<DIM> lds;
+  static_assert(sizeof(lds.o[0]) >= (DIM / 64) * 16 * kWeightRow * 2, "a wave's weights lie where its sums will");
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
+  const int outputs = a.kv_heads * plan.head_tiles;  // of a row
+  const int rows = a.sequences;
+  // A CU's second workgroup: the first one's waves go before its own (and ended
+  // after 41 us of a 51 us loop), so it takes the lead in every other step.
+  const bool young = blockIdx.x >= 256;
+  // this workgroup's units at..until, in row `row`, whose first is `before`
+  int64_t at, until, share, before;
+  int row, lane_slot = 0, lane_len = 0;
+  const bool in_lanes = plan.dealt && rows <= 64;  // lane: row
+  if (plan.dealt) {
+    // every wave for itself: a lane takes `per` rows
+    const int per = (rows + 63) >> 6, first = lane * per;
+    int units = 0;
+    bool some = false;  // a row that is worth cutting
+    for (int j0 = 0; j0 < per; j0 += 4) {
 #pragma unroll
-  for (int u = 0; u < G; ++u) mids[u] = sum_over_groups(st.mids[u]);
-  {
-    const int h = lane & 15, g = lane >> 4;
-    if (g == 0) {
-      lds.m[wave][h] = st.m;
-      lds.l[wave][h] = l;
-    }
-    if (h < heads) {
-#pragma unroll
-      for (int u = 0; u < G; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f32x4 x;
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-            x[n] = ldexpf(st.o[u][n][i], (n & 1 ? 20 : 24) - 15 + st.ev) + mids[u];
-          *reinterpret_cast<f32x4 *>(&lds.o[wave][h][64 * u + 16 * g + 4 * i]) = x;
+      for (int j = 0; j < 4; ++j) {
+        const int r = first + j0 + j;
+        if (j0 + j < per && r < rows) {
+          lane_slot = a.slots[r];
+          lane_len = a.kv.length(lane_slot);
+          const int n = units_of(lane_len);
+          units += n + kOutputUnits;
+          some |= n > kWhole;
         }
+      }
     }
+    const int sum = inclusive_sum(units);
+    const int64_t total = (int64_t)__builtin_amdgcn_readlane(sum, 63) * outputs;
+    share = quotient(total + gridDim.x - 1, gridDim.x);
+    share = max(share, (int64_t)(__any(some) ? 1 : kOutputUnits + kWhole));
+    at = blockIdx.x * share;
+    until = min(total, at + share);
+    if (at >= total) return;
+    // the lane that has the row of the first unit, then the row
+    const int unit = (int)quotient(at, outputs);
+    const uint64_t over = __ballot(sum > unit);
+    const int who = __ffsll((unsigned long long)over) - 1;
+    int start = __builtin_amdgcn_readlane(sum - units, who);
+    row = who * per;
+    if (per > 1) {
+      while (true) {
+        const int n = units_of(a.kv.length(a.slots[row])) + kOutputUnits;
+        if (start + n > unit) break;
+        start += n;
+        ++row;
+      }
+    }
+    before = start;
+  } else {
+    // a workgroup per output
+    row = (int)(blockIdx.x / (unsigned)outputs);
+    const int n = units_of(a.kv.length(a.slots[row])) + kOutputUnits;
+    before = 0;
+    share = n;
+    at = (int64_t)(blockIdx.x % (unsigned)outputs) * n;
+    until = at + n;
   }
-  join_parts<DT, DIM>(a, plan, lds, counters, partials, row, kvh, tile, heads, split, parts, len);
+  const __amdgpu_buffer_rsrc_t rs =
+      raw_rsrc(partials, plan.dealt ? 2u * gridDim.x * (uint32_t)part_floats(a.group, DIM) * 4u : 0u);
+
+  // the piece at `at`, which moves to the next one
+  const auto next_piece = [&]() {
+    Piece p;
+    p.row = row;
+    p.before = before;
+    p.slot = in_lanes ? __builtin_amdgcn_readlane(lane_slot, row) : a.slots[row];
+    p.len = in_lanes ? __builtin_amdgcn_readlane(lane_len, row) : a.kv.length(p.slot);
+    p.steps = units_of(p.len);
+    const int all = p.steps + kOutputUnits;
+    const uint32_t rel = (uint32_t)(at - before * outputs);
+    const int output = (int)(rel / (uint32_t)all), skip = (int)(rel - (uint32_t)output * all);
+    const int take = (int)min((int64_t)(all - skip), until - at);
+    const int step0 = max(0, skip - kOutputUnits), step1 = skip + take - kOutputUnits;
+    p.none = step1 <= 0;
+    p.whole = step1 - step0 == p.steps;
+    p.begin = step0 * kUnit;
+    p.end = min(p.len, step1 * kUnit);
+    const int tile = output % plan.head_tiles;
+    p.kvh = output / plan.head_tiles;
+    p.heads = min(16, a.group - 16 * tile);
+    p.head0 = p.kvh * a.group + 16 * tile;
+    p.first = before * outputs + (int64_t)output * all + kOutputUnits;
+    at += take;
+    if (at >= (before + all) * outputs) {
+      before += all;
+      ++row;
+    }
+    return p;
+  };
+
+  // the loads of a wave's tiles of a piece; a ring of tiles: one is worked on
+  // while the others are loaded
+  const char *const k = (const char *)a.kv.k, *const v = (const char *)a.kv.v;
+  constexpr uint32_t kCodes = sizeof(typename Tile<DIM>::Codes);
+  const uint32_t k_lane = (lane & 15) * Kv4<DIM>::kRow + (lane >> 4) * kCodes, v_lane = lane * kCodes;
+  const char *const p_lane = (lane & 32 ? v : k) + (lane & 15) * (4 * G);
+  const int shift = a.kv.page_shift;
+  Piece piece;
+  Window<DIM> win;
+  Tile<DIM> t[kTiles];
+  int pos, loaded;  // of the piece: the next step's first key, the steps loaded
+  const auto load = [&](Tile<DIM> &t, int p) {
+    if ((loaded & 31) == 0)
+      win.look_up(a.kv.table + (int64_t)piece.slot * a.kv.max_pages, a.kv.page_stride * 2,
+                  piece.kvh * Kv4<DIM>::head_bytes(1 << shift), (piece.len - 1) >> shift, a.kv.num_pages, shift, p,
+                  lane);
+    const int64_t c0 = win.block(2 * (loaded & 31)), c1 = win.block(2 * (loaded & 31) + 1);
+    // from a block's codes to its pairs
+    const int mask = (1 << shift) - 1, ends = Kv4<DIM>::pairs_at(1 << shift);
+    const int64_t p0 = c0 + ends - (p & mask) * (Kv4<DIM>::kRow - 4 * G);
+    const int64_t p1 = c1 + ends - ((p + 16) & mask) * (Kv4<DIM>::kRow - 4 * G);
+    t.pairs = *reinterpret_cast<const typename Words<G>::type *>(p_lane + (lane & 16 ? p1 : p0));
+    t.k[0] = *reinterpret_cast<const typename Tile<DIM>::Codes *>(k + c0 + k_lane);
+    t.k[1] = *reinterpret_cast<const typename Tile<DIM>::Codes *>(k + c1 + k_lane);
+    t.v[0] = *reinterpret_cast<const typename Tile<DIM>::Codes *>(v + c0 + v_lane);
+    t.v[1] = *reinterpret_cast<const typename Tile<DIM>::Codes *>(v + c1 + v_lane);
+    ++loaded;
+  };
+  u32x4 raw[DIM / 32];
+  const auto start = [&]() {
+    piece = next_piece();
+    if (piece.none) return;
+    load_query<DIM>(raw, a, piece.row, piece.head0, piece.heads, lane);
+    pos = piece.begin + wave * kStep;
+    loaded = 0;
+#pragma unroll
+    for (int d = 0; d + 1 < kTiles; ++d)
+      if (pos + d * kUnit < piece.end) load(t[d], pos + d * kUnit);
+  };
+  start();
+  while (true) {
+    const int end = piece.end;
+    const bool none = piece.none;
+    if (!none) {
+    State<DIM> st;
+    st.m = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    st.l = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < G; ++u) {
+      st.mids[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) st.o[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    st.ev = kLeastExponent;
+    if (pos < end) {
+      uint16_t *weights = reinterpret_cast<uint16_t *>(&lds.o[wave][0][0]);
+      Query<DIM> q;
+      open_query<DT, DIM>(q, raw, a.scale, piece.heads, lane);
+      bool more = true;
+      const auto turn = [&](Tile<DIM> &now, Tile<DIM> &ahead, auto fresh) {
+        const int live = end - pos;  // keys of this step: more than there are but at the end
+        const bool tail = live < kStep;
+        if (live > (kTiles - 1) * kUnit) load(ahead, pos + (kTiles - 1) * kUnit);
+        if (tail) {  // (uniform) what the page holds behind the end does not count
+          asm volatile("");
+          if ((lane & 31) >= live)
+#pragma unroll
+            for (int u = 0; u < G; ++u) now.pairs[u] = 0;
+        }
+        const Pairs<DIM> pairs = spread<DIM>(now.pairs);
+        if (young) {
+          if (&now == &t[0]) __builtin_amdgcn_s_setprio(1);
+          else __builtin_amdgcn_s_setprio(0);
+        }
+        f32x4 x[2];
+        scores<DT, DIM>(x, now, pairs, q);
+        weigh<DT, DIM, decltype(fresh)::value>(st, x, pairs, q, weights, tail, live, lane);
+        wave_lds_sync();
+        add_values<DIM>(st, now.v, weights, lane);
+        wave_lds_sync();
+        pos += kUnit;
+        more = live > kUnit;
+      };
+      turn(t[0], t[kTiles - 1], std::true_type());
+      while (more) {
+#pragma unroll
+        for (int d = 1; d <= kTiles; ++d) {
+          turn(t[d % kTiles], t[(d + kTiles - 1) % kTiles], std::false_type());
+          if (!more) break;
+        }
+      }
+    }
+    // ---- join the waves ----
+    {
+      // heads 4 g + i, over 16 lanes; then head lane % 16
+      float *own = &lds.o[wave][0][0];  // [quantity][head]
+      const int h = lane & 15, g = lane >> 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float l = sum16(st.l[i]);
+        float mids[G];
+#pragma unroll
+        for (int u = 0; u < G; ++u) mids[u] = sum16(st.mids[u][i]);
+        if (h == 0) {
+          lds.m[wave][4 * g + i] = st.m[i];
+          lds.l[wave][4 * g + i] = l;
+#pragma unroll
+          for (int u = 0; u < G; ++u) own[16 * u + 4 * g + i] = mids[u];
+        }
+      }
+      wave_lds_sync();
+      float mids[G];
+#pragma unroll
+      for (int u = 0; u < G; ++u) mids[u] = own[16 * u + h];
+      wave_lds_sync();
+      if (h < piece.heads) {
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f32x4 y;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = ldexpf(st.o[u][j][i], (j & 1 ? 20 : 24) - kTop + st.ev) + mids[u];
+            *reinterpret_cast<f32x4 *>(&lds.o[wave][h][64 * u + 16 * g + 4 * i]) = y;
+          }
+      }
+    }
+    }
+    const Piece done = piece;
+    const bool more = at < until;
+    if (more) start();  // (its loads pass while the waves are joined)
+    if (!none) {
+      int part = 0, parts = 1;
+      DealtParts place = {0};
+      if (!done.whole) {
+        place.first = (int)quotient(done.first, share);
+        part = (int)blockIdx.x - place.first;
+        parts = (int)quotient(done.first + done.steps - 1, share) - place.first + 1;
+      }
+      join_parts<DT, DIM, 8>(a, lds, counters + place.first, rs, place, done.row, done.head0, done.heads, part, parts,
+                          done.len > 0);
+    }
+    if (!more) break;
+    __syncthreads();  // the join's reads of lds are done
+  }
 }
 
 }  // namespace
 
-hipError_t launch_attention_decode4(const AttentionArgs &a, const DecodeAttentionPlan &p, uint32_t *counters,
+// Rows of up to kMaxDealtRows have their units dealt out in equal shares to as
+// many workgroups as the card holds at once, so that the longest row ends with
+// the others; more rows than that are a workgroup for each (row, output).
+Decode4Plan plan_attention_decode4(int64_t rows, int q_heads, int kv_heads, int head_dim, int64_t max_len) {
+  Decode4Plan p;
+  p.head_tiles = (q_heads / kv_heads + 15) / 16;
+  const int64_t outputs = rows * kv_heads * p.head_tiles;
+  const int64_t units = std::max<int64_t>(1, (max_len + kUnit - 1) / kUnit), most = outputs * (units + kOutputUnits);
+  p.dealt = rows <= kMaxDealtRows && rows * (units + kOutputUnits) < int64_t(1) << 31;  // (the sums' type)
+  const int resident = 256 * (head_dim == 64 ? kDecode4Resident<64> : kDecode4Resident<128>);
+  p.workgroups = (int)(p.dealt ? std::min<int64_t>(most, resident) : outputs);
+  return p;
+}
+
+size_t attention_decode4_partial_bytes(const Decode4Plan &p, int q_heads, int kv_heads, int head_dim) {
+  return p.dealt ? (size_t)2 * p.workgroups * part_floats(q_heads / kv_heads, head_dim) * 4 : 0;
+}
+
+hipError_t launch_attention_decode4(const AttentionArgs &a, const Decode4Plan &p, uint32_t *counters,
                                     float *partials, hipStream_t st) {
-  const dim3 grid((unsigned)(a.kv_heads * p.head_tiles), (unsigned)a.sequences, (unsigned)p.splits);
+  const dim3 grid((unsigned)p.workgroups);
 #define PARO_DECODE4(DT, DIM) \
   hipLaunchKernelGGL((decode4_attention_kernel<DT, DIM>), grid, dim3(256), 0, st, a, p, counters, partials)
   if (a.dt == kF16) {

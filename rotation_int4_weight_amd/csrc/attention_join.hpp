@@ -59,24 +59,28 @@ __device__ __forceinline__ u32x2 pack_row(const f32x4 &o, float inv) {
                pack2<DT>(within_type<F>(o[2] * inv), within_type<F>(o[3] * inv))};
 }
 
+// Where an output's parts lie in the workspace: part p in the place_of(p)-th
+// slot of part_floats floats.
+struct PartsInOrder {
+  __device__ __forceinline__ int operator()(int p) const { return p; }
+};
+// floats of a part: per head DIM sums, maximum, sum, 2 unused
+__host__ __device__ inline int part_floats(int group, int dim) { return (group < 16 ? group : 16) * (dim + 4); }
+
 // Called by all threads once every wave has written its o, m and l (no barrier
-// needed in between).  counters and partials: the workspace's.
-template <int DT, int DIM>
-__device__ __forceinline__ void join_parts(const AttentionArgs &a, const DecodeAttentionPlan &plan,
-                                           DecodeJoin<DIM> &lds, uint32_t *__restrict__ counters,
-                                           float *__restrict__ partials, int64_t row, int kvh, int tile, int heads,
-                                           int split, int parts, int len) {
+// needed in between): part `part` of `parts` of the `heads` query heads from
+// head0 of a row.  counter: this output's; rs: the slots (neither is used with
+// one part).  BATCH parts are loaded together by each thread.  some: the row has a key; without one it is zero.
+template <int DT, int DIM, int BATCH, class Place>
+__device__ __forceinline__ void join_parts(const AttentionArgs &a, DecodeJoin<DIM> &lds, uint32_t *counter,
+                                           __amdgpu_buffer_rsrc_t rs, Place place_of, int64_t row, int head0,
+                                           int heads, int part, int parts, bool some) {
   constexpr int RS = DecodeJoin<DIM>::RS;
-  const int head0 = kvh * a.group + 16 * tile;
   __syncthreads();
   // thread: head t / (DIM / 4), four channels; heads in passes
   constexpr int kPerHead = DIM / 4, kHeadsPerPass = 256 / kPerHead;
-  const int hp = a.group < 16 ? a.group : 16;  // heads of a part's slot in the workspace
-  const int64_t item = (row * a.kv_heads + kvh) * plan.head_tiles + tile;
-  const int slot_floats = hp * (DIM + 4);  // per head: DIM sums, maximum, sum, 2 unused
+  const int slot_floats = part_floats(a.group, DIM);
   const int ch = ((int)threadIdx.x % kPerHead) * 4;
-  const __amdgpu_buffer_rsrc_t rs =  // not used with one part
-      raw_rsrc(partials + item * plan.splits * slot_floats, (uint32_t)(plan.splits * slot_floats * 4));
   for (int h = (int)threadIdx.x / kPerHead; h < heads; h += kHeadsPerPass) {
     float m = lds.m[0][h];
 #pragma unroll
@@ -91,12 +95,12 @@ __device__ __forceinline__ void join_parts(const AttentionArgs &a, const DecodeA
       o += k * *reinterpret_cast<const f32x4 *>(&lds.o[w][h][ch]);
     }
     if (parts == 1) {
-      const float inv = len > 0 ? 1.f / sum : 0.f;
+      const float inv = some ? 1.f / sum : 0.f;
       const u32x2 y = pack_row<DT>(o, inv);
       *reinterpret_cast<u32x2 *>(a.y + row * a.y_token + (int64_t)(head0 + h) * a.y_head + ch) =
-          len > 0 ? y : u32x2{0, 0};
+          some ? y : u32x2{0, 0};
     } else {
-      const uint32_t at = (uint32_t)(split * slot_floats + h * (DIM + 4)) * 4u;
+      const uint32_t at = (uint32_t)(place_of(part) * slot_floats + h * (DIM + 4)) * 4u;
       __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), rs, at + ch * 4, 0, kCoherent);
       if (ch == 0) {
         const u32x2 ml = {__float_as_uint(m), __float_as_uint(sum)};
@@ -108,15 +112,14 @@ __device__ __forceinline__ void join_parts(const AttentionArgs &a, const DecodeA
   // ---- join the parts: the last workgroup to arrive, in their order ----
   __builtin_amdgcn_s_waitcnt(0);  // this thread's part has been stored
   __syncthreads();
-  uint32_t *cnt = counters + item;
   if (threadIdx.x == 0) {
-    const uint32_t old = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t old = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     lds.last = old == (uint32_t)(parts - 1);
   }
   __syncthreads();
   if (!lds.last) return;
   // DIM / 4 threads per head leave room for `lanes` of them per output: each
-  // takes every lanes-th part, eight loads in flight together
+  // takes every lanes-th part, BATCH loads in flight together
   const int lanes = max(1, kHeadsPerPass / heads);
   const int sub = (int)threadIdx.x / kPerHead;
   float *const jo = &lds.o[0][0][0];  // [sub][RS], after the waves' use of o
@@ -125,18 +128,17 @@ __device__ __forceinline__ void join_parts(const AttentionArgs &a, const DecodeA
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, sum = 0.f;
     if (h < heads) {
-      constexpr int kBatch = 8;
-      for (int p0 = first; p0 < parts; p0 += kBatch * lanes) {
-        f32x4 x[kBatch];
-        u32x2 ml[kBatch];
+      for (int p0 = first; p0 < parts; p0 += BATCH * lanes) {
+        f32x4 x[BATCH];
+        u32x2 ml[BATCH];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const uint32_t at = (uint32_t)(min(p0 + u * lanes, parts - 1) * slot_floats + h * (DIM + 4)) * 4u;
+        for (int u = 0; u < BATCH; ++u) {
+          const uint32_t at = (uint32_t)(place_of(min(p0 + u * lanes, parts - 1)) * slot_floats + h * (DIM + 4)) * 4u;
           x[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at + ch * 4, 0, kCoherent));
           ml[u] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, at + DIM * 4, 0, kCoherent));
         }
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u)
+        for (int u = 0; u < BATCH; ++u)
           if (p0 + u * lanes < parts) add_part(o, m, sum, x[u], __uint_as_float(ml[u][0]), __uint_as_float(ml[u][1]));
       }
     }
@@ -159,7 +161,7 @@ __device__ __forceinline__ void join_parts(const AttentionArgs &a, const DecodeA
     const u32x2 y = pack_row<DT>(o, inv);
     *reinterpret_cast<u32x2 *>(a.y + row * a.y_token + (int64_t)(head0 + h) * a.y_head + ch) = y;
   }
-  if (threadIdx.x == 0) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 }  // namespace paro
