@@ -151,7 +151,7 @@ def load(path: str | None = None):
     lib.paro_attention_decode_workspace_bytes.restype = SZ
     lib.paro_kv_append.argtypes = [P, I32, P, I64, I64, P, I64, I64, P, P, P, I64, I64, P]
     lib.paro_kv_read.argtypes = [P, I32, P, I64, I64, P, I64, I64, I32, P, P, P, I64, I64, P]
-    lib.paro_rotary.argtypes = [P, P, I32, P, P, I64, P, P]
+    lib.paro_rotary.argtypes = [ctypes.POINTER(ParoRotaryShapeC), P, I32, P, P, I64, P, P]
     lib.paro_rotary_frequencies.argtypes = [P, I32, P, P]
     lib.paro_kv_reserve.argtypes = [P, P, P, I64, P, P, SZ, P]
     lib.paro_kv_fork.argtypes = [P, P, P, I64, P, P, SZ, P]
@@ -203,12 +203,27 @@ def _stream_handle(stream):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_torch_module = _dtypes = None
+
+
+def _torch():
+    """The torch module (an import statement takes longer than a small call's other checks)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dt(t) -> int:
-    import torch
-    return {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}[t.dtype]
+    global _dtypes
+    if _dtypes is None:
+        torch = _torch()
+        _dtypes = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+    return _dtypes[t.dtype]
 
 
 class DeviceLayer:
@@ -485,7 +500,7 @@ class KVCache:
     """
 
     def __init__(self, k, v, refs, table, lengths, dtype=None):
-        import torch
+        torch = _torch()
         what = "KVCache"
         _need(k.dim() == 5 and v.shape == k.shape, 2, what, "k and v: (layers, pages, kv_heads, page_size, head_dim)")
         four = k.dtype == torch.uint8
@@ -503,6 +518,7 @@ class KVCache:
             _need(head_dim in (36, 72), 2, what, "four bits: 36 bytes for 64 channels or 72 for 128")
             head_dim = head_dim * 16 // 9
         self.dtype, self.device, self.bits = dtype, k.device, 4 if four else 16
+        self.row_shape = kv_heads, head_dim  # of K and V rows
         dt = F16 if dtype == torch.float16 else BF16
         self.c = ParoKvCacheC(layers, kv_heads, head_dim, page_size, pages, table.shape[0], table.shape[1],
                               KV4_F16 + dt if four else dt, k.data_ptr(), v.data_ptr(), refs.data_ptr(),
@@ -512,7 +528,7 @@ class KVCache:
     @classmethod
     def empty(cls, layers, pages, kv_heads, page_size, head_dim, slots, max_pages, dtype, device="cuda", bits=16):
         """A cache with all slots empty and all pages free; bits: 16, or 4 for rows of dtype held in four bits."""
-        import torch
+        torch = _torch()
         _need(bits in (4, 16), 5, "KVCache.empty", "bits: 4 or 16")
         _need(bits == 16 or head_dim in (64, 128), 5, "KVCache.empty", "four bits: heads of 64 or 128 channels")
         shape = (layers, pages, kv_heads, page_size, head_dim if bits == 16 else head_dim * 9 // 16)
@@ -538,10 +554,11 @@ def _scratch(workspace, device, what):
 
 def _index(t, dtype, n, device, what, name):
     """t: a contiguous 1-d tensor of n entries (None: any)."""
-    if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() or t.device != device:
+    shape = t.shape
+    if t.dtype != dtype or len(shape) != 1 or not t.is_contiguous() or t.device != device:
         raise ParoError(3, what, f"{name}: a contiguous 1-d {dtype} tensor on {device}")
-    if n is not None and t.shape[0] != n:
-        raise ParoError(2, what, f"{name} has {t.shape[0]} entries, {n} expected")
+    if n is not None and shape[0] != n:
+        raise ParoError(2, what, f"{name} has {shape[0]} entries, {n} expected")
 
 
 def _rows(t, dtype, device, what, name):
@@ -556,12 +573,12 @@ def _rows(t, dtype, device, what, name):
 
 def _launch(fn, device, stream, *args):
     """Calls fn(*args, stream) with `device` current; the stream defaults to that device's current one."""
-    import torch
+    torch = _torch()
     if device.type != "cuda":
         raise ParoError(1, fn.__name__, f"tensors in device memory are required, not on {device}")
     # the raw handle: looking up a Stream object takes longer than the rest of a call's checks
     handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream_handle(stream)
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         return fn(*args, handle)
     with torch.cuda.device(device):
         return fn(*args, handle)
@@ -576,7 +593,7 @@ def _shape_of(q, kv_heads, scale, causal, qs, ys, ks=(0, 0), vs=(0, 0)):
 def paro_attention_prompt(q, k, v, cu_q, cu_k, y, scale=None, causal=True, stream=None) -> None:
     """q, y: (tokens, q_heads, head_dim); k, v: (keys, kv_heads, head_dim), fp16/bf16 views; cu_q, cu_k: int64
     (sequences + 1,) device tensors; scale: 1 / sqrt(head_dim) if None."""
-    import torch
+    torch = _torch()
     what, dt, dev = "paro_attention_prompt", q.dtype, q.device
     qs, ks, vs, ys = (_rows(t, dt, dev, what, name) for t, name in ((q, "q"), (k, "k"), (v, "v"), (y, "y")))
     _need(dt in (torch.float16, torch.bfloat16), 3, what, "fp16 or bf16")
@@ -601,7 +618,7 @@ def paro_attention_prompt_cached(cache: KVCache, layer: int, q, slots, cu_q, y, 
     """q, y: (tokens, q_heads, head_dim) of the cache's dtype: the newest rows of the slots; slots: int32
     (sequences,); cu_q: int64 (sequences + 1,); workspace: zero-filled before its first use, of
     paro_attention_prompt_cached_workspace_bytes() bytes: splits the keys of few rows over workgroups."""
-    import torch
+    torch = _torch()
     what, dt, dev = "paro_attention_prompt_cached", cache.dtype, cache.device
     qs, ys = _rows(q, dt, dev, what, "q"), _rows(y, dt, dev, what, "y")
     _need(y.shape == q.shape, 2, what, "y like q")
@@ -621,7 +638,7 @@ def paro_attention_decode_workspace_bytes(cache: KVCache, rows: int, q_heads: in
 def paro_attention_decode(cache: KVCache, layer: int, q, slots, y, workspace, scale=None, stream=None) -> None:
     """q, y: (rows, q_heads, head_dim), one new token per row; slots: int32 (rows,); workspace: zero-filled before
     its first use, of paro_attention_decode_workspace_bytes() bytes."""
-    import torch
+    torch = _torch()
     what, dt, dev = "paro_attention_decode", cache.dtype, cache.device
     qs, ys = _rows(q, dt, dev, what, "q"), _rows(y, dt, dev, what, "y")
     _need(y.shape == q.shape, 2, what, "y like q")
@@ -637,43 +654,51 @@ def paro_kv_append(cache: KVCache, layer: int, k, v, slots, cu=None, stream=None
     """k, v: (tokens, kv_heads, head_dim) of the cache's dtype become the newest positions of the slots: rows
     cu[i]..cu[i + 1] of slot slots[i] (int32), one row per slot if cu (int64) is None; granted: paro_kv_reserve's,
     whose refused entries are then skipped."""
-    import torch
+    torch = _torch()
     what, dt, dev = "paro_kv_append", cache.dtype, cache.device
     ks, vs = _rows(k, dt, dev, what, "k"), _rows(v, dt, dev, what, "v")
-    rows, heads, d = k.shape
-    if v.shape != k.shape or heads != cache.c.kv_heads or d != cache.c.head_dim:
-        raise ParoError(2, what, f"k and v: (tokens, {cache.c.kv_heads}, {cache.c.head_dim})")
-    _index(slots, torch.int32, None, dev, what, "slots")
+    shape = k.shape
+    if v.shape != shape or tuple(shape[1:]) != cache.row_shape:
+        raise ParoError(2, what, "k and v: (tokens, %d, %d)" % cache.row_shape)
+    n = _entries(torch, dev, what, slots, cu, "granted", granted)
+    rc = _launch(load().paro_kv_append, dev, stream, cache.ref, layer, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
+                 vs[1], slots.data_ptr(), _ptr(cu), _ptr(granted), n, shape[0])
+    if rc:
+        _check(rc, what)
+
+
+def _entries(torch, device, what, slots, cu, name, more):
+    """The entries of a call on packed rows: int32 slots, int64 offsets or None, another int32 list or None."""
+    _index(slots, torch.int32, None, device, what, "slots")
     n = slots.shape[0]
     if cu is not None:
-        _index(cu, torch.int64, n + 1, dev, what, "cu")
-    if granted is not None:
-        _index(granted, torch.int32, n, dev, what, "granted")
-    _check(_launch(load().paro_kv_append, dev, stream, cache.ref, layer, k.data_ptr(), ks[0], ks[1], v.data_ptr(),
-                   vs[0], vs[1], slots.data_ptr(), _ptr(cu), _ptr(granted), n, rows), what)
+        _index(cu, torch.int64, n + 1, device, what, "cu")
+    if more is not None:
+        _index(more, torch.int32, n, device, what, name)
+    return n
 
 
 def paro_kv_read(cache: KVCache, layer: int, k, v, slots, cu=None, first=None, stream=None) -> None:
     """k, v: (tokens, kv_heads, head_dim) of the cache's dtype or fp32 (either may be None) are set to what the slots
     hold: rows cu[i]..cu[i + 1] (one row per slot if cu is None) to positions first[i] and up (int32 (n,)), or to the
     newest ones if first is None; rows beyond what a slot holds are zero."""
-    import torch
+    torch = _torch()
     what, dev = "paro_kv_read", cache.device
-    outs = [t for t in (k, v) if t is not None]
-    _need(outs, 1, what, "k or v is required")
-    out, shape = outs[0].dtype, outs[0].shape
-    _need(out in (cache.dtype, torch.float32), 3, what, f"k and v: {cache.dtype} or fp32")
-    ks, vs = (_rows(t, out, dev, what, name) if t is not None else (0, 0) for t, name in ((k, "k"), (v, "v")))
-    if any(t.shape != shape for t in outs) or shape[1:] != (cache.c.kv_heads, cache.c.head_dim):
-        raise ParoError(2, what, f"k and v: (tokens, {cache.c.kv_heads}, {cache.c.head_dim})")
-    _index(slots, torch.int32, None, dev, what, "slots")
-    n = slots.shape[0]
-    if cu is not None:
-        _index(cu, torch.int64, n + 1, dev, what, "cu")
-    if first is not None:
-        _index(first, torch.int32, n, dev, what, "first")
-    _check(_launch(load().paro_kv_read, dev, stream, cache.ref, layer, _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1],
-                   _dt(outs[0]), slots.data_ptr(), _ptr(cu), _ptr(first), n, shape[0]), what)
+    one = v if k is None else k
+    if one is None:
+        raise ParoError(1, what, "k or v is required")
+    out, shape = one.dtype, one.shape
+    if out != cache.dtype and out != torch.float32:
+        raise ParoError(3, what, f"k and v: {cache.dtype} or fp32")
+    if tuple(shape[1:]) != cache.row_shape or (v is not None and v.shape != shape):
+        raise ParoError(2, what, "k and v: (tokens, %d, %d)" % cache.row_shape)
+    ks = (0, 0) if k is None else _rows(k, out, dev, what, "k")
+    vs = (0, 0) if v is None else _rows(v, out, dev, what, "v")
+    n = _entries(torch, dev, what, slots, cu, "first", first)
+    rc = _launch(load().paro_kv_read, dev, stream, cache.ref, layer, _ptr(k), ks[0], ks[1], _ptr(v), vs[0], vs[1],
+                 _dt(one), slots.data_ptr(), _ptr(cu), _ptr(first), n, shape[0])
+    if rc:
+        _check(rc, what)
 
 
 def paro_kv_workspace_bytes(cache: KVCache) -> int:
@@ -682,7 +707,7 @@ def paro_kv_workspace_bytes(cache: KVCache) -> int:
 
 
 def _plan_call(fn, what, cache, names, a, b, out, workspace, stream):
-    import torch
+    torch = _torch()
     dev = cache.device
     n = a.shape[0] if a.dim() else 0
     for t, name in zip((a, b, out), names):
@@ -705,7 +730,7 @@ def paro_kv_fork(cache: KVCache, parents, children, granted, workspace, stream=N
 
 def paro_kv_free(cache: KVCache, slots, stream=None) -> None:
     """Empties the slots (int32 tensor) and gives up their pages."""
-    import torch
+    torch = _torch()
     _index(slots, torch.int32, None, cache.device, "paro_kv_free", "slots")
     _check(_launch(load().paro_kv_free, cache.device, stream, cache.ref, slots.data_ptr(), slots.shape[0]),
            "paro_kv_free")
@@ -713,7 +738,7 @@ def paro_kv_free(cache: KVCache, slots, stream=None) -> None:
 
 def paro_kv_compact(cache: KVCache, used, workspace, stream=None) -> None:
     """Moves the pages in use to the lowest indices; used: int32 (1,), set to their number."""
-    import torch
+    torch = _torch()
     what, dev = "paro_kv_compact", cache.device
     _index(used, torch.int32, 1, dev, what, "used")
     _check(_launch(load().paro_kv_compact, dev, stream, cache.ref, used.data_ptr(), _ptr(workspace),
@@ -730,7 +755,7 @@ def paro_rotary_frequencies(rot_dim: int, base: float = 10000.0, kind: str = "no
     """(freqs, magnitude): the angle per position of each pair of channels, float64 (rot_dim // 2,) on `device`, and
     what multiplies cosine and sine.  kind: "none", "linear", "base", "bands" or "ramp" (include/paro.h gives their
     formulas), stretching a trained `context` by `factor`; low, high: 1 and 4 ("bands") or 1 and 32 ("ramp") if None."""
-    import torch
+    torch = _torch()
     what = "paro_rotary_frequencies"
     _need(kind in ROTARY, 5, what, f"kind: one of {', '.join(ROTARY)}")
     s = ParoRotaryScalingC(ROTARY[kind], base, factor, context, 1.0 if low is None else low,
@@ -745,15 +770,18 @@ def paro_rotary(x, positions, freqs, y, interleaved: bool = False, inverse: bool
     """x, y: (tokens, heads, head_dim) fp16/bf16/fp32 views, y may be x; positions: int32 (tokens,); freqs: float64
     (rot_dim // 2,), radians per position: channel pairs (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved, turn by
     positions * freqs (inverse: back, which is the gradient), the channels from rot_dim on are copied."""
-    import torch
-    what, dt, dev = "paro_rotary", x.dtype, x.device
+    torch = _torch()
+    what, dt, dev, shape = "paro_rotary", x.dtype, x.device, x.shape
     xs, ys = _rows(x, dt, dev, what, "x"), _rows(y, dt, dev, what, "y")
-    _need(dt in (torch.float16, torch.bfloat16, torch.float32), 3, what, "fp16, bf16 or fp32")
-    _need(y.shape == x.shape, 2, what, "y like x")
-    tokens, heads, d = x.shape
+    if dt not in (torch.float16, torch.bfloat16, torch.float32):
+        raise ParoError(3, what, "fp16, bf16 or fp32")
+    if y.shape != shape:
+        raise ParoError(2, what, "y like x")
+    tokens, heads, d = shape
     _index(positions, torch.int32, tokens, dev, what, "positions")
     _index(freqs, torch.float64, None, dev, what, "freqs")
-    s = ParoRotaryShapeC(heads, d, 2 * freqs.shape[0], bool(interleaved), bool(inverse), magnitude, xs[0], xs[1],
-                         ys[0], ys[1])
-    _check(_launch(load().paro_rotary, dev, stream, ctypes.byref(s), x.data_ptr(), _dt(x), positions.data_ptr(),
-                   freqs.data_ptr(), tokens, y.data_ptr()), what)
+    s = ParoRotaryShapeC(heads, d, 2 * freqs.shape[0], bool(interleaved), bool(inverse), magnitude, xs[0], xs[1], ys[0], ys[1])
+    rc = _launch(load().paro_rotary, dev, stream, s, x.data_ptr(), _dt(x), positions.data_ptr(), freqs.data_ptr(),
+                 tokens, y.data_ptr())
+    if rc:
+        _check(rc, what)

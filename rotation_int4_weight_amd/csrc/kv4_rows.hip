@@ -1,16 +1,20 @@
 // kv4_rows.hip - rows into the pages of a cache in four bits (paro_kv_append)
 // and out of the pages of either kind of cache (paro_kv_read).
 //
-// A wave takes one row.  A lane takes eight channels, eight lanes a group of 64:
-// lowest and greatest value by three exchanges inside eight lanes.
+// A wave takes one row, or a share of it where there are few rows; a lane takes
+// eight channels, eight lanes a group of 64: lowest and greatest value by three
+// exchanges inside eight lanes.
 // The code is decided exactly, for any 16-bit inputs:
-//   - scale = (greatest - low) / 15 is one division in 64 bits.
-//   - q = (x - low) / scale is computed in fp32 with the scale's power of two
-//     taken out (so that nothing overflows), which is within 2^-18 of the
-//     quotient; f = floor(q) then says which half, f + 1/2, could be the border,
-//     and x - low is compared with (f + 1/2) scale in 64 bits: above it the
-//     code is f + 1, below f, on it the even one.  The three terms' sum is exact
-//     for fp16; for bf16 where x and low are less than 2^45 apart in size.
+//   - scale = (greatest - low) / 15 is taken in 64 bits where fp32 leaves open to
+//     which 16-bit number it rounds.
+//   - With t = x - low, f = floor(t / scale), which fp32 gives to within one of the
+//     right one, and d = t - (f + 1/2) scale, whose sign and zero a fused
+//     multiply-add leaves right, the code is f rounded up where d > 0, down where
+//     d < 0 and to even where d = 0: one rounding of f + 1/2 +- 1/4 or + 0.
+//   - A t that fp32 rounded decides wrongly only where d = 0: then d is taken in
+//     64 bits.
+//   - Groups whose scale lies near the ends of fp32 are moved to its middle first,
+//     by a power of two.
 #include <math.h>
 
 #include <algorithm>
@@ -32,110 +36,155 @@ __device__ __forceinline__ float from_lane(float x) {
 }
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141;
 __device__ __forceinline__ float min8(float x) {
-  x = fminf(x, from_lane<kXor1>(x));
-  x = fminf(x, from_lane<kXor2>(x));
-  return fminf(x, from_lane<kMirror8>(x));
+  x = __builtin_elementwise_minimum(x, from_lane<kXor1>(x));
+  x = __builtin_elementwise_minimum(x, from_lane<kXor2>(x));
+  return __builtin_elementwise_minimum(x, from_lane<kMirror8>(x));
 }
 __device__ __forceinline__ float max8(float x) {
-  x = fmaxf(x, from_lane<kXor1>(x));
-  x = fmaxf(x, from_lane<kXor2>(x));
-  return fmaxf(x, from_lane<kMirror8>(x));
+  x = __builtin_elementwise_maximum(x, from_lane<kXor1>(x));
+  x = __builtin_elementwise_maximum(x, from_lane<kXor2>(x));
+  return __builtin_elementwise_maximum(x, from_lane<kMirror8>(x));
 }
 
-struct Coded {
-  uint32_t code[8];
-  uint32_t pair;  // scale in the low half, low in the high one
-};
-
-// Eight channels of a group whose other channels the seven lanes beside have.
+// Eight channels of a group whose other channels the seven lanes beside have: the
+// pair {scale, low}, and the codes as whole numbers.
 template <int DT>
-__device__ __forceinline__ Coded quantise(u32x4 raw) {
-  Coded out;
+__device__ __forceinline__ uint32_t quantise(u32x4 raw, float (&code)[8]) {
   float x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = act_to_f32<DT>(raw[i / 2] >> (16 * (i & 1)) & 0xffffu);
-  float low = x[0], high = x[0], bad = 0.f;
+  float low = x[0], high = x[0];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    low = fminf(low, x[i]);
-    high = fmaxf(high, x[i]);
-    bad = __builtin_fmaf(x[i], 0.f, bad);  // NaN if any is not finite
+  for (int i = 1; i < 8; ++i) {
+    low = __builtin_elementwise_minimum(low, x[i]);  // (NaN stays NaN)
+    high = __builtin_elementwise_maximum(high, x[i]);
   }
   low = min8(low);
   high = max8(high);
-  bad += from_lane<kXor1>(bad);
-  bad += from_lane<kXor2>(bad);
-  bad += from_lane<kMirror8>(bad);
-  const float scale32 = (float)(((double)high - (double)low) / 15.0);
-  const uint32_t sbits = pack2<DT>(scale32, 0.f);  // low half
-  const float scale = act_to_f32<DT>(sbits & 0xffffu);
-  if (bad != bad) {
-    const uint32_t nan = DT == kF16 ? 0x7e007e00u : 0x7fc07fc0u;
-    out.pair = nan;
+  const bool none = !(fabsf(low) < INFINITY && fabsf(high) < INFINITY);
+  // The scale's type has so few bits that a fifteenth of the range from fp32
+  // products, good to 2^-22, rounds as the exact one does, unless a border
+  // between two of its numbers lies that near (or the range leaves fp32's middle).
+  const float range = high - low, fifteenth = range * (1.f / 15.f);
+  uint32_t pair = pack2<DT>(fifteenth * (1.f - 0x1p-22f), fifteenth * (1.f + 0x1p-22f));
+  if (__any((pair & 0xffffu) != pair >> 16 || !(range >= 0x1p-100f && range < INFINITY)))
+    pair = pack2<DT>((float)(((double)high - (double)low) / 15.0), 0.f);
+  const float scale = act_to_f32<DT>(pair & 0xffffu);
+  float unit = 1.f, mid = scale, least_x = low;
+  if (__any(!(scale > 0x1p-60f && scale < 0x1p60f) && scale > 0.f)) {
+    int e;
+    (void)frexpf(scale, &e);
+    unit = scale > 0x1p-60f && scale < 0x1p60f ? 1.f : ldexpf(1.f, min(127, 1 - e));
+    mid *= unit;
+    least_x *= unit;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out.code[i] = 0;
-    return out;
+    for (int i = 0; i < 8; ++i) x[i] *= unit;
   }
-  out.pair = pack2<DT>(scale, low);
-  // unit: a power of two that brings the scale near 1 (exact where 2^127 does)
-  int e;
-  (void)frexpf(scale, &e);
-  const float unit = ldexpf(1.f, min(127, 1 - e));
-  const float lowu = low * unit, inv = 1.f / (scale * unit);
+  const float inv = __builtin_amdgcn_rcpf(mid), half = 0.5f * mid, sure = inv * 0x1p30f;
+  float f[8], d[8];
+  float near = 1.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float f = fminf(fmaxf(floorf(__builtin_fmaf(x[i], unit, -lowu) * inv), 0.f), 15.f);
-    const double over = ((double)x[i] - (double)low) - ((double)f + 0.5) * (double)scale;
-    const uint32_t c = (uint32_t)f;
-    const uint32_t up = c + (over > 0.0 || (over == 0.0 && (c & 1u)) ? 1u : 0u);
-    out.code[i] = scale > 0.f ? min(up, 15u) : 0u;
+    const float t = x[i] - least_x;
+    f[i] = floorf(t * inv);
+    d[i] = __builtin_fmaf(-f[i], mid, t - half);
+    near = fminf(near, fabsf(d[i]));
   }
-  return out;
+  if (__any(near == 0.f)) {
+    bool rounded = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = x[i] - least_x;
+      rounded |= d[i] == 0.f && (x[i] - t != least_x || t + least_x != x[i]);
+    }
+    if (__any(rounded)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const double d64 = ((double)x[i] - (double)least_x) - ((double)f[i] + 0.5) * (double)mid;
+        // (its sign and zero are what counts)
+        d[i] = d[i] == 0.f ? (d64 > 0.0 ? mid : d64 < 0.0 ? -mid : 0.f) : d[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    code[i] = __builtin_amdgcn_fmed3f(
+        rintf(f[i] + __builtin_amdgcn_fmed3f(__builtin_fmaf(d[i], sure, 0.5f), 0.25f, 0.75f)), 0.f, 15.f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) code[i] = scale > 0.f && !none ? code[i] : 0.f;
+  return none ? (DT == kF16 ? 0x7e007e00u : 0x7fc07fc0u) : pack2<DT>(scale, low);
+}
+
+// Four codes, the first in the lowest bits.
+__device__ __forceinline__ uint32_t four(float a, float b, float c, float d) {
+  return (uint32_t)__builtin_fmaf(__builtin_fmaf(__builtin_fmaf(d, 16.f, c), 16.f, b), 16.f, a);
+}
+
+// Shares of a row: its pieces of 512 channels (of K, then of V, where they are
+// quantised; of both where they are read) are taken by `shares` waves in turn.  Few rows are cut so, as one wave's arithmetic takes
+// longer than the look-ups that each of them then repeats.
+constexpr int kChannels = 512;
+int shares_of(int64_t rows, int pieces) {
+  int n = 1;
+  while (n < pieces && rows * n < 4096) n *= 2;
+  return n;
+}
+__device__ __forceinline__ int wave_of_grid() {
+  return __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + wave_id()));
 }
 
 // K and V rows of the newest positions into the pages; where a row does not
 // belong (see entry_of, named_before, newest_position, page_at) it is skipped.
 template <int DT, int DIM>
-__global__ void __launch_bounds__(256) append4_kernel(KvLayer kv, int kv_heads, const uint16_t *__restrict__ k,
-                                                      int64_t k_token, int64_t k_head, const uint16_t *__restrict__ v,
-                                                      int64_t v_token, int64_t v_head,
+__global__ void __launch_bounds__(256) append4_kernel(KvLayer kv, int kv_heads, int shares,
+                                                      const uint16_t *__restrict__ k, int64_t k_token, int64_t k_head,
+                                                      const uint16_t *__restrict__ v, int64_t v_token, int64_t v_head,
                                                       const int32_t *__restrict__ slots,
                                                       const int64_t *__restrict__ cu,
                                                       const int32_t *__restrict__ granted, int n, int64_t tokens) {
   typedef Kv4<DIM> L;
-  const int64_t row = (int64_t)blockIdx.x * 4 + wave_id();
+  const int wave = wave_of_grid(), share = wave % shares;
+  const int64_t row = wave / shares;
   if (row >= tokens) return;
   const int lane = lane_id();
+  const int width = kv_heads * DIM, chunks = (width + kChannels - 1) / kChannels;
+  // piece p: channels c.. of K or V; whole groups of eight lanes have one or have none
+  const auto fetch = [&](int p) {
+    const int c = (p % chunks) * kChannels + lane * 8;
+    if (c >= width) return u32x4{0, 0, 0, 0};
+    const bool second = p >= chunks;
+    return *reinterpret_cast<const u32x4 *>((second ? v : k) + row * (second ? v_token : k_token) +
+                                            c / DIM * (second ? v_head : k_head) + c % DIM);
+  };
+  u32x4 raw = fetch(share);  // (passes while the position is looked up)
   Entry e;
   if (!entry_of(cu, n, row, tokens, lane, e)) return;
   const int s = slots[e.i];
-  if (s < 0 || s >= kv.slots || (granted && granted[e.i] == 0) || named_before(slots, e.i, lane)) return;
+  const bool refused = granted && granted[e.i] == 0;
+  float code[8];
+  uint32_t pair = quantise<DT>(raw, code);
+  if (s < 0 || s >= kv.slots || refused || named_before(slots, e.i, lane)) return;
   const int64_t pos = newest_position(kv, s, e, row);
   if (pos < 0) return;
   const int page = page_at(kv, s, pos);
   if (page < 0) return;
-  const int size = 1 << kv.page_shift, p = (int)(pos & (size - 1));
-  const int pairs = L::pairs_at(size) + p * L::kGroups * 4;
-  // whole groups of eight lanes stay or leave
-  for (int c = lane * 8; c < kv_heads * DIM; c += 512) {
-    const int h = c / DIM, d = c % DIM;
-    const Coded a = quantise<DT>(*reinterpret_cast<const u32x4 *>(k + row * k_token + h * k_head + d));
-    const Coded b = quantise<DT>(*reinterpret_cast<const u32x4 *>(v + row * v_token + h * v_head + d));
-    char *kb = (char *)(kv.k + page * kv.page_stride) + h * L::head_bytes(size);
-    char *vb = (char *)(kv.v + page * kv.page_stride) + h * L::head_bytes(size);
-    uint32_t w = 0, w0 = 0, w1 = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w |= a.code[i] << (4 * ((i >> 1) + 4 * (i & 1)));
-      (i < 4 ? w0 : w1) |= b.code[i] << (4 * (i & 3));
+  const int size = 1 << kv.page_shift, at = (int)(pos & (size - 1));
+  for (int p = share; p < 2 * chunks; p += shares) {
+    if (p != share) pair = quantise<DT>(raw, code);
+    if (p + shares < 2 * chunks) raw = fetch(p + shares);
+    const int c = (p % chunks) * kChannels + lane * 8, d = c % DIM;
+    if (c >= width) continue;
+    const bool second = p >= chunks;
+    char *to = (char *)((second ? kv.v : kv.k) + page * kv.page_stride) + c / DIM * L::head_bytes(size);
+    if (second) {
+      *reinterpret_cast<uint16_t *>(to + L::v_word(at, d / 4)) = (uint16_t)four(code[0], code[1], code[2], code[3]);
+      *reinterpret_cast<uint16_t *>(to + L::v_word(at, d / 4 + 1)) = (uint16_t)four(code[4], code[5], code[6], code[7]);
+    } else {
+      *reinterpret_cast<uint32_t *>(to + L::k_word(at, d / 8)) =
+          four(code[0], code[2], code[4], code[6]) | four(code[1], code[3], code[5], code[7]) << 16;
     }
-    *reinterpret_cast<uint32_t *>(kb + L::k_word(p, d / 8)) = w;
-    *reinterpret_cast<uint16_t *>(vb + L::v_word(p, d / 4)) = (uint16_t)w0;
-    *reinterpret_cast<uint16_t *>(vb + L::v_word(p, d / 4 + 1)) = (uint16_t)w1;
-    if ((lane & 7) == 0) {
-      *reinterpret_cast<uint32_t *>(kb + pairs + (d / kKv4Group) * 4) = a.pair;
-      *reinterpret_cast<uint32_t *>(vb + pairs + (d / kKv4Group) * 4) = b.pair;
-    }
+    if ((lane & 7) == 0)
+      *reinterpret_cast<uint32_t *>(to + L::pairs_at(size) + (at * L::kGroups + d / kKv4Group) * 4) = pair;
   }
 }
 
@@ -153,9 +202,10 @@ __device__ __forceinline__ void store8(void *p, int64_t at, const float (&x)[8])
 }
 
 template <int DT, int OUT, int DIM, bool FOUR>
-__global__ void __launch_bounds__(256) read_kernel(KvReadArgs a) {
+__global__ void __launch_bounds__(256) read_kernel(KvReadArgs a, int shares) {
   typedef Kv4<DIM> L;
-  const int64_t row = (int64_t)blockIdx.x * 4 + wave_id();
+  const int wave = wave_of_grid(), share = wave % shares;
+  const int64_t row = wave / shares;
   if (row >= a.tokens) return;
   const int lane = lane_id();
   Entry e;
@@ -163,51 +213,79 @@ __global__ void __launch_bounds__(256) read_kernel(KvReadArgs a) {
   const int s = a.slots[e.i], len = a.kv.length(s);
   const int64_t pos = a.first ? a.first[e.i] + (row - e.low) : (int64_t)len - (e.high - row);
   const int page = pos >= 0 && pos < len ? page_at(a.kv, s, pos) : -1;
-  const int size = 1 << a.kv.page_shift, p = (int)(pos & (size - 1));
-  for (int c = lane * 8; c < a.kv_heads * DIM; c += 512) {
+  const int size = 1 << a.kv.page_shift, at = (int)(pos & (size - 1));
+  const int width = a.kv_heads * DIM;
+  const uint16_t *kp = a.kv.k + (int64_t)max(page, 0) * a.kv.page_stride,
+                 *vp = a.kv.v + (int64_t)max(page, 0) * a.kv.page_stride;
+  for (int c = share * kChannels + lane * 8; c < width; c += shares * kChannels) {
     const int h = c / DIM, d = c % DIM;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      void *to = w ? a.v : a.k;
-      if (!to) continue;
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    const int64_t ko = row * a.k_token + h * a.k_head + d, vo = row * a.v_token + h * a.v_head + d;
+    if constexpr (FOUR) {
+      const char *kf = (const char *)kp + h * L::head_bytes(size), *vf = (const char *)vp + h * L::head_bytes(size);
+      const int pair = L::pairs_at(size) + (at * L::kGroups + d / kKv4Group) * 4;
+      uint32_t kw = 0, k2 = 0, v0 = 0, v1 = 0, v2 = 0;
       if (page >= 0) {
-        const uint16_t *base = (w ? a.kv.v : a.kv.k) + page * a.kv.page_stride;
-        if constexpr (FOUR) {
-          const char *from = (const char *)base + h * L::head_bytes(size);
-          const uint32_t pair =
-              *reinterpret_cast<const uint32_t *>(from + L::pairs_at(size) + (p * L::kGroups + d / kKv4Group) * 4);
-          const float scale = act_to_f32<DT>(pair & 0xffffu), low = act_to_f32<DT>(pair >> 16);
-          const uint32_t word = w ? *reinterpret_cast<const uint16_t *>(from + L::v_word(p, d / 4)) |
-                                        (uint32_t)*reinterpret_cast<const uint16_t *>(from + L::v_word(p, d / 4 + 1)) << 16
-                                  : *reinterpret_cast<const uint32_t *>(from + L::k_word(p, d / 8));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int n = w ? i : (i >> 1) + 4 * (i & 1);
-            x[i] = __builtin_fmaf((float)(word >> (4 * n) & 15u), scale, low);
-          }
-        } else {
-          const u32x4 r = *reinterpret_cast<const u32x4 *>(base + ((int64_t)h << a.kv.page_shift) * DIM + p * DIM + d);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = act_to_f32<DT>(r[i / 2] >> (16 * (i & 1)) & 0xffffu);
+        if (a.k) {
+          kw = *reinterpret_cast<const uint32_t *>(kf + L::k_word(at, d / 8));
+          k2 = *reinterpret_cast<const uint32_t *>(kf + pair);
+        }
+        if (a.v) {
+          v0 = *reinterpret_cast<const uint16_t *>(vf + L::v_word(at, d / 4));
+          v1 = *reinterpret_cast<const uint16_t *>(vf + L::v_word(at, d / 4 + 1));
+          v2 = *reinterpret_cast<const uint32_t *>(vf + pair);
         }
       }
-      store8<OUT>(to, row * (w ? a.v_token : a.k_token) + h * (w ? a.v_head : a.k_head) + d, x);
+      float x[8];
+      if (a.k) {
+        const float scale = act_to_f32<DT>(k2 & 0xffffu), low = act_to_f32<DT>(k2 >> 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[i] = __builtin_fmaf((float)(kw >> (4 * ((i >> 1) + 4 * (i & 1))) & 15u), scale, low);
+        store8<OUT>(a.k, ko, x);
+      }
+      if (a.v) {
+        const float scale = act_to_f32<DT>(v2 & 0xffffu), low = act_to_f32<DT>(v2 >> 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf((float)((i < 4 ? v0 : v1) >> (4 * (i & 3)) & 15u), scale, low);
+        store8<OUT>(a.v, vo, x);
+      }
+    } else {
+      const int64_t from = ((int64_t)h << a.kv.page_shift) * DIM + at * DIM + d;
+      u32x4 kr = {0, 0, 0, 0}, vr = {0, 0, 0, 0};
+      if (page >= 0) {
+        if (a.k) kr = *reinterpret_cast<const u32x4 *>(kp + from);
+        if (a.v) vr = *reinterpret_cast<const u32x4 *>(vp + from);
+      }
+      if constexpr (OUT == DT) {
+        if (a.k) *reinterpret_cast<u32x4 *>((uint16_t *)a.k + ko) = kr;
+        if (a.v) *reinterpret_cast<u32x4 *>((uint16_t *)a.v + vo) = vr;
+      } else {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = act_to_f32<DT>(kr[i / 2] >> (16 * (i & 1)) & 0xffffu);
+        if (a.k) store8<OUT>(a.k, ko, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = act_to_f32<DT>(vr[i / 2] >> (16 * (i & 1)) & 0xffffu);
+        if (a.v) store8<OUT>(a.v, vo, x);
+      }
     }
   }
 }
 
+template <int DT, int OUT, int DIM, bool FOUR>
+void launch_read(const KvReadArgs &a, hipStream_t st) {
+  const int shares = shares_of(a.tokens, (a.kv_heads * a.head_dim + kChannels - 1) / kChannels);
+  const dim3 grid((unsigned)((a.tokens * shares + 3) / 4)), block(256);
+  hipLaunchKernelGGL((read_kernel<DT, OUT, DIM, FOUR>), grid, block, 0, st, a, shares);
+}
 template <int DT, int OUT>
 void launch_read(const KvReadArgs &a, hipStream_t st) {
-  const dim3 grid((unsigned)((a.tokens + 3) / 4)), block(256);
   if (a.four) {
-    if (a.head_dim == 64) hipLaunchKernelGGL((read_kernel<DT, OUT, 64, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((read_kernel<DT, OUT, 128, true>), grid, block, 0, st, a);
+    if (a.head_dim == 64) launch_read<DT, OUT, 64, true>(a, st);
+    else launch_read<DT, OUT, 128, true>(a, st);
   } else {
-    if (a.head_dim == 64) hipLaunchKernelGGL((read_kernel<DT, OUT, 64, false>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((read_kernel<DT, OUT, 128, false>), grid, block, 0, st, a);
+    if (a.head_dim == 64) launch_read<DT, OUT, 64, false>(a, st);
+    else launch_read<DT, OUT, 128, false>(a, st);
   }
 }
 
@@ -217,9 +295,10 @@ hipError_t launch_kv_append4(const KvLayer &kv, int kv_heads, int head_dim, int 
                              int64_t k_token, int64_t k_head, const uint16_t *v, int64_t v_token, int64_t v_head,
                              const int32_t *slots, const int64_t *cu, const int32_t *granted, int n, int64_t tokens,
                              hipStream_t st) {
-  const dim3 grid((unsigned)((tokens + 3) / 4)), block(256);
+  const int shares = shares_of(tokens, 2 * ((kv_heads * head_dim + kChannels - 1) / kChannels));
+  const dim3 grid((unsigned)((tokens * shares + 3) / 4)), block(256);
 #define PARO_APPEND4(DT, DIM)                                                                                    \
-  hipLaunchKernelGGL((append4_kernel<DT, DIM>), grid, block, 0, st, kv, kv_heads, k, k_token, k_head, v, v_token, \
+  hipLaunchKernelGGL((append4_kernel<DT, DIM>), grid, block, 0, st, kv, kv_heads, shares, k, k_token, k_head, v, v_token, \
                      v_head, slots, cu, granted, n, tokens)
   if (dt == kF16) {
     if (head_dim == 64) PARO_APPEND4(kF16, 64);
