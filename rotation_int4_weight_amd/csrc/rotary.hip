@@ -80,6 +80,13 @@ struct Piece {
 // n / d for n * d < 2^32, with m = ceil(2^32 / d) (d > 1; d == 1: m = 0)
 __device__ __forceinline__ int divide(int n, uint32_t m) { return m ? (int)__umulhi((uint32_t)n, m) : n; }
 
+// Channels of a unit that is copied: the first of them is a multiple of twice the
+// pairs' common divisor that V is.
+template <int DT, int V, bool INTERLEAVED>
+constexpr int rest_unit() {
+  return INTERLEAVED || V == (DT == kF32 ? 4 : 8) ? V : 2 * V;
+}
+
 struct Split {
   int tokens, heads;         // of a workgroup
   int turned, units;         // units of a head: the turned ones, all
@@ -89,6 +96,7 @@ struct Split {
 template <int DT, int V, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, Split w) {
   typedef Piece<DT, V> P;
+  constexpr int kRest = rest_unit<DT, V, INTERLEAVED>();
   __shared__ float2 turn[kThreads];  // [token][pair]
   const int64_t token0 = (int64_t)blockIdx.x * w.tokens;
   const int head0 = blockIdx.y * w.heads;
@@ -112,11 +120,11 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, Split w)
     t.x = t.y = typename P::type{};
     const bool rest = t.unit >= w.turned;
     if (n >= items || h >= heads || (rest && in_place)) return t;
-    const int c = rest ? 2 * a.pairs + (t.unit - w.turned) * V : t.unit * V;
+    const int c = rest ? 2 * a.pairs + (t.unit - w.turned) * kRest : t.unit * V;
     t.from = (token0 + t.row) * a.x_token + (head0 + h) * a.x_head + c;
     t.to = (token0 + t.row) * a.y_token + (head0 + h) * a.y_head + c;
     t.x = P::load(a.x, t.from);
-    if (!INTERLEAVED && !rest) t.y = P::load(a.x, t.from + a.pairs);
+    if (rest ? kRest > V : !INTERLEAVED) t.y = P::load(a.x, t.from + (rest ? V : a.pairs));
     return t;
   };
   Item next = fetch(threadIdx.x);  // (passes while the angles are taken)
@@ -141,6 +149,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a, Split w)
     if (t.from < 0) continue;
     if (t.unit >= w.turned) {
       P::store(a.y, t.to, t.x);
+      if constexpr (kRest > V) P::store(a.y, t.to + V, t.y);
       continue;
     }
     const float2 *cs = turn + t.row * a.pairs;
@@ -176,7 +185,7 @@ template <int DT, int V, bool INTERLEAVED>
 void launch(const RotaryArgs &a, hipStream_t st) {
   Split w;
   w.turned = INTERLEAVED ? 2 * a.pairs / V : a.pairs / V;
-  w.units = w.turned + (a.head_dim - 2 * a.pairs) / V;
+  w.units = w.turned + (a.head_dim - 2 * a.pairs) / rest_unit<DT, V, INTERLEAVED>();
   // as many tokens as share 256 angles, fewer and then fewer heads where that
   // leaves CUs idle (divide() needs items * divisor below 2^32)
   w.heads = a.heads;
@@ -195,11 +204,15 @@ void launch(const RotaryArgs &a, hipStream_t st) {
 template <int DT>
 void launch_typed(const RotaryArgs &a, hipStream_t st) {
   constexpr int V = DT == kF32 ? 4 : 8;  // 16 bytes
+  // units as wide as the pairs allow
   if (a.interleaved) {
     if (2 * a.pairs % V == 0) launch<DT, V, true>(a, st);
+    else if (V > 4 && a.pairs % 2 == 0) launch<DT, 4, true>(a, st);
     else launch<DT, 2, true>(a, st);
   } else {
     if (a.pairs % V == 0) launch<DT, V, false>(a, st);
+    else if (V > 4 && a.pairs % 4 == 0) launch<DT, 4, false>(a, st);
+    else if (a.pairs % 2 == 0) launch<DT, 2, false>(a, st);
     else launch<DT, 1, false>(a, st);
   }
 }

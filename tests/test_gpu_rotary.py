@@ -52,7 +52,7 @@ def frequencies(rot, **kw):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("dim,rot", [(8, 2), (8, 8), (64, 64), (64, 32), (80, 20), (80, 22), (96, 48), (128, 128),
-                                     (128, 126), (256, 64), (512, 512), (512, 6)])
+                                     (128, 126), (256, 64), (512, 512), (512, 6), (64, 24), (128, 56), (72, 36)])
 def test_sizes(dtype, interleaved, dim, rot):
     for tokens, heads in ((1, 1), (5, 3), (67, 2), (300, 1)):
         x, pos = randn((tokens, heads, dim), dtype, dim + rot), ints(tokens, rot)
