@@ -45,6 +45,7 @@ constexpr int kOutputUnits = 3;              // what an output costs beside its 
 constexpr int kTiles = 2;
 constexpr float kSlack = 3.f;                // a maximum moves when it rose by more than 2^kSlack
 constexpr int kTop = 12;                     // weights times scales stay under 2^(kTop + kSlack) in fp16
+constexpr float kLeastMaximum = -3e38f;      // scores that fp32 does not hold weigh nothing, also among themselves
 constexpr int kLeastExponent = -126;         // of the values' scale
 
 template <int N>
@@ -288,7 +289,7 @@ __device__ __forceinline__ void weigh(State<DIM> &st, f32x4 (&x)[2], const Pairs
   if (FRESH || __any(top > kSlack)) {
     if constexpr (FRESH) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st.m[i] = max16(fmaxf(x[0][i], x[1][i])) * q.factor[i];
+      for (int i = 0; i < 4; ++i) st.m[i] = fmaxf(max16(fmaxf(x[0][i], x[1][i])) * q.factor[i], kLeastMaximum);
     } else {
       raise<DIM>(st, x, q, reinterpret_cast<float *>(lds), lane);
     }
@@ -495,7 +496,7 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
     if (per > 1) {
       while (true) {
         const int n = units_of(a.kv.length(a.slots[row])) + kOutputUnits;
-        if (start + n > unit) break;
+        if (start + n > unit || row + 1 >= rows) break;
         start += n;
         ++row;
       }
@@ -538,7 +539,7 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
     at += take;
     if (at >= (before + all) * outputs) {
       before += all;
-      ++row;
+      row = min(row + 1, rows - 1);
     }
     return p;
   };
@@ -587,89 +588,89 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
     const int end = piece.end;
     const bool none = piece.none;
     if (!none) {
-    State<DIM> st;
-    st.m = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    st.l = f32x4{0.f, 0.f, 0.f, 0.f};
+      State<DIM> st;
+      st.m = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      st.l = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < G; ++u) {
-      st.mids[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int u = 0; u < G; ++u) {
+        st.mids[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) st.o[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    st.ev = kLeastExponent;
-    if (pos < end) {
-      uint16_t *weights = reinterpret_cast<uint16_t *>(&lds.o[wave][0][0]);
-      Query<DIM> q;
-      open_query<DT, DIM>(q, raw, a.scale, piece.heads, lane);
-      bool more = true;
-      const auto turn = [&](Tile<DIM> &now, Tile<DIM> &ahead, auto fresh) {
-        const int live = end - pos;  // keys of this step: more than there are but at the end
-        const bool tail = live < kStep;
-        if (live > (kTiles - 1) * kUnit) load(ahead, pos + (kTiles - 1) * kUnit);
-        if (tail) {  // (uniform) what the page holds behind the end does not count
-          asm volatile("");
-          if ((lane & 31) >= live)
+        for (int j = 0; j < 4; ++j) st.o[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      st.ev = kLeastExponent;
+      if (pos < end) {
+        uint16_t *weights = reinterpret_cast<uint16_t *>(&lds.o[wave][0][0]);
+        Query<DIM> q;
+        open_query<DT, DIM>(q, raw, a.scale, piece.heads, lane);
+        bool more = true;
+        const auto turn = [&](Tile<DIM> &now, Tile<DIM> &ahead, auto fresh) {
+          const int live = end - pos;  // keys of this step: more than there are but at the end
+          const bool tail = live < kStep;
+          if (live > (kTiles - 1) * kUnit) load(ahead, pos + (kTiles - 1) * kUnit);
+          if (tail) {  // (uniform) what the page holds behind the end does not count
+            asm volatile("");
+            if ((lane & 31) >= live)
 #pragma unroll
-            for (int u = 0; u < G; ++u) now.pairs[u] = 0;
-        }
-        const Pairs<DIM> pairs = spread<DIM>(now.pairs);
-        if (young) {
-          if (&now == &t[0]) __builtin_amdgcn_s_setprio(1);
-          else __builtin_amdgcn_s_setprio(0);
-        }
-        f32x4 x[2];
-        scores<DT, DIM>(x, now, pairs, q);
-        weigh<DT, DIM, decltype(fresh)::value>(st, x, pairs, q, weights, tail, live, lane);
-        wave_lds_sync();
-        add_values<DIM>(st, now.v, weights, lane);
-        wave_lds_sync();
-        pos += kUnit;
-        more = live > kUnit;
-      };
-      turn(t[0], t[kTiles - 1], std::true_type());
-      while (more) {
+              for (int u = 0; u < G; ++u) now.pairs[u] = 0;
+          }
+          const Pairs<DIM> pairs = spread<DIM>(now.pairs);
+          if (young) {
+            if (&now == &t[0]) __builtin_amdgcn_s_setprio(1);
+            else __builtin_amdgcn_s_setprio(0);
+          }
+          f32x4 x[2];
+          scores<DT, DIM>(x, now, pairs, q);
+          weigh<DT, DIM, decltype(fresh)::value>(st, x, pairs, q, weights, tail, live, lane);
+          wave_lds_sync();
+          add_values<DIM>(st, now.v, weights, lane);
+          wave_lds_sync();
+          pos += kUnit;
+          more = live > kUnit;
+        };
+        turn(t[0], t[kTiles - 1], std::true_type());
+        while (more) {
 #pragma unroll
-        for (int d = 1; d <= kTiles; ++d) {
-          turn(t[d % kTiles], t[(d + kTiles - 1) % kTiles], std::false_type());
-          if (!more) break;
+          for (int d = 1; d <= kTiles; ++d) {
+            turn(t[d % kTiles], t[(d + kTiles - 1) % kTiles], std::false_type());
+            if (!more) break;
+          }
         }
       }
-    }
-    // ---- join the waves ----
-    {
-      // heads 4 g + i, over 16 lanes; then head lane % 16
-      float *own = &lds.o[wave][0][0];  // [quantity][head]
-      const int h = lane & 15, g = lane >> 4;
+      // ---- join the waves ----
+      {
+        // heads 4 g + i, over 16 lanes; then head lane % 16
+        float *own = &lds.o[wave][0][0];  // [quantity][head]
+        const int h = lane & 15, g = lane >> 4;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float l = sum16(st.l[i]);
+        for (int i = 0; i < 4; ++i) {
+          const float l = sum16(st.l[i]);
+          float mids[G];
+#pragma unroll
+          for (int u = 0; u < G; ++u) mids[u] = sum16(st.mids[u][i]);
+          if (h == 0) {
+            lds.m[wave][4 * g + i] = st.m[i];
+            lds.l[wave][4 * g + i] = l;
+#pragma unroll
+            for (int u = 0; u < G; ++u) own[16 * u + 4 * g + i] = mids[u];
+          }
+        }
+        wave_lds_sync();
         float mids[G];
 #pragma unroll
-        for (int u = 0; u < G; ++u) mids[u] = sum16(st.mids[u][i]);
-        if (h == 0) {
-          lds.m[wave][4 * g + i] = st.m[i];
-          lds.l[wave][4 * g + i] = l;
+        for (int u = 0; u < G; ++u) mids[u] = own[16 * u + h];
+        wave_lds_sync();
+        if (h < piece.heads) {
 #pragma unroll
-          for (int u = 0; u < G; ++u) own[16 * u + 4 * g + i] = mids[u];
+          for (int u = 0; u < G; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              f32x4 y;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[j] = ldexpf(st.o[u][j][i], (j & 1 ? 20 : 24) - kTop + st.ev) + mids[u];
+              *reinterpret_cast<f32x4 *>(&lds.o[wave][h][64 * u + 16 * g + 4 * i]) = y;
+            }
         }
       }
-      wave_lds_sync();
-      float mids[G];
-#pragma unroll
-      for (int u = 0; u < G; ++u) mids[u] = own[16 * u + h];
-      wave_lds_sync();
-      if (h < piece.heads) {
-#pragma unroll
-        for (int u = 0; u < G; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            f32x4 y;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = ldexpf(st.o[u][j][i], (j & 1 ? 20 : 24) - kTop + st.ev) + mids[u];
-            *reinterpret_cast<f32x4 *>(&lds.o[wave][h][64 * u + 16 * g + 4 * i]) = y;
-          }
-      }
-    }
     }
     const Piece done = piece;
     const bool more = at < until;
@@ -678,7 +679,7 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
       int part = 0, parts = 1;
       DealtParts place = {0};
       if (!done.whole) {
-        place.first = (int)quotient(done.first, share);
+        place.first = (int)min(quotient(done.first, share), (int64_t)gridDim.x - 1);
         part = (int)blockIdx.x - place.first;
         parts = (int)quotient(done.first + done.steps - 1, share) - place.first + 1;
       }

@@ -140,6 +140,20 @@ def test_one_key_with_a_scale_far_over_the_others():
                 check(c, q, [0], decode(c, q, ints([0])))
 
 
+def test_scores_below_the_range_of_fp32_weigh_nothing():
+    """Keys whose products leave fp32 downwards fill whole steps, the first ones and others, of some waves."""
+    c = _kv4.fill(paro, [300], 16, 1, 64, torch.bfloat16, 2)
+    kp = pairs_view(c, c.k)
+    for p in [*range(64), *range(160, 192), 250]:
+        kp[0, int(c.table[0, p // 16]), 0, p % 16, 0, 0] = 0.0
+        kp[0, int(c.table[0, p // 16]), 0, p % 16, 0, 1] = -3e38
+    q = rows((1, 3, 64), torch.bfloat16, 4).abs() + 100.0
+    kept = [p for p in range(300) if p not in {*range(64), *range(160, 192), 250}]
+    k, v = _kv4.held_rows(c, 0, 0)
+    y = decode(c, q, ints([0]), scale=0.01)
+    _kv4.check_decode(y[0], q[0], k[kept], v[kept], 0.01)
+
+
 def test_queries_of_one_large_channel():
     for dtype in TYPES:
         c = _kv4.fill(paro, [200], 16, 1, 128, dtype, 2, k_scale=0.01)
