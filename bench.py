@@ -524,6 +524,9 @@ ATTENTION_METRIC = "Attention between the q/k/v and the output projections: prom
 KERNEL_FILES["attention"] = ("attention_prompt.hip", "attention.hpp", "common.hpp", "mfma.hpp")
 KERNEL_FILES["attention_decode"] = ("attention_decode.hip", "kv_pages.hip", "attention.hpp", "attention_join.hpp",
                                     "kv_rows.hpp", "common.hpp", "mfma.hpp")
+KERNEL_FILES["attention_decode4"] = ("attention_decode4.hip", "kv4_rows.hip", "rotary.hip", "attention.hpp",
+                                     "attention_join.hpp", "kv_rows.hpp", "kv4.hpp", "rotary.hpp", "common.hpp",
+                                     "mfma.hpp")
 HEAD_DIM = 128  # the Llama-3-8B heads: q_proj has 32 of them, k_proj and v_proj 8
 
 
@@ -532,7 +535,9 @@ def bench_attention(args, paro, synth, np, torch, dev):
     is: --op attention, one causal prompt of the workload's tokens over packed
     q, k, v (paro_attention_prompt); --op attention_decode, one serving step
     of 64 sequences of that length over a paged cache (paro_kv_append, then
-    paro_attention_decode), the cache larger than the MALL."""
+    paro_attention_decode), the cache larger than the MALL; --op
+    attention_decode4, the same over a cache in four bits, with the step's rotary
+    positions before it (paro_rotary)."""
     spec = synth.WORKLOADS[4]
     layers = {name: O for name, _, O in spec["layers"]}
     heads, kv_heads = layers["q_proj"] // HEAD_DIM, layers["k_proj"] // HEAD_DIM
@@ -552,10 +557,12 @@ def bench_attention(args, paro, synth, np, torch, dev):
         config = {"workload": "llama3-8b-attention-prompt-t%d-bf16" % M, "buffer_sets": nsets}
     else:
         rows, page = 64, 16
-        per = M // page
-        cache = paro.KVCache.empty(1, rows * per, kv_heads, page, HEAD_DIM, rows, per, tdt, device=dev)
-        cache.k.normal_(generator=gen)
-        cache.v.normal_(generator=gen)
+        per, four = M // page, args.op == "attention_decode4"
+        cache = paro.KVCache.empty(1, rows * per, kv_heads, page, HEAD_DIM, rows, per, tdt, device=dev,
+                                   bits=4 if four else 16)
+        if not four:
+            cache.k.normal_(generator=gen)
+            cache.v.normal_(generator=gen)
         order = torch.randperm(rows * per, device=dev, generator=gen).to(torch.int32)
         cache.table.copy_(order.view(rows, per))
         cache.refs.fill_(1)
@@ -564,13 +571,22 @@ def bench_attention(args, paro, synth, np, torch, dev):
         q, k, v = rand(rows, heads, HEAD_DIM), rand(rows, kv_heads, HEAD_DIM), rand(rows, kv_heads, HEAD_DIM)
         y = torch.empty_like(q)
         ws = paro.make_workspace(paro.paro_attention_decode_workspace_bytes(cache, rows, heads), device=dev)
+        if four:
+            for s in range(rows):
+                paro.paro_kv_append(cache, 0, rand(M, kv_heads, HEAD_DIM), rand(M, kv_heads, HEAD_DIM), slots[s:s + 1],
+                                    torch.tensor([0, M], dtype=torch.int64, device=dev), stream=stream)
+            fused, turned = rand(rows, heads + 2 * kv_heads, HEAD_DIM), torch.empty_like(torch.cat([q, k], 1))
+            positions, (freqs, _) = cache.lengths - 1, paro.paro_rotary_frequencies(HEAD_DIM, 500000.0, device=dev)
+            q, k, v = turned[:, :heads], turned[:, heads:], fused[:, heads + kv_heads:]
 
         def step(i):
+            if four:
+                paro.paro_rotary(fused[:, :heads + kv_heads], positions, freqs, turned, stream=stream)
             paro.paro_kv_append(cache, 0, k, v, slots, stream=stream)
             paro.paro_attention_decode(cache, 0, q, slots, y, ws, stream=stream)
-        work = 4.0 * rows * M * kv_heads * HEAD_DIM  # K and V read once
+        work = (9 / 8 if four else 4.0) * rows * M * kv_heads * HEAD_DIM  # K and V read once
         unit, scale, peak, bound = "GB/s", 1e9, HBM_PEAK_GBS, "hbm"
-        config = {"workload": "llama3-8b-attention-decode-r%d-t%d-bf16" % (rows, M), "page_size": page}
+        config = {"workload": "llama3-8b-attention-decode%s-r%d-t%d-bf16" % ("4" if four else "", rows, M), "page_size": page}
     for i in range(args.warmup):
         step(i)
     torch.cuda.synchronize()
@@ -666,7 +682,7 @@ def main():
     ap.add_argument("--no-ceiling", action="store_true",
                     help="skip the measured ceiling (device copy for decode, library dense GEMM for prefill)")
     ap.add_argument("--op", choices=("linear", "quantize", "rotate", "rotate_backward", "moe", "mxfp4", "attention",
-                                     "attention_decode"),
+                                     "attention_decode", "attention_decode4"),
                     default="linear",
                     help="linear: the inference hot path (default); quantize: the offline W -> (qweight, "
                          "qzeros, scales) transform of the workload's first layer; rotate_backward: the "
@@ -675,7 +691,9 @@ def main():
                          "mxfp4: the W4A4 MXFP4 linear of the workload's first layer; rotate: the input "
                          "scaling and rotation of every layer (dense prefill form, staged form beside it); "
                          "attention, attention_decode: the attention of the decoder layer, one prompt of 4096 "
-                         "tokens or one step of 64 sequences of 4096 over the paged cache")
+                         "tokens or one step of 64 sequences of 4096 over the paged cache; attention_decode4: "
+                         "such a step over a cache in four bits, rotary positions and the cache's new rows "
+                         "included")
     ap.add_argument("--calib-copy", type=int, default=0, metavar="BYTES",
                     help="instead of the benchmark: copy BYTES between two device buffers --steps times "
                          "(reference dispatches for scaling the FETCH_SIZE / WRITE_SIZE counters)")
@@ -721,7 +739,7 @@ def main():
     if args.op == "mxfp4":
         bench_mxfp4(args, paro, synth, np, torch, dev)
         return
-    if args.op in ("attention", "attention_decode"):
+    if args.op in ("attention", "attention_decode", "attention_decode4"):
         bench_attention(args, paro, synth, np, torch, dev)
         return
     spec = synth.WORKLOADS[args.workload]
