@@ -3,18 +3,28 @@
 //
 // A wave takes one row, or a share of it where there are few rows; a lane takes
 // eight channels, eight lanes a group of 64: lowest and greatest value by three
-// exchanges inside eight lanes.
-// The code is decided exactly, for any 16-bit inputs:
+// exchanges inside eight lanes.  The rows' loads pass while the wave looks up
+// entry, slot, length and page, which depend on one another.
+// The format's code is decided exactly for any 16-bit inputs, in fp32 except
+// where that leaves it open:
 //   - scale = (greatest - low) / 15 is taken in 64 bits where fp32 leaves open to
 //     which 16-bit number it rounds.
-//   - With t = x - low, f = floor(t / scale), which fp32 gives to within one of the
-//     right one, and d = t - (f + 1/2) scale, whose sign and zero a fused
-//     multiply-add leaves right, the code is f rounded up where d > 0, down where
-//     d < 0 and to even where d = 0: one rounding of f + 1/2 +- 1/4 or + 0.
-//   - A t that fp32 rounded decides wrongly only where d = 0: then d is taken in
-//     64 bits.
-//   - Groups whose scale lies near the ends of fp32 are moved to its middle first,
-//     by a power of two.
+//   - With t = x - low, t / scale + 2^7 in fp32 keeps multiples of 2^-16 and is
+//     off by less than 2^-17 before: half of a code comes out as that half, and
+//     the next addition, of 2^23, rounds it to the even code.  What is nearer
+//     than 2^-16 to a half without being one may come out wrong.
+//   - d = t - code scale says so: a fused multiply-add has it exactly where it
+//     is near half of the scale.  |d| under that half: the code is right.  Over
+//     it, or equal to it with a t that fp32 rounded: the wave decides in 64 bits,
+//     by the sign of t - (floor(t / scale) + 1/2) scale.
+//   - So are groups whose scale is near the ends of fp32, moved to its middle by
+//     a power of two first, or subnormal (there 15 may be the limit).
+// What bounds it: 4096 rows of 8 heads of 128 channels are written in 11.0 us
+// (21.5 MB) and read back as 16 bits in 11.4 (21.5 MB): about 5 us are launch and
+// look-ups (64 rows: 4.3 and 4.0 us), the rest 190 vector instructions per 512
+// channels written (all stores left out: 9.0 us), and the bytes of those read
+// (95537 rows: 124 us, 4.9 TB/s, what a copy reaches).
+
 #include <math.h>
 
 #include <algorithm>
@@ -46,10 +56,34 @@ __device__ __forceinline__ float max8(float x) {
   return __builtin_elementwise_maximum(x, from_lane<kMirror8>(x));
 }
 
-// Eight channels of a group whose other channels the seven lanes beside have: the
-// pair {scale, low}, and the codes as whole numbers.
+// The codes where fp32 leaves one of them open (see the header).
 template <int DT>
-__device__ __forceinline__ uint32_t quantise(u32x4 raw, float (&code)[8]) {
+__device__ __forceinline__ void codes_in_64_bits(const float (&values)[8], float low, float scale, float (&code)[8]) {
+  float unit = 1.f;
+  if (scale > 0.f && !(scale > 0x1p-60f && scale < 0x1p60f)) {
+    int e;
+    (void)frexpf(scale, &e);
+    unit = ldexpf(1.f, min(127, 1 - e));
+  }
+  const float mid = scale * unit, least_x = low * unit;
+  const float inv = __builtin_amdgcn_rcpf(mid), half = 0.5f * mid, sure = inv * 0x1p30f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = values[i] * unit, t = x - least_x;
+    const float f = floorf(t * inv);
+    float d = __builtin_fmaf(-f, mid, t - half);
+    const double d64 = ((double)x - (double)least_x) - ((double)f + 0.5) * (double)mid;
+    // (its sign and zero are what counts)
+    d = d == 0.f ? (d64 > 0.0 ? mid : d64 < 0.0 ? -mid : 0.f) : d;
+    code[i] = __builtin_amdgcn_fmed3f(
+        rintf(f + __builtin_amdgcn_fmed3f(__builtin_fmaf(d, sure, 0.5f), 0.25f, 0.75f)), 0.f, 15.f);
+  }
+}
+
+// Eight channels of a group whose other channels the seven lanes beside have: the
+// pair {scale, low}, and the codes as whole numbers; false: they are all 0.
+template <int DT>
+__device__ __forceinline__ bool quantise(u32x4 raw, uint32_t &pair, float (&code)[8]) {
   float x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = act_to_f32<DT>(raw[i / 2] >> (16 * (i & 1)) & 0xffffu);
@@ -66,53 +100,32 @@ __device__ __forceinline__ uint32_t quantise(u32x4 raw, float (&code)[8]) {
   // products, good to 2^-22, rounds as the exact one does, unless a border
   // between two of its numbers lies that near (or the range leaves fp32's middle).
   const float range = high - low, fifteenth = range * (1.f / 15.f);
-  uint32_t pair = pack2<DT>(fifteenth * (1.f - 0x1p-22f), fifteenth * (1.f + 0x1p-22f));
+  pair = pack2<DT>(fifteenth * (1.f - 0x1p-22f), fifteenth * (1.f + 0x1p-22f));
   if (__any((pair & 0xffffu) != pair >> 16 || !(range >= 0x1p-100f && range < INFINITY)))
     pair = pack2<DT>((float)(((double)high - (double)low) / 15.0), 0.f);
   const float scale = act_to_f32<DT>(pair & 0xffffu);
-  float unit = 1.f, mid = scale, least_x = low;
-  if (__any(!(scale > 0x1p-60f && scale < 0x1p60f) && scale > 0.f)) {
-    int e;
-    (void)frexpf(scale, &e);
-    unit = scale > 0x1p-60f && scale < 0x1p60f ? 1.f : ldexpf(1.f, min(127, 1 - e));
-    mid *= unit;
-    least_x *= unit;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= unit;
-  }
-  const float inv = __builtin_amdgcn_rcpf(mid), half = 0.5f * mid, sure = inv * 0x1p30f;
-  float f[8], d[8];
-  float near = 1.f;
+  // (a subnormal scale may be so far off a fifteenth that codes need the limit)
+  constexpr float kLeast = DT == kF16 ? 0x1p-14f : 0x1p-60f, kMost = DT == kF16 ? 0x1p16f : 0x1p60f;
+  const float inv = __builtin_amdgcn_rcpf(scale), half = 0.5f * scale;
+  float d[8], far = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = x[i] - least_x;
-    f[i] = floorf(t * inv);
-    d[i] = __builtin_fmaf(-f[i], mid, t - half);
-    near = fminf(near, fabsf(d[i]));
+    const float t = x[i] - low;
+    code[i] = (__builtin_fmaf(t, inv, 0x1p7f) + 0x1p23f) - (0x1p23f + 0x1p7f);
+    d[i] = __builtin_fmaf(-code[i], scale, t);
+    far = fmaxf(far, fabsf(d[i]));
   }
-  if (__any(near == 0.f)) {
-    bool rounded = false;
+  bool open = scale > 0.f && !(scale >= kLeast && scale < kMost);
+  if (__any(far >= half)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float t = x[i] - least_x;
-      rounded |= d[i] == 0.f && (x[i] - t != least_x || t + least_x != x[i]);
-    }
-    if (__any(rounded)) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const double d64 = ((double)x[i] - (double)least_x) - ((double)f[i] + 0.5) * (double)mid;
-        // (its sign and zero are what counts)
-        d[i] = d[i] == 0.f ? (d64 > 0.0 ? mid : d64 < 0.0 ? -mid : 0.f) : d[i];
-      }
+      const float t = x[i] - low;
+      open |= fabsf(d[i]) > half || (fabsf(d[i]) == half && (x[i] - t != low || t + low != x[i]));
     }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    code[i] = __builtin_amdgcn_fmed3f(
-        rintf(f[i] + __builtin_amdgcn_fmed3f(__builtin_fmaf(d[i], sure, 0.5f), 0.25f, 0.75f)), 0.f, 15.f);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) code[i] = scale > 0.f && !none ? code[i] : 0.f;
-  return none ? (DT == kF16 ? 0x7e007e00u : 0x7fc07fc0u) : pack2<DT>(scale, low);
+  if (__any(open)) codes_in_64_bits<DT>(x, low, scale, code);
+  pair = none ? (DT == kF16 ? 0x7e007e00u : 0x7fc07fc0u) : pack2<DT>(scale, low);
+  return scale > 0.f && !none;
 }
 
 // Four codes, the first in the lowest bits.
@@ -121,8 +134,11 @@ __device__ __forceinline__ uint32_t four(float a, float b, float c, float d) {
 }
 
 // Shares of a row: its pieces of 512 channels (of K, then of V, where they are
-// quantised; of both where they are read) are taken by `shares` waves in turn.  Few rows are cut so, as one wave's arithmetic takes
-// longer than the look-ups that each of them then repeats.
+// quantised; of both where they are read) are taken by `shares` waves in turn.
+// Few rows are cut so, as one wave's arithmetic takes longer than the look-ups
+// that each of them then repeats: up to 4096 waves (written and read back, 64
+// rows 14.7 us with a wave each, 12.4 cut; 4096 rows 22.0 either way, cut into
+// four 24.4).
 constexpr int kChannels = 512;
 int shares_of(int64_t rows, int pieces) {
   int n = 1;
@@ -162,7 +178,8 @@ __global__ void __launch_bounds__(256) append4_kernel(KvLayer kv, int kv_heads, 
   const int s = slots[e.i];
   const bool refused = granted && granted[e.i] == 0;
   float code[8];
-  uint32_t pair = quantise<DT>(raw, code);
+  uint32_t pair;
+  bool some = quantise<DT>(raw, pair, code);
   if (s < 0 || s >= kv.slots || refused || named_before(slots, e.i, lane)) return;
   const int64_t pos = newest_position(kv, s, e, row);
   if (pos < 0) return;
@@ -170,18 +187,18 @@ __global__ void __launch_bounds__(256) append4_kernel(KvLayer kv, int kv_heads, 
   if (page < 0) return;
   const int size = 1 << kv.page_shift, at = (int)(pos & (size - 1));
   for (int p = share; p < 2 * chunks; p += shares) {
-    if (p != share) pair = quantise<DT>(raw, code);
+    if (p != share) some = quantise<DT>(raw, pair, code);
     if (p + shares < 2 * chunks) raw = fetch(p + shares);
     const int c = (p % chunks) * kChannels + lane * 8, d = c % DIM;
     if (c >= width) continue;
     const bool second = p >= chunks;
     char *to = (char *)((second ? kv.v : kv.k) + page * kv.page_stride) + c / DIM * L::head_bytes(size);
     if (second) {
-      *reinterpret_cast<uint16_t *>(to + L::v_word(at, d / 4)) = (uint16_t)four(code[0], code[1], code[2], code[3]);
-      *reinterpret_cast<uint16_t *>(to + L::v_word(at, d / 4 + 1)) = (uint16_t)four(code[4], code[5], code[6], code[7]);
+      *reinterpret_cast<uint16_t *>(to + L::v_word(at, d / 4)) = (uint16_t)(some ? four(code[0], code[1], code[2], code[3]) : 0u);
+      *reinterpret_cast<uint16_t *>(to + L::v_word(at, d / 4 + 1)) = (uint16_t)(some ? four(code[4], code[5], code[6], code[7]) : 0u);
     } else {
       *reinterpret_cast<uint32_t *>(to + L::k_word(at, d / 8)) =
-          four(code[0], code[2], code[4], code[6]) | four(code[1], code[3], code[5], code[7]) << 16;
+          some ? four(code[0], code[2], code[4], code[6]) | four(code[1], code[3], code[5], code[7]) << 16 : 0u;
     }
     if ((lane & 7) == 0)
       *reinterpret_cast<uint32_t *>(to + L::pairs_at(size) + (at * L::kGroups + d / kKv4Group) * 4) = pair;
@@ -298,8 +315,8 @@ hipError_t launch_kv_append4(const KvLayer &kv, int kv_heads, int head_dim, int 
   const int shares = shares_of(tokens, 2 * ((kv_heads * head_dim + kChannels - 1) / kChannels));
   const dim3 grid((unsigned)((tokens * shares + 3) / 4)), block(256);
 #define PARO_APPEND4(DT, DIM)                                                                                    \
-  hipLaunchKernelGGL((append4_kernel<DT, DIM>), grid, block, 0, st, kv, kv_heads, shares, k, k_token, k_head, v, v_token, \
-                     v_head, slots, cu, granted, n, tokens)
+  hipLaunchKernelGGL((append4_kernel<DT, DIM>), grid, block, 0, st, kv, kv_heads, shares, k, k_token, k_head, v, \
+                     v_token, v_head, slots, cu, granted, n, tokens)
   if (dt == kF16) {
     if (head_dim == 64) PARO_APPEND4(kF16, 64);
     else PARO_APPEND4(kF16, 128);
