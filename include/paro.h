@@ -702,8 +702,10 @@ size_t paro_attention_prompt_cached_workspace_bytes(const paro_kv_cache *cache, 
  *   repeated call gives identical bits.
  * Over a cache in four bits q and y are in the rows' type; scores are fp32 sums
  * over codes and pairs, queries are taken as fp16 times a power of two of their
- * row's (values below 2^-39 of the row's largest are lost), and what is rounded
- * to fp16, for either type, is the weights times the scales.
+ * row's (kept to 2^-35 of the row's largest), and what is rounded to fp16, for
+ * either type, is the weights times the scales.  There the rows share the card by
+ * their lengths, so the split, and with it the last bits of a result, depends on
+ * the lengths of all rows of the call; a repeated call gives identical bits.
  * rows <= 32768.
  */
 int paro_attention_decode(const paro_kv_cache *cache, int layer, const paro_attention_shape *shape, const void *q,
@@ -713,8 +715,8 @@ size_t paro_attention_decode_workspace_bytes(const paro_kv_cache *cache, int64_t
 
 /*
  * New K and V rows into the pages of one layer: rows cu[i]..cu[i+1] of k and
- * v [tokens][kv_heads][head_dim] (the rows' dtype: F16 or BF16 after the cache's; strides in elements as in
- * paro_attention_shape) become the newest positions of slot slots[i], i.e.
+ * v [tokens][kv_heads][head_dim] (the rows' dtype: F16 or BF16 after the cache's;
+ * strides in elements as in paro_attention_shape) become the newest positions of slot slots[i], i.e.
  * lengths[slots[i]] - (cu[i+1] - cu[i]) and up, which paro_kv_reserve has
  * granted before.  cu: DEVICE int64 [n + 1], or NULL for one row per entry
  * (tokens == n).  granted: DEVICE int32 [n], what paro_kv_reserve gave for the

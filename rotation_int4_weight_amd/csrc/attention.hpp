@@ -89,12 +89,11 @@ hipError_t launch_attention_decode(const AttentionArgs &a, const DecodeAttention
                                    float *partials, hipStream_t st);
 
 // The same over a cache in four bits: the keys of all rows together are dealt
-// out to the workgroups that the card holds at once, a counter and two slots for
-// parts each.
+// out to the workgroups that the card holds at once (two per CU), a counter and
+// two slots for parts each.
 constexpr int kMaxDealtRows = 1024;
-template <int DIM>
-constexpr int kDecode4Resident = DIM == 64 ? 2 : 2;  // workgroups per CU
-constexpr int kDecode4Counters = 256 * 4;
+constexpr int kDecode4Resident = 2;  // workgroups per CU
+constexpr int kDecode4Counters = 256 * kDecode4Resident;
 struct Decode4Plan {
   int head_tiles;  // as above
   int workgroups;

@@ -19,11 +19,35 @@
 //     two of their row's, those that meet bits 4..7 by 1/16 of it.
 //   - The layout of the pages (include/paro.h) is the order of the operands: a
 //     lane's 16 bytes of K are its share of one key's channels for every
-//     contraction step, its 16 bytes of V four keys of eight channels.  S^T and
-//     O^T fragments lie as in attention_decode.hip, with the head in lane % 16.
-//   - Pairs are loaded a word per lane and step, opened and shared through LDS.
-//   - What is rounded to fp16 is p s 2^(15 - ev), with 2^ev over every scale of V
-//     so far (and 2^-16 of every |low|: smaller scales than that add nothing).
+//     contraction step, its 16 bytes of V four keys of eight channels.
+//   - The first product has the key in lane % 16 and heads in its registers, so
+//     that a lane has the pairs of its own keys only: each lane loads one key's
+//     pairs of K or of V, and swaps of lane halves and quarters spread them.  The
+//     second has the head in lane % 16; the weights change places in LDS.
+//   - Running maximum m of score * log2 e, moved when a score rose by more than
+//     2^kSlack over it, and sum of the weights, both fp32.
+//   - What is rounded to fp16 is p s 2^(kTop - ev), with 2^ev over every scale of V
+//     so far: off by 2^-11 of itself, or 2^-(25 + kTop) of the largest scale,
+//     which is far less than what a 16-bit output shows.
+// Work is dealt out in units (kUnit keys of an output, an output being a row and
+// up to 16 query heads of a key-value head), so that the 512 workgroups that the
+// card holds end together whatever the rows' lengths are; see kOutputUnits,
+// kJoinUnits and plan_attention_decode4.
+//
+// What bounds it: where rows are long the bytes, 9/8 per key and channel (9/32 of
+// the 16-bit cache's): two rows of 131072 and 100001 keys (8 heads of 128
+// channels, 32 query heads, 266 MB) take 60 us, 4.4 TB/s, 64 rows of up to 4096
+// (141 MB) 42 us.  In its steady state the card takes in 5.1 to 5.6 TB/s (a copy
+// moves 4.8); 8 us are the start (look-ups of slot, length and table, then the
+// first keys: 3 us), the first step (2) and the join (3.4).  One row of 777 keys,
+// 8 outputs over 56 workgroups of one step each: 10 us, of which those are 8.
+// Both sides of the choices, us:
+//   - two workgroups per CU and one: 42 and 61 (64 rows), 60 and 89 (two rows);
+//     three or four leave too few registers, and spill.
+//   - a ring of two tiles and of three: 42 and 42.5, 60 and 62.
+//   - the younger workgroup of a CU ahead in every other step (s_setprio), and
+//     never: 42 and 44, 60 and 64.  The older one's waves go first otherwise, and
+//     ended after 41 us of a 51 us loop.
 #include <math.h>
 
 #include <algorithm>
@@ -40,10 +64,20 @@ namespace {
 
 constexpr int kStep = 32;                    // keys per wave and step
 constexpr int kUnit = kStep * kDecodeWaves;  // keys per workgroup and step
-constexpr int kWhole = 3;                    // units: where no row has more, shares hold whole rows
-constexpr int kOutputUnits = 3;              // what an output costs beside its steps, in steps
-constexpr int kTiles = 2;
-constexpr float kSlack = 3.f;                // a maximum moves when it rose by more than 2^kSlack
+// What an output costs beside its steps, in steps: its start and its end (0, 3
+// and 6: 59, 42 and 44 us for 64 rows of up to 4096; 10.4, 11.3 and 11.3 us for 40
+// rows of up to 1500 with 2 heads).
+constexpr int kOutputUnits = 3;
+// Outputs are cut where a workgroup's share ends, at the cost of a join, unless
+// the longest one has at most kWhole steps and is no longer than a share and
+// kJoinUnits together.  Cut and whole, us: 30 rows of 100 keys 11.0 and 8.8, 30 of
+// up to 400 15.3 and 11.2, 64 of up to 700 19.0 and 17.5, one of 384 9.6 and 9.5;
+// but 30 of up to 1000 15.4 and 17, one of 777 10.0 and 12.9, 300 of up to 3000
+// 122 and 131.
+constexpr int kJoinUnits = 5;
+constexpr int kWhole = 7;
+constexpr int kTiles = 2;                    // of a wave's ring
+constexpr float kSlack = 3.f;                // a maximum moves when a score rose by more than 2^kSlack over it
 constexpr int kTop = 12;                     // weights times scales stay under 2^(kTop + kSlack) in fp16
 constexpr float kLeastMaximum = -3e38f;      // scores that fp32 does not hold weigh nothing, also among themselves
 constexpr int kLeastExponent = -126;         // of the values' scale
@@ -407,8 +441,8 @@ __device__ __forceinline__ void open_query(Query<DIM> &q, const u32x4 (&raw)[DIM
 // How a call's work is dealt out (see plan_attention_decode4): rows one after
 // another, each row's outputs (key-value heads, head tiles) one after another, an
 // output being kOutputUnits for its start and end and a unit per kUnit keys (an
-// empty row has one).  A workgroup takes `share` units in a row; the steps of an
-// output begin kOutputUnits behind its first unit.
+// empty row has one).  A workgroup takes `share` units one after another; the
+// steps of an output begin kOutputUnits behind its first unit.
 __device__ __forceinline__ int units_of(int len) { return max(1, (len + kUnit - 1) / kUnit); }
 
 // The sum of the lanes up to this one.
@@ -446,7 +480,7 @@ struct Piece {
 };
 
 template <int DT, int DIM>
-__global__ void __launch_bounds__(256, kDecode4Resident<DIM>)
+__global__ void __launch_bounds__(256, kDecode4Resident)
 decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict__ counters,
                          float *__restrict__ partials) {
   constexpr int G = DIM / 64;
@@ -455,18 +489,22 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
   const int outputs = a.kv_heads * plan.head_tiles;  // of a row
   const int rows = a.sequences;
-  // A CU's second workgroup: the first one's waves go before its own (and ended
-  // after 41 us of a 51 us loop), so it takes the lead in every other step.
+  // a CU's second workgroup, which takes the lead in every other step (see the header)
   const bool young = blockIdx.x >= 256;
   // this workgroup's units at..until, in row `row`, whose first is `before`
   int64_t at, until, share, before;
-  int row, lane_slot = 0, lane_len = 0;
-  const bool in_lanes = plan.dealt && rows <= 64;  // lane: row
+  bool cut = false;  // outputs are cut where a share ends; else they are the workgroup's that has their first unit
+  int row, row0 = 0, lane_slot = 0, lane_len = 0;  // lane: row row0 + lane
+  const auto look_at = [&](int first) {
+    row0 = first;
+    lane_slot = a.slots[min(first + lane, rows - 1)];
+    lane_len = a.kv.length(lane_slot);
+  };
   if (plan.dealt) {
     // every wave for itself: a lane takes `per` rows
     const int per = (rows + 63) >> 6, first = lane * per;
     int units = 0;
-    bool some = false;  // a row that is worth cutting
+    int longest = 0;
     for (int j0 = 0; j0 < per; j0 += 4) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -476,36 +514,45 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
           lane_len = a.kv.length(lane_slot);
           const int n = units_of(lane_len);
           units += n + kOutputUnits;
-          some |= n > kWhole;
+          longest = max(longest, n);
         }
       }
     }
     const int sum = inclusive_sum(units);
     const int64_t total = (int64_t)__builtin_amdgcn_readlane(sum, 63) * outputs;
     share = quotient(total + gridDim.x - 1, gridDim.x);
-    share = max(share, (int64_t)(__any(some) ? 1 : kOutputUnits + kWhole));
+    cut = __any(longest > min(kWhole, (int)min(share, (int64_t)kWhole) + kJoinUnits - kOutputUnits));
     at = blockIdx.x * share;
     until = min(total, at + share);
     if (at >= total) return;
     // the lane that has the row of the first unit, then the row
     const int unit = (int)quotient(at, outputs);
-    const uint64_t over = __ballot(sum > unit);
-    const int who = __ffsll((unsigned long long)over) - 1;
-    int start = __builtin_amdgcn_readlane(sum - units, who);
-    row = who * per;
+    int who = __ffsll((unsigned long long)__ballot(sum > unit)) - 1;
+    int end = sum, begin = 0;
     if (per > 1) {
-      while (true) {
-        const int n = units_of(a.kv.length(a.slots[row])) + kOutputUnits;
-        if (start + n > unit || row + 1 >= rows) break;
-        start += n;
+      begin = __builtin_amdgcn_readlane(sum - units, who);
+      look_at(who * per);
+      units = row0 + lane < rows ? units_of(lane_len) + kOutputUnits : 0;
+      end = begin + inclusive_sum(units);
+      who = __ffsll((unsigned long long)__ballot(end > unit)) - 1;
+    }
+    row = row0 + who;
+    before = __builtin_amdgcn_readlane(end - units, who);
+    if (!cut) {
+      const int all = __builtin_amdgcn_readlane(units_of(lane_len), who) + kOutputUnits;
+      const int skip = (int)((uint32_t)(at - before * outputs) % (uint32_t)all);
+      at += skip ? all - skip : 0;
+      if (at >= until) return;
+      if (at >= (before + all) * outputs) {
+        before += all;
         ++row;
       }
     }
-    before = start;
   } else {
     // a workgroup per output
     row = (int)(blockIdx.x / (unsigned)outputs);
-    const int n = units_of(a.kv.length(a.slots[row])) + kOutputUnits;
+    look_at(row);
+    const int n = units_of(__builtin_amdgcn_readfirstlane(lane_len)) + kOutputUnits;
     before = 0;
     share = n;
     at = (int64_t)(blockIdx.x % (unsigned)outputs) * n;
@@ -519,13 +566,14 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
     Piece p;
     p.row = row;
     p.before = before;
-    p.slot = in_lanes ? __builtin_amdgcn_readlane(lane_slot, row) : a.slots[row];
-    p.len = in_lanes ? __builtin_amdgcn_readlane(lane_len, row) : a.kv.length(p.slot);
+    if (row - row0 >= 64) look_at(row);
+    p.slot = __builtin_amdgcn_readlane(lane_slot, row - row0);
+    p.len = __builtin_amdgcn_readlane(lane_len, row - row0);
     p.steps = units_of(p.len);
     const int all = p.steps + kOutputUnits;
     const uint32_t rel = (uint32_t)(at - before * outputs);
     const int output = (int)(rel / (uint32_t)all), skip = (int)(rel - (uint32_t)output * all);
-    const int take = (int)min((int64_t)(all - skip), until - at);
+    const int take = cut ? (int)min((int64_t)(all - skip), until - at) : all;
     const int step0 = max(0, skip - kOutputUnits), step1 = skip + take - kOutputUnits;
     p.none = step1 <= 0;
     p.whole = step1 - step0 == p.steps;
@@ -683,7 +731,7 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
         part = (int)blockIdx.x - place.first;
         parts = (int)quotient(done.first + done.steps - 1, share) - place.first + 1;
       }
-      join_parts<DT, DIM, 8>(a, lds, counters + place.first, rs, place, done.row, done.head0, done.heads, part, parts,
+      join_parts<DT, DIM>(a, lds, counters + place.first, rs, place, done.row, done.head0, done.heads, part, parts,
                           done.len > 0);
     }
     if (!more) break;
@@ -695,15 +743,17 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
 
 // Rows of up to kMaxDealtRows have their units dealt out in equal shares to as
 // many workgroups as the card holds at once, so that the longest row ends with
-// the others; more rows than that are a workgroup for each (row, output).
+// the others; more rows than that, whose lengths take too long to look up in
+// every workgroup, are a workgroup for each output.  Dealt and not, us: 64 rows of
+// up to 4096 42 and 52, rows of 131072 and 100001 60 and 1177, 1000 of up to 500
+// 129 and 126, 2000 of up to 300 230 and 206.
 Decode4Plan plan_attention_decode4(int64_t rows, int q_heads, int kv_heads, int head_dim, int64_t max_len) {
   Decode4Plan p;
   p.head_tiles = (q_heads / kv_heads + 15) / 16;
   const int64_t outputs = rows * kv_heads * p.head_tiles;
   const int64_t units = std::max<int64_t>(1, (max_len + kUnit - 1) / kUnit), most = outputs * (units + kOutputUnits);
   p.dealt = rows <= kMaxDealtRows && rows * (units + kOutputUnits) < int64_t(1) << 31;  // (the sums' type)
-  const int resident = 256 * (head_dim == 64 ? kDecode4Resident<64> : kDecode4Resident<128>);
-  p.workgroups = (int)(p.dealt ? std::min<int64_t>(most, resident) : outputs);
+  p.workgroups = (int)(p.dealt ? std::min<int64_t>(most, 256 * kDecode4Resident) : outputs);
   return p;
 }
 

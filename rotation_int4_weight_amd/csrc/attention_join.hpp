@@ -14,6 +14,9 @@ namespace paro {
 
 constexpr int kDecodeWaves = 4;  // of a decode workgroup
 constexpr int kCoherent = 16;    // SC1: device-scope loads and stores of the parts
+// Parts that a thread has in flight together (with 16 the kernel over four bits
+// spills registers).
+constexpr int kJoinBatch = 8;
 
 // What the waves hand over: sums relative to 2^m, m the maximum of scores * log2 e.
 template <int DIM>
@@ -70,8 +73,9 @@ __host__ __device__ inline int part_floats(int group, int dim) { return (group <
 // Called by all threads once every wave has written its o, m and l (no barrier
 // needed in between): part `part` of `parts` of the `heads` query heads from
 // head0 of a row.  counter: this output's; rs: the slots (neither is used with
-// one part).  BATCH parts are loaded together by each thread.  some: the row has a key; without one it is zero.
-template <int DT, int DIM, int BATCH, class Place>
+// one part).  some: the row has a key; without one it is zero.  Storing a part,
+// counting and joining takes 2 to 3.4 us.
+template <int DT, int DIM, class Place>
 __device__ __forceinline__ void join_parts(const AttentionArgs &a, DecodeJoin<DIM> &lds, uint32_t *counter,
                                            __amdgpu_buffer_rsrc_t rs, Place place_of, int64_t row, int head0,
                                            int heads, int part, int parts, bool some) {
@@ -119,7 +123,7 @@ __device__ __forceinline__ void join_parts(const AttentionArgs &a, DecodeJoin<DI
   __syncthreads();
   if (!lds.last) return;
   // DIM / 4 threads per head leave room for `lanes` of them per output: each
-  // takes every lanes-th part, BATCH loads in flight together
+  // takes every lanes-th part, kJoinBatch loads in flight together
   const int lanes = max(1, kHeadsPerPass / heads);
   const int sub = (int)threadIdx.x / kPerHead;
   float *const jo = &lds.o[0][0][0];  // [sub][RS], after the waves' use of o
@@ -128,17 +132,17 @@ __device__ __forceinline__ void join_parts(const AttentionArgs &a, DecodeJoin<DI
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, sum = 0.f;
     if (h < heads) {
-      for (int p0 = first; p0 < parts; p0 += BATCH * lanes) {
-        f32x4 x[BATCH];
-        u32x2 ml[BATCH];
+      for (int p0 = first; p0 < parts; p0 += kJoinBatch * lanes) {
+        f32x4 x[kJoinBatch];
+        u32x2 ml[kJoinBatch];
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u) {
+        for (int u = 0; u < kJoinBatch; ++u) {
           const uint32_t at = (uint32_t)(place_of(min(p0 + u * lanes, parts - 1)) * slot_floats + h * (DIM + 4)) * 4u;
           x[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at + ch * 4, 0, kCoherent));
           ml[u] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, at + DIM * 4, 0, kCoherent));
         }
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u)
+        for (int u = 0; u < kJoinBatch; ++u)
           if (p0 + u * lanes < parts) add_part(o, m, sum, x[u], __uint_as_float(ml[u][0]), __uint_as_float(ml[u][1]));
       }
     }
