@@ -139,33 +139,35 @@ __device__ __forceinline__ Pairs<DIM> spread(const typename Words<DIM / 64>::typ
 }
 
 // A lane's head in the second product is lane % 16; in the first one a lane has
-// key lane % 16 and the heads 4 g .. 4 g + 3, g = lane / 16.
-template <int DIM>
+// key lane % 16 and N heads, g, g + 4, .. with g = lane / 16: head h of the queries
+// is row 4 (h % 4) + h / 4 of the operand, so that few heads fill few registers.
+template <int DIM, int N>
 struct State {
   static constexpr int G = DIM / 64;
   // o[u][n][i]: the first sum of channel 64 u + 16 g + 4 i + n of head lane % 16,
   // times 2^(kTop - ev - 24) (n odd: 2^(kTop - ev - 20))
   f32x4 o[G][4];
-  // of heads 4 g + i, over keys lane % 16 of each block: sums of weights times mid, and of weights
-  f32x4 mids[G], l;
-  f32x4 m;  // weights are exp2(score * log2 e - m), at most 2^kSlack
-  int ev;   // 2^ev: over the scales of V
+  // of heads g + 4 i, over keys lane % 16 of each block: sums of weights times mid, and of weights
+  float mids[G][N], l[N];
+  float m[N];  // weights are exp2(score * log2 e - m), at most 2^kSlack
+  int ev;      // 2^ev: over the scales of V
 };
 
 // Weights of one u for the second product, [head][key], keys in the order in
 // which a lane takes them: 4 g .. 4 g + 3 of the first block, then of the second.
 constexpr int kWeightRow = 40;  // halves: rows of four lanes apart lie on different banks
 
-// A row's queries: their fp16 fragments (head lane % 16), and for heads 4 g + i
+// A row's queries: their fp16 fragments (head query_of(lane)), and for heads g + 4 i
 // 2^-24 times their sums by group, and what makes scores * log2 e of a product: a
 // factor >= 0, times 2^rest where `more` (for the wave) says that it is not 1.
-template <int DIM>
+template <int DIM, int N>
 struct Query {
   u32x4 w[DIM / 32];
-  f32x4 sum[DIM / 64], factor;
-  int rest[4];
+  float sum[DIM / 64][N], factor[N];
+  int rest[N];
   bool more;
 };
+__device__ __forceinline__ int query_of(int lane) { return (lane >> 2 & 3) + 4 * (lane & 3); }
 
 // codes of the even (bits 0..3, 8..11) or odd (4..7, 12..15) nibble of 16-bit
 // halves as fp16: n = 0..3 from the lowest
@@ -203,9 +205,10 @@ __device__ __forceinline__ float sum16(float x) {
 }
 
 // The products of one step's 32 keys with the queries, times `factor` (and
-// 2^rest): x[b][i] of key 16 b + lane % 16 and head 4 g + i.
-template <int DT, int DIM>
-__device__ __forceinline__ void scores(f32x4 (&x)[2], const Tile<DIM> &t, const Pairs<DIM> &p, const Query<DIM> &q) {
+// 2^rest): x[b][i] of key 16 b + lane % 16 and head g + 4 i.
+template <int DT, int DIM, int N>
+__device__ __forceinline__ void scores(float (&x)[2][N], const Tile<DIM> &t, const Pairs<DIM> &p,
+                                       const Query<DIM, N> &q) {
   constexpr int G = DIM / 64;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
@@ -221,7 +224,7 @@ __device__ __forceinline__ void scores(f32x4 (&x)[2], const Tile<DIM> &t, const 
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       float s = 0.f;
 #pragma unroll
       for (int u = 0; u < G; ++u) {
@@ -237,20 +240,21 @@ __device__ __forceinline__ void scores(f32x4 (&x)[2], const Tile<DIM> &t, const 
 
 // The maxima rise: weights, sums and outputs so far are made relative to the new
 // ones.  keeps: 16 floats of the wave's.
-template <int DIM>
-__device__ __forceinline__ void raise(State<DIM> &st, const f32x4 (&x)[2], const Query<DIM> &q, float *keeps, int lane) {
+template <int DIM, int N>
+__device__ __forceinline__ void raise(State<DIM, N> &st, const float (&x)[2][N], const Query<DIM, N> &q, float *keeps,
+                                      int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < N; ++i) {
     const float m = fmaxf(st.m[i], max16(fmaxf(x[0][i], x[1][i])) * q.factor[i]);
     const float keep = m == st.m[i] ? 1.f : __builtin_amdgcn_exp2f(st.m[i] - m);
     st.m[i] = m;
     st.l[i] *= keep;
 #pragma unroll
     for (int u = 0; u < DIM / 64; ++u) st.mids[u][i] *= keep;
-    if ((lane & 15) == 0) keeps[4 * (lane >> 4) + i] = keep;
+    if ((lane & 15) == 0) keeps[(lane >> 4) + 4 * i] = keep;
   }
   wave_lds_sync();
-  const float keep = keeps[lane & 15];
+  const float keep = keeps[(lane & 15) & (4 * N - 1)];  // (other lanes' sums are not used)
   wave_lds_sync();
 #pragma unroll
   for (int u = 0; u < DIM / 64; ++u)
@@ -267,9 +271,9 @@ __device__ __forceinline__ int exponent_over(int ev, float size) {
 
 // Weights of the scores x, into the sums and, times the scales of V, into `lds`
 // (2^(kTop - ev) p s in fp16).  FRESH: the first step.
-template <int DT, int DIM, bool FRESH>
-__device__ __forceinline__ void weigh(State<DIM> &st, f32x4 (&x)[2], const Pairs<DIM> &pairs,
-                                      const Query<DIM> &q, uint16_t *lds, bool end, int live, int lane) {
+template <int DT, int DIM, int N, bool FRESH>
+__device__ __forceinline__ void weigh(State<DIM, N> &st, float (&x)[2][N], const Pairs<DIM> &pairs,
+                                      const Query<DIM, N> &q, uint16_t *lds, bool end, int live, int lane) {
   constexpr int G = DIM / 64;
   float vs[2][G], mid[2][G];
   float size = 0.f;
@@ -303,66 +307,66 @@ __device__ __forceinline__ void weigh(State<DIM> &st, f32x4 (&x)[2], const Pairs
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[b][i] = ldexpf(x[b][i], q.rest[i]);
+      for (int i = 0; i < N; ++i) x[b][i] = ldexpf(x[b][i], q.rest[i]);
   }
   if (end) {  // (uniform) dead keys do not raise a maximum
     asm volatile("");
 #pragma unroll
     for (int b = 0; b < 2; ++b)
-      if (16 * b + (lane & 15) >= live) x[b] = f32x4{-3e38f, -3e38f, -3e38f, -3e38f};
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[b][i] = 16 * b + (lane & 15) >= live ? -3e38f : x[b][i];
   }
-  f32x4 w[2];
+  float w[2][N];
   float top = -INFINITY;
 #pragma unroll
   for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       w[b][i] = __builtin_fmaf(x[b][i], q.factor[i], -st.m[i]);
       top = fmaxf(top, w[b][i]);
     }
   if (FRESH || __any(top > kSlack)) {
     if constexpr (FRESH) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st.m[i] = fmaxf(max16(fmaxf(x[0][i], x[1][i])) * q.factor[i], kLeastMaximum);
+      for (int i = 0; i < N; ++i) st.m[i] = fmaxf(max16(fmaxf(x[0][i], x[1][i])) * q.factor[i], kLeastMaximum);
     } else {
-      raise<DIM>(st, x, q, reinterpret_cast<float *>(lds), lane);
+      raise<DIM, N>(st, x, q, reinterpret_cast<float *>(lds), lane);
     }
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[b][i] = __builtin_fmaf(x[b][i], q.factor[i], -st.m[i]);
+      for (int i = 0; i < N; ++i) w[b][i] = __builtin_fmaf(x[b][i], q.factor[i], -st.m[i]);
   }
 #pragma unroll
   for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[b][i] = __builtin_amdgcn_exp2f(w[b][i]);
+    for (int i = 0; i < N; ++i) w[b][i] = __builtin_amdgcn_exp2f(w[b][i]);
   if (end) {
     asm volatile("");
 #pragma unroll
     for (int b = 0; b < 2; ++b)
-      if (16 * b + (lane & 15) >= live) w[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[b][i] = 16 * b + (lane & 15) >= live ? 0.f : w[b][i];
   }
-  st.l += w[0] + w[1];
+#pragma unroll
+  for (int i = 0; i < N; ++i) st.l[i] += w[0][i] + w[1][i];
   // key 16 b + 4 j + k of a block stands at 8 j + 4 b + k
-  uint16_t *to = lds + (4 * (lane >> 4)) * kWeightRow + 8 * (lane >> 2 & 3) + (lane & 3);
+  uint16_t *to = lds + (lane >> 4) * kWeightRow + 8 * (lane >> 2 & 3) + (lane & 3);
 #pragma unroll
   for (int u = 0; u < G; ++u)
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      st.mids[u] += w[b] * mid[b][u];
-      const f32x4 r = w[b] * vs[b][u];
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const uint32_t h = __builtin_bit_cast(uint32_t, f16x2{(_Float16)r[i], (_Float16)r[i + 1]});
-        to[(16 * u + i) * kWeightRow + 4 * b] = (uint16_t)h;
-        to[(16 * u + i + 1) * kWeightRow + 4 * b] = (uint16_t)(h >> 16);
-      }
+    for (int i = 0; i < N; ++i) {
+      st.mids[u][i] = __builtin_fmaf(w[0][i], mid[0][u], __builtin_fmaf(w[1][i], mid[1][u], st.mids[u][i]));
+      const uint32_t h =
+          __builtin_bit_cast(uint32_t, f16x2{(_Float16)(w[0][i] * vs[0][u]), (_Float16)(w[1][i] * vs[1][u])});
+      to[(16 * u + 4 * i) * kWeightRow] = (uint16_t)h;
+      to[(16 * u + 4 * i) * kWeightRow + 4] = (uint16_t)(h >> 16);
     }
 }
 
 // The second product.
-template <int DIM>
-__device__ __forceinline__ void add_values(State<DIM> &st, const typename Words<DIM / 32>::type (&codes)[2],
+template <int DIM, int N>
+__device__ __forceinline__ void add_values(State<DIM, N> &st, const typename Words<DIM / 32>::type (&codes)[2],
                                            const uint16_t *lds, int lane) {
 #pragma unroll
   for (int u = 0; u < DIM / 64; ++u) {
@@ -376,24 +380,24 @@ __device__ __forceinline__ void add_values(State<DIM> &st, const typename Words<
   }
 }
 
-// Lane: head lane%16, channels 32 x + 8 g..; unused heads repeat the last one.
+// Lane: head query_of(lane), channels 32 x + 8 g..; unused heads repeat the last one.
 template <int DIM>
 __device__ __forceinline__ void load_query(u32x4 (&raw)[DIM / 32], const AttentionArgs &a, int64_t row, int head0,
                                            int heads, int lane) {
   const uint16_t *qp =
-      a.q + row * a.q_token + (int64_t)(head0 + min(lane & 15, heads - 1)) * a.q_head + 8 * (lane >> 4);
+      a.q + row * a.q_token + (int64_t)(head0 + min(query_of(lane), heads - 1)) * a.q_head + 8 * (lane >> 4);
 #pragma unroll
   for (int x = 0; x < DIM / 32; ++x) raw[x] = *reinterpret_cast<const u32x4 *>(qp + 32 * x);
 }
 
-template <int DT, int DIM>
-__device__ __forceinline__ void open_query(Query<DIM> &q, const u32x4 (&raw)[DIM / 32], float scale, int heads,
+template <int DT, int DIM, int N>
+__device__ __forceinline__ void open_query(Query<DIM, N> &q, const u32x4 (&raw)[DIM / 32], float scale, int heads,
                                            int lane) {
   constexpr int G = DIM / 64, KS = DIM / 32;
   float most = 0.f;
 #pragma unroll
   for (int x = 0; x < KS; ++x) {
-    q.w[x] = (lane & 15) < heads ? raw[x] : u32x4{0, 0, 0, 0};
+    q.w[x] = query_of(lane) < heads ? raw[x] : u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(act_to_f32<DT>(q.w[x][j / 2] >> (16 * (j & 1)) & 0xffffu)));
   }
@@ -424,15 +428,15 @@ __device__ __forceinline__ void open_query(Query<DIM> &q, const u32x4 (&raw)[DIM
   const int rest = scale2 > 0.f ? shift - part : 0;
   const float factor = scale2 > 0.f ? ldexpf(scale2, part) : 0.f;
   q.more = __any(rest != 0);
-  // from head lane % 16 to heads 4 g + i
+  // from rows lane % 16 to rows 4 g + i, heads g + 4 i
 #pragma unroll
   for (int u = 0; u < G; ++u) {
     const float all = sum_over_groups(sum[u]) * 0x1p-24f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q.sum[u][i] = __shfl(all, 4 * (lane >> 4) + i, 64);
+    for (int i = 0; i < N; ++i) q.sum[u][i] = __shfl(all, 4 * (lane >> 4) + i, 64);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < N; ++i) {
     q.factor[i] = __shfl(factor, 4 * (lane >> 4) + i, 64);
     q.rest[i] = __shfl(rest, 4 * (lane >> 4) + i, 64);
   }
@@ -479,7 +483,7 @@ struct Piece {
   bool whole, none;    // none: only units that stand for an output's start
 };
 
-template <int DT, int DIM>
+template <int DT, int DIM, int N>
 __global__ void __launch_bounds__(256, kDecode4Resident)
 decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict__ counters,
                          float *__restrict__ partials) {
@@ -636,20 +640,24 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
     const int end = piece.end;
     const bool none = piece.none;
     if (!none) {
-      State<DIM> st;
-      st.m = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      st.l = f32x4{0.f, 0.f, 0.f, 0.f};
+      State<DIM, N> st;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        st.m[i] = -INFINITY;
+        st.l[i] = 0.f;
+      }
 #pragma unroll
       for (int u = 0; u < G; ++u) {
-        st.mids[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < N; ++i) st.mids[u][i] = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) st.o[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
       st.ev = kLeastExponent;
       if (pos < end) {
         uint16_t *weights = reinterpret_cast<uint16_t *>(&lds.o[wave][0][0]);
-        Query<DIM> q;
-        open_query<DT, DIM>(q, raw, a.scale, piece.heads, lane);
+        Query<DIM, N> q;
+        open_query<DT, DIM, N>(q, raw, a.scale, piece.heads, lane);
         bool more = true;
         const auto turn = [&](Tile<DIM> &now, Tile<DIM> &ahead, auto fresh) {
           const int live = end - pos;  // keys of this step: more than there are but at the end
@@ -666,11 +674,11 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
             if (&now == &t[0]) __builtin_amdgcn_s_setprio(1);
             else __builtin_amdgcn_s_setprio(0);
           }
-          f32x4 x[2];
-          scores<DT, DIM>(x, now, pairs, q);
-          weigh<DT, DIM, decltype(fresh)::value>(st, x, pairs, q, weights, tail, live, lane);
+          float x[2][N];
+          scores<DT, DIM, N>(x, now, pairs, q);
+          weigh<DT, DIM, N, decltype(fresh)::value>(st, x, pairs, q, weights, tail, live, lane);
           wave_lds_sync();
-          add_values<DIM>(st, now.v, weights, lane);
+          add_values<DIM, N>(st, now.v, weights, lane);
           wave_lds_sync();
           pos += kUnit;
           more = live > kUnit;
@@ -686,26 +694,26 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
       }
       // ---- join the waves ----
       {
-        // heads 4 g + i, over 16 lanes; then head lane % 16
+        // heads g + 4 i, over 16 lanes; then head lane % 16
         float *own = &lds.o[wave][0][0];  // [quantity][head]
         const int h = lane & 15, g = lane >> 4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < N; ++i) {
           const float l = sum16(st.l[i]);
           float mids[G];
 #pragma unroll
           for (int u = 0; u < G; ++u) mids[u] = sum16(st.mids[u][i]);
           if (h == 0) {
-            lds.m[wave][4 * g + i] = st.m[i];
-            lds.l[wave][4 * g + i] = l;
+            lds.m[wave][g + 4 * i] = st.m[i];
+            lds.l[wave][g + 4 * i] = l;
 #pragma unroll
-            for (int u = 0; u < G; ++u) own[16 * u + 4 * g + i] = mids[u];
+            for (int u = 0; u < G; ++u) own[16 * u + g + 4 * i] = mids[u];
           }
         }
         wave_lds_sync();
         float mids[G];
 #pragma unroll
-        for (int u = 0; u < G; ++u) mids[u] = own[16 * u + h];
+        for (int u = 0; u < G; ++u) mids[u] = own[16 * u + (h & (4 * N - 1))];
         wave_lds_sync();
         if (h < piece.heads) {
 #pragma unroll
@@ -764,14 +772,26 @@ size_t attention_decode4_partial_bytes(const Decode4Plan &p, int q_heads, int kv
 hipError_t launch_attention_decode4(const AttentionArgs &a, const Decode4Plan &p, uint32_t *counters,
                                     float *partials, hipStream_t st) {
   const dim3 grid((unsigned)p.workgroups);
-#define PARO_DECODE4(DT, DIM) \
-  hipLaunchKernelGGL((decode4_attention_kernel<DT, DIM>), grid, dim3(256), 0, st, a, p, counters, partials)
+  const int heads = std::min(a.group, 16);
+#define PARO_DECODE4(DT, DIM)                                                                                        \
+  if (heads <= 4)                                                                                                    \
+    hipLaunchKernelGGL((decode4_attention_kernel<DT, DIM, 1>), grid, dim3(256), 0, st, a, p, counters, partials);     \
+  else if (heads <= 8)                                                                                               \
+    hipLaunchKernelGGL((decode4_attention_kernel<DT, DIM, 2>), grid, dim3(256), 0, st, a, p, counters, partials);     \
+  else                                                                                                               \
+    hipLaunchKernelGGL((decode4_attention_kernel<DT, DIM, 4>), grid, dim3(256), 0, st, a, p, counters, partials)
   if (a.dt == kF16) {
-    if (a.head_dim == 64) PARO_DECODE4(kF16, 64);
-    else PARO_DECODE4(kF16, 128);
+    if (a.head_dim == 64) {
+      PARO_DECODE4(kF16, 64);
+    } else {
+      PARO_DECODE4(kF16, 128);
+    }
   } else {
-    if (a.head_dim == 64) PARO_DECODE4(kBF16, 64);
-    else PARO_DECODE4(kBF16, 128);
+    if (a.head_dim == 64) {
+      PARO_DECODE4(kBF16, 64);
+    } else {
+      PARO_DECODE4(kBF16, 128);
+    }
   }
 #undef PARO_DECODE4
   return hipGetLastError();
