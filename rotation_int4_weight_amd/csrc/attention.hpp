@@ -97,7 +97,8 @@ constexpr int kDecode4Counters = 256 * kDecode4Resident;
 struct Decode4Plan {
   int head_tiles;  // as above
   int workgroups;
-  bool dealt;      // false: a workgroup per row, key-value head and head tile
+  bool dealt;      // false: a workgroup per output, that is row, key-value head and head tile
+  int whole;       // the same where no row has more units than this
 };
 Decode4Plan plan_attention_decode4(int64_t rows, int q_heads, int kv_heads, int head_dim, int64_t max_len);
 size_t attention_decode4_partial_bytes(const Decode4Plan &p, int q_heads, int kv_heads, int head_dim);

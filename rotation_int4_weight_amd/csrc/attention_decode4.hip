@@ -32,22 +32,27 @@
 // Work is dealt out in units (kUnit keys of an output, an output being a row and
 // up to 16 query heads of a key-value head), so that the 512 workgroups that the
 // card holds end together whatever the rows' lengths are; see kOutputUnits,
-// kJoinUnits and plan_attention_decode4.
+// kWhole and plan_attention_decode4.
 //
 // What bounds it: where rows are long the bytes, 9/8 per key and channel (9/32 of
 // the 16-bit cache's): two rows of 131072 and 100001 keys (8 heads of 128
-// channels, 32 query heads, 266 MB) take 60 us, 4.4 TB/s, 64 rows of up to 4096
-// (141 MB) 42 us.  In its steady state the card takes in 5.1 to 5.6 TB/s (a copy
-// moves 4.8); 8 us are the start (look-ups of slot, length and table, then the
-// first keys: 3 us), the first step (2) and the join (3.4).  One row of 777 keys,
-// 8 outputs over 56 workgroups of one step each: 10 us, of which those are 8.
+// channels, 32 query heads, 266 MB) take 59 us, 4.5 TB/s, 64 rows of up to 4096
+// (141 MB) 37.4 us.  In its steady state the card takes in 5.2 to 5.6 TB/s (a copy
+// moves 4.8); about 7 us are the start (look-ups of slot, length and table, then
+// the first keys), the first step and the join.  One row of 777 keys, 8 outputs
+// over 56 workgroups of one step each: 9.5 us, of which those are 7.
 // Both sides of the choices, us:
-//   - two workgroups per CU and one: 42 and 61 (64 rows), 60 and 89 (two rows);
-//     three or four leave too few registers, and spill.
-//   - a ring of two tiles and of three: 42 and 42.5, 60 and 62.
+//   - two workgroups per CU and one: 37 and 52 (64 rows), 59 and 77 (two rows);
+//     three: 43 and 67, the registers of two tiles and the sums no longer fit.
+//   - a ring of two tiles and of three: 37.4 and 37.6, 59.2 and 60.4.
 //   - the younger workgroup of a CU ahead in every other step (s_setprio), and
-//     never: 42 and 44, 60 and 64.  The older one's waves go first otherwise, and
-//     ended after 41 us of a 51 us loop.
+//     never: 37.4 and 38.5, 59.3 and 60.6.  The older one's waves go first
+//     otherwise, and ended after 41 us of a 51 us loop.
+//   - a lane with the pairs of its own four keys loaded, and spread by swaps from
+//     one load: the same time.
+//   - heads in every fourth row of the first product's operand, N registers of
+//     them, and four registers whatever the heads: 37.4 and 39.2, 300 rows of up
+//     to 1000 47 and 50.4.
 #include <math.h>
 
 #include <algorithm>
@@ -65,15 +70,14 @@ namespace {
 constexpr int kStep = 32;                    // keys per wave and step
 constexpr int kUnit = kStep * kDecodeWaves;  // keys per workgroup and step
 // What an output costs beside its steps, in steps: its start and its end (0, 3
-// and 6: 59, 42 and 44 us for 64 rows of up to 4096; 10.4, 11.3 and 11.3 us for 40
-// rows of up to 1500 with 2 heads).
+// and 6: 47.5, 37.4 and 39.2 us for 64 rows of up to 4096, 62, 47 and 50.5 for 300
+// of up to 1000; 2 and 4 as 3).
 constexpr int kOutputUnits = 3;
-// Outputs are cut where a workgroup's share ends, at the cost of a join, unless
-// the longest one has at most kWhole steps and is no longer than a share and
-// kJoinUnits together.  Cut and whole, us: 30 rows of 100 keys 11.0 and 8.8, 30 of
-// up to 400 15.3 and 11.2, 64 of up to 700 19.0 and 17.5, one of 384 9.6 and 9.5;
-// but 30 of up to 1000 15.4 and 17, one of 777 10.0 and 12.9, 300 of up to 3000
-// 122 and 131.
+// Where there are more outputs than workgroups they are cut where a share ends,
+// at the cost of a join, unless the longest one has at most kWhole steps and is no
+// longer than a share and kJoinUnits together.  Cut and whole, us: 300 rows of up
+// to 300 keys 33.2 and 30.9, 1000 of up to 500 104.5 and 103.5; but 300 of up to
+// 1000 47 and 49, 300 of up to 3000 109 and 116.
 constexpr int kJoinUnits = 5;
 constexpr int kWhole = 7;
 constexpr int kTiles = 2;                    // of a wave's ring
@@ -460,11 +464,6 @@ __device__ __forceinline__ int inclusive_sum(int x) {
   return x;
 }
 
-// a / b for 0 <= a, 0 < b
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
 // The slots of an output's parts: a workgroup's second slot has what it began
 // and did not end, its first what it went on with.
 struct DealtParts {
@@ -478,8 +477,7 @@ struct Piece {
   int steps;           // of the row
   int begin, end;      // the piece's keys
   int kvh, heads, head0;
-  int64_t before;      // units before the row's, over the number of outputs
-  int64_t first;       // the output's first step
+  uint32_t first;      // the output's first step, in units
   bool whole, none;    // none: only units that stand for an output's start
 };
 
@@ -495,8 +493,9 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
   const int rows = a.sequences;
   // a CU's second workgroup, which takes the lead in every other step (see the header)
   const bool young = blockIdx.x >= 256;
-  // this workgroup's units at..until, in row `row`, whose first is `before`
-  int64_t at, until, share, before;
+  // this workgroup's units at..until, in row `row`, whose first is before * outputs
+  // (the host has seen that all of a call's units are fewer than 2^31)
+  uint32_t at, until, share = 1, before = 0;
   bool cut = false;  // outputs are cut where a share ends; else they are the workgroup's that has their first unit
   int row, row0 = 0, lane_slot = 0, lane_len = 0;  // lane: row row0 + lane
   const auto look_at = [&](int first) {
@@ -504,11 +503,10 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
     lane_slot = a.slots[min(first + lane, rows - 1)];
     lane_len = a.kv.length(lane_slot);
   };
-  if (plan.dealt) {
-    // every wave for itself: a lane takes `per` rows
-    const int per = (rows + 63) >> 6, first = lane * per;
-    int units = 0;
-    int longest = 0;
+  const int per = plan.dealt ? (rows + 63) >> 6 : 2;  // rows that a lane looks up
+  int units = 0, longest = 0;
+  if (plan.dealt) {  // every wave for itself
+    const int first = lane * per;
     for (int j0 = 0; j0 < per; j0 += 4) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -522,19 +520,29 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
         }
       }
     }
+  }
+  if (!plan.dealt || !__any(longest > plan.whole)) {
+    // a workgroup per output
+    if (blockIdx.x >= (uint32_t)(rows * outputs)) return;
+    row = (int)(blockIdx.x / (uint32_t)outputs);
+    if (per > 1) look_at(row);
+    const int n = units_of(__builtin_amdgcn_readlane(lane_len, row - row0)) + kOutputUnits;
+    at = (blockIdx.x - (uint32_t)(row * outputs)) * (uint32_t)n;
+    until = at + n;
+  } else {
     const int sum = inclusive_sum(units);
-    const int64_t total = (int64_t)__builtin_amdgcn_readlane(sum, 63) * outputs;
-    share = quotient(total + gridDim.x - 1, gridDim.x);
-    cut = __any(longest > min(kWhole, (int)min(share, (int64_t)kWhole) + kJoinUnits - kOutputUnits));
+    const uint32_t total = (uint32_t)__builtin_amdgcn_readlane(sum, 63) * outputs;
+    share = (total + gridDim.x - 1) / gridDim.x;
     at = blockIdx.x * share;
     until = min(total, at + share);
     if (at >= total) return;
+    cut = __any(longest > (int)min((uint32_t)kWhole, share + kJoinUnits - kOutputUnits));
     // the lane that has the row of the first unit, then the row
-    const int unit = (int)quotient(at, outputs);
+    const int unit = (int)(at / (uint32_t)outputs);
     int who = __ffsll((unsigned long long)__ballot(sum > unit)) - 1;
-    int end = sum, begin = 0;
+    int end = sum;
     if (per > 1) {
-      begin = __builtin_amdgcn_readlane(sum - units, who);
+      const int begin = __builtin_amdgcn_readlane(sum - units, who);
       look_at(who * per);
       units = row0 + lane < rows ? units_of(lane_len) + kOutputUnits : 0;
       end = begin + inclusive_sum(units);
@@ -543,8 +551,8 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
     row = row0 + who;
     before = __builtin_amdgcn_readlane(end - units, who);
     if (!cut) {
-      const int all = __builtin_amdgcn_readlane(units_of(lane_len), who) + kOutputUnits;
-      const int skip = (int)((uint32_t)(at - before * outputs) % (uint32_t)all);
+      const uint32_t all = __builtin_amdgcn_readlane(units_of(lane_len), who) + kOutputUnits;
+      const uint32_t skip = (at - before * outputs) % all;
       at += skip ? all - skip : 0;
       if (at >= until) return;
       if (at >= (before + all) * outputs) {
@@ -552,15 +560,6 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
         ++row;
       }
     }
-  } else {
-    // a workgroup per output
-    row = (int)(blockIdx.x / (unsigned)outputs);
-    look_at(row);
-    const int n = units_of(__builtin_amdgcn_readfirstlane(lane_len)) + kOutputUnits;
-    before = 0;
-    share = n;
-    at = (int64_t)(blockIdx.x % (unsigned)outputs) * n;
-    until = at + n;
   }
   const __amdgpu_buffer_rsrc_t rs =
       raw_rsrc(partials, plan.dealt ? 2u * gridDim.x * (uint32_t)part_floats(a.group, DIM) * 4u : 0u);
@@ -569,15 +568,14 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
   const auto next_piece = [&]() {
     Piece p;
     p.row = row;
-    p.before = before;
     if (row - row0 >= 64) look_at(row);
     p.slot = __builtin_amdgcn_readlane(lane_slot, row - row0);
     p.len = __builtin_amdgcn_readlane(lane_len, row - row0);
     p.steps = units_of(p.len);
     const int all = p.steps + kOutputUnits;
-    const uint32_t rel = (uint32_t)(at - before * outputs);
+    const uint32_t rel = at - before * outputs;
     const int output = (int)(rel / (uint32_t)all), skip = (int)(rel - (uint32_t)output * all);
-    const int take = cut ? (int)min((int64_t)(all - skip), until - at) : all;
+    const int take = cut ? (int)min((uint32_t)(all - skip), until - at) : all;
     const int step0 = max(0, skip - kOutputUnits), step1 = skip + take - kOutputUnits;
     p.none = step1 <= 0;
     p.whole = step1 - step0 == p.steps;
@@ -587,7 +585,7 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
     p.kvh = output / plan.head_tiles;
     p.heads = min(16, a.group - 16 * tile);
     p.head0 = p.kvh * a.group + 16 * tile;
-    p.first = before * outputs + (int64_t)output * all + kOutputUnits;
+    p.first = before * outputs + (uint32_t)output * all + kOutputUnits;
     at += take;
     if (at >= (before + all) * outputs) {
       before += all;
@@ -735,9 +733,9 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
       int part = 0, parts = 1;
       DealtParts place = {0};
       if (!done.whole) {
-        place.first = (int)min(quotient(done.first, share), (int64_t)gridDim.x - 1);
+        place.first = (int)min(done.first / share, gridDim.x - 1);
         part = (int)blockIdx.x - place.first;
-        parts = (int)quotient(done.first + done.steps - 1, share) - place.first + 1;
+        parts = (int)((done.first + done.steps - 1) / share) - place.first + 1;
       }
       join_parts<DT, DIM>(a, lds, counters + place.first, rs, place, done.row, done.head0, done.heads, part, parts,
                           done.len > 0);
@@ -752,16 +750,20 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
 // Rows of up to kMaxDealtRows have their units dealt out in equal shares to as
 // many workgroups as the card holds at once, so that the longest row ends with
 // the others; more rows than that, whose lengths take too long to look up in
-// every workgroup, are a workgroup for each output.  Dealt and not, us: 64 rows of
-// up to 4096 42 and 52, rows of 131072 and 100001 60 and 1177, 1000 of up to 500
-// 129 and 126, 2000 of up to 300 230 and 206.
+// every workgroup, are a workgroup for each output.  So are outputs that the card
+// holds at once where none has more than `whole` units, which grows with their
+// number, since the shares do.  Dealt and not, us: 64 rows of up to 4096 37.4 and
+// 44, rows of 131072 and 100001 59 and 1014, one of 777 9.5 and 10.8, 300 of up to
+// 3000 109 and 115; but 64 of up to 700 16.8 and 11.7, 64 of up to 1500 20.8 and
+// 18.3, 30 of up to 400 10.8 and 8.3, one of 512 9.2 and 8.8.
 Decode4Plan plan_attention_decode4(int64_t rows, int q_heads, int kv_heads, int head_dim, int64_t max_len) {
   Decode4Plan p;
   p.head_tiles = (q_heads / kv_heads + 15) / 16;
   const int64_t outputs = rows * kv_heads * p.head_tiles;
   const int64_t units = std::max<int64_t>(1, (max_len + kUnit - 1) / kUnit), most = outputs * (units + kOutputUnits);
-  p.dealt = rows <= kMaxDealtRows && rows * (units + kOutputUnits) < int64_t(1) << 31;  // (the sums' type)
+  p.dealt = rows <= kMaxDealtRows && most < int64_t(1) << 30;  // (the sums' type)
   p.workgroups = (int)(p.dealt ? std::min<int64_t>(most, 256 * kDecode4Resident) : outputs);
+  p.whole = outputs <= p.workgroups ? 5 + (int)outputs / 48 : 0;
   return p;
 }
 

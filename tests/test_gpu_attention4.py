@@ -79,7 +79,7 @@ def test_rows_share_the_card(rows_):
     assert torch.equal(y.view(torch.int16), decode(c, q, ints(slots)).view(torch.int16))
 
 
-@pytest.mark.parametrize("rows_,most", [(30, 400), (64, 700), (65, 900), (300, 900), (300, 2500), (1024, 300),
+@pytest.mark.parametrize("rows_,most", [(30, 400), (64, 700), (65, 900), (200, 500), (300, 900), (300, 2500), (1024, 300),
                                         (1024, 1500), (1025, 300)])
 def test_many_rows(rows_, most):
     """Every row of calls whose outputs are cut, are not cut, and have a workgroup each; one row is far the longest
