@@ -159,7 +159,7 @@ struct State {
 
 // Weights of one u for the second product, [head][key], keys in the order in
 // which a lane takes them: 4 g .. 4 g + 3 of the first block, then of the second.
-constexpr int kWeightRow = 40;  // halves: rows of four lanes apart lie on different banks
+constexpr int kWeightRow = 40;  // halves: what 16 lanes read together lies on different banks
 
 // A row's queries: their fp16 fragments (head query_of(lane)), and for heads g + 4 i
 // 2^-24 times their sums by group, and what makes scores * log2 e of a product: a
@@ -548,7 +548,8 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
       end = begin + inclusive_sum(units);
       who = __ffsll((unsigned long long)__ballot(end > unit)) - 1;
     }
-    row = row0 + who;
+    who = max(who, 0);  // (no lane, should lengths change while they are read)
+    row = min(row0 + who, rows - 1);
     before = __builtin_amdgcn_readlane(end - units, who);
     if (!cut) {
       const uint32_t all = __builtin_amdgcn_readlane(units_of(lane_len), who) + kOutputUnits;
@@ -557,7 +558,7 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
       if (at >= until) return;
       if (at >= (before + all) * outputs) {
         before += all;
-        ++row;
+        row = min(row + 1, rows - 1);
       }
     }
   }

@@ -57,7 +57,8 @@ def test_lengths(dtype, dim, page):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("kv_heads,group", [(1, 1), (3, 2), (2, 7), (1, 16), (2, 17), (1, 40), (8, 4), (5, 1)])
+@pytest.mark.parametrize("kv_heads,group", [(1, 1), (3, 2), (2, 3), (2, 5), (2, 7), (1, 8), (1, 9), (1, 16), (2, 17),
+                                            (1, 40), (8, 4), (5, 1), (1, 256), (256, 1)])
 def test_heads(dtype, kv_heads, group):
     lengths = [300, 45]
     for dim in (64, 128):
@@ -91,6 +92,14 @@ def test_many_rows(rows_, most):
     y = decode(c, q, ints(slots))
     check(c, q, slots, y)
     assert torch.equal(y.view(torch.int16), decode(c, q, ints(slots)).view(torch.int16))
+
+
+def test_the_most_rows():
+    c = _kv4.fill(paro, [70, 0, 300, 5], 16, 1, 64, torch.bfloat16, 3)
+    q, slots = rows((8, 2, 64), torch.bfloat16, 1), [0, 3, 1, 2, -1, 2, 4, 0]
+    y = decode(c, q.repeat(4096, 1, 1), ints(slots).repeat(4096)).view(4096, 8, 2, 64)
+    check(c, q, slots, y[0])
+    assert torch.equal(y.view(torch.int16), y[:1].expand(4096, 8, 2, 64).contiguous().view(torch.int16))
 
 
 @pytest.mark.parametrize("dtype", TYPES)
