@@ -14,9 +14,11 @@ namespace paro {
 
 constexpr int kDecodeWaves = 4;  // of a decode workgroup
 constexpr int kCoherent = 16;    // SC1: device-scope loads and stores of the parts
-// Parts that a thread has in flight together (with 16 the kernel over four bits
-// spills registers).
-constexpr int kJoinBatch = 8;
+// Parts that a thread has in flight together.  With 2, 4 and 8 one row of 777 keys
+// takes 8.7, 8.2 and 8.8 us over four bits, 40 rows of up to 1500 9.8, 9.6 and 10.3
+// (over 16 bits 6.9 with 4, 7.3 with 8): the code of a larger batch costs more than
+// a second round of loads; 16 spill registers.
+constexpr int kJoinBatch = 4;
 
 // What the waves hand over: sums relative to 2^m, m the maximum of scores * log2 e.
 template <int DIM>
