@@ -37,10 +37,11 @@
 // What bounds it: where rows are long the bytes, 9/8 per key and channel (9/32 of
 // the 16-bit cache's): two rows of 131072 and 100001 keys (8 heads of 128
 // channels, 32 query heads, 266 MB) take 59 us, 4.5 TB/s, 64 rows of up to 4096
-// (141 MB) 37.4 us.  In its steady state the card takes in 5.2 to 5.6 TB/s (a copy
-// moves 4.8); about 7 us are the start (look-ups of slot, length and table, then
-// the first keys), the first step and the join.  One row of 777 keys, 8 outputs
-// over 56 workgroups of one step each: 9.5 us, of which those are 7.
+// (141 MB) 36.9 us.  In its steady state the card takes in 5.2 to 5.6 TB/s (a copy
+// moves 4.8 to 5.0); about 6 us are the start and the join.  One row of 777 keys, 8
+// outputs over 56 workgroups of one step each, 8.2 us: slot and length 1.2, table
+// 1.0, queries and first keys 0.7, the step 1.3, a part stored and counted 1.3,
+// the parts joined 1.6, the rest a launch.
 // Both sides of the choices, us:
 //   - two workgroups per CU and one: 37 and 52 (64 rows), 59 and 77 (two rows);
 //     three: 43 and 67, the registers of two tiles and the sums no longer fit.
@@ -754,7 +755,7 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
 // every workgroup, are a workgroup for each output.  So are outputs that the card
 // holds at once where none has more than `whole` units, which grows with their
 // number, since the shares do.  Dealt and not, us: 64 rows of up to 4096 37.4 and
-// 44, rows of 131072 and 100001 59 and 1014, one of 777 9.5 and 10.8, 300 of up to
+// 44, rows of 131072 and 100001 59 and 1014, one of 777 9 and 10.8, 300 of up to
 // 3000 109 and 115; but 64 of up to 700 16.8 and 11.7, 64 of up to 1500 20.8 and
 // 18.3, 30 of up to 400 10.8 and 8.3, one of 512 9.2 and 8.8.
 Decode4Plan plan_attention_decode4(int64_t rows, int q_heads, int kv_heads, int head_dim, int64_t max_len) {

@@ -76,7 +76,7 @@ __host__ __device__ inline int part_floats(int group, int dim) { return (group <
 // needed in between): part `part` of `parts` of the `heads` query heads from
 // head0 of a row.  counter: this output's; rs: the slots (neither is used with
 // one part).  some: the row has a key; without one it is zero.  Storing a part,
-// counting and joining takes 2 to 3.4 us.
+// counting and joining takes 2 to 3 us.
 template <int DT, int DIM, class Place>
 __device__ __forceinline__ void join_parts(const AttentionArgs &a, DecodeJoin<DIM> &lds, uint32_t *counter,
                                            __amdgpu_buffer_rsrc_t rs, Place place_of, int64_t row, int head0,
