@@ -91,14 +91,14 @@ hipError_t launch_attention_decode(const AttentionArgs &a, const DecodeAttention
 // The same over a cache in four bits: the keys of all rows together are dealt
 // out to the workgroups that the card holds at once (two per CU), a counter and
 // two slots for parts each.
-constexpr int kMaxDealtRows = 1024;
+constexpr int kMaxDealtRows = 4096;
 constexpr int kDecode4Resident = 2;  // workgroups per CU
 constexpr int kDecode4Counters = 256 * kDecode4Resident;
 struct Decode4Plan {
   int head_tiles;  // as above
   int workgroups;
   bool dealt;      // false: a workgroup per output, that is row, key-value head and head tile
-  int whole;       // the same where no row has more units than this
+  int whole;       // the same where no row has more units than this; 0: more outputs than workgroups
 };
 Decode4Plan plan_attention_decode4(int64_t rows, int q_heads, int kv_heads, int head_dim, int64_t max_len);
 size_t attention_decode4_partial_bytes(const Decode4Plan &p, int q_heads, int kv_heads, int head_dim);

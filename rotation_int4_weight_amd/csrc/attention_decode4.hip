@@ -31,9 +31,10 @@
 //     which is far less than what a 16-bit output shows.
 // Work is dealt out in units (kUnit keys of an output, an output being a row and
 // up to 16 query heads of a key-value head), so that the 512 workgroups that the
-// card holds end together whatever the rows' lengths are; see kOutputUnits,
-// kWhole and plan_attention_decode4.
-//
+// card holds end together whatever the rows' lengths are.  A workgroup's four waves
+// share an output and join their sums; where there are many short ones each wave
+// takes outputs of its own, with nothing to join.  See kOutputUnits, kLoneShare and
+// plan_attention_decode4.
 // What bounds it: where rows are long the bytes, 9/8 per key and channel (9/32 of
 // the 16-bit cache's): two rows of 131072 and 100001 keys (8 heads of 128
 // channels, 32 query heads, 266 MB) take 59 us, 4.5 TB/s, 64 rows of up to 4096
@@ -74,13 +75,12 @@ constexpr int kUnit = kStep * kDecodeWaves;  // keys per workgroup and step
 // and 6: 47.5, 37.4 and 39.2 us for 64 rows of up to 4096, 62, 47 and 50.5 for 300
 // of up to 1000; 2 and 4 as 3).
 constexpr int kOutputUnits = 3;
-// Where there are more outputs than workgroups they are cut where a share ends,
-// at the cost of a join, unless the longest one has at most kWhole steps and is no
-// longer than a share and kJoinUnits together.  Cut and whole, us: 300 rows of up
-// to 300 keys 33.2 and 30.9, 1000 of up to 500 104.5 and 103.5; but 300 of up to
-// 1000 47 and 49, 300 of up to 3000 109 and 116.
-constexpr int kJoinUnits = 5;
-constexpr int kWhole = 7;
+// Waves have outputs of their own where there are more outputs than workgroups and
+// the longest has at most two thirds of the units of a wave's share.  Shared by
+// four waves and one each, us: 300 rows of up to 300 keys 33 and 25, 1000 of up to
+// 500 104 and 91, 1000 of 500 148 and 121; but 300 of up to 1000 (longest 8, share
+// 9) 46 and 52.
+constexpr uint32_t kLoneShare = 2, kLoneLongest = 3;
 constexpr int kTiles = 2;                    // of a wave's ring
 constexpr float kSlack = 3.f;                // a maximum moves when a score rose by more than 2^kSlack over it
 constexpr int kTop = 12;                     // weights times scales stay under 2^(kTop + kSlack) in fp16
@@ -108,8 +108,8 @@ template <int DIM>
 struct Window {
   uint32_t low, high;  // of this lane's block
   __device__ __forceinline__ void look_up(const int32_t *__restrict__ table, int64_t page_bytes, int64_t head_offset,
-                                          int last, int num_pages, int shift, int pos, int lane) {
-    const int p = pos + kUnit * (lane >> 1) + 16 * (lane & 1);
+                                          int last, int num_pages, int shift, int pos, int stride, int lane) {
+    const int p = pos + stride * (lane >> 1) + 16 * (lane & 1);
     int page = table[min(p >> shift, last)];
     page = page < 0 ? 0 : page >= num_pages ? num_pages - 1 : page;
     const int64_t at = (int64_t)page * page_bytes + head_offset + (p & ((1 << shift) - 1)) * Kv4<DIM>::kRow;
@@ -482,7 +482,10 @@ struct Piece {
   bool whole, none;    // none: only units that stand for an output's start
 };
 
-template <int DT, int DIM, int N>
+// MANY: more outputs than workgroups, or not dealt (a kernel of its own, since the
+// other's code is shorter and its calls are: one row of 777 keys 8.2 us, 9.1 with
+// both in one).
+template <int DT, int DIM, int N, bool MANY>
 __global__ void __launch_bounds__(256, kDecode4Resident)
 decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict__ counters,
                          float *__restrict__ partials) {
@@ -494,10 +497,11 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
   const int rows = a.sequences;
   // a CU's second workgroup, which takes the lead in every other step (see the header)
   const bool young = blockIdx.x >= 256;
-  // this workgroup's units at..until, in row `row`, whose first is before * outputs
+  // this workgroup's (or wave's) units at..until, in row `row`, whose first is before * outputs
   // (the host has seen that all of a call's units are fewer than 2^31)
   uint32_t at, until, share = 1, before = 0;
-  bool cut = false;  // outputs are cut where a share ends; else they are the workgroup's that has their first unit
+  bool whole = true;  // outputs are not cut
+  bool lone = false;  // each wave has outputs of its own, those whose first unit is in its share
   int row, row0 = 0, lane_slot = 0, lane_len = 0;  // lane: row row0 + lane
   const auto look_at = [&](int first) {
     row0 = first;
@@ -508,9 +512,10 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
   int units = 0, longest = 0;
   if (plan.dealt) {  // every wave for itself
     const int first = lane * per;
-    for (int j0 = 0; j0 < per; j0 += 4) {
+    constexpr int kRows = MANY ? 8 : 4;  // looked up together
+    for (int j0 = 0; j0 < per; j0 += kRows) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kRows; ++j) {
         const int r = first + j0 + j;
         if (j0 + j < per && r < rows) {
           lane_slot = a.slots[r];
@@ -522,7 +527,7 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
       }
     }
   }
-  if (!plan.dealt || !__any(longest > plan.whole)) {
+  if (MANY ? !plan.dealt : !__any(longest > plan.whole)) {
     // a workgroup per output
     if (blockIdx.x >= (uint32_t)(rows * outputs)) return;
     row = (int)(blockIdx.x / (uint32_t)outputs);
@@ -534,10 +539,17 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
     const int sum = inclusive_sum(units);
     const uint32_t total = (uint32_t)__builtin_amdgcn_readlane(sum, 63) * outputs;
     share = (total + gridDim.x - 1) / gridDim.x;
-    at = blockIdx.x * share;
+    uint32_t worker = blockIdx.x;
+    const uint32_t of_wave = (share + kDecodeWaves - 1) / kDecodeWaves;
+    lone = MANY && !__any((uint32_t)longest * kLoneLongest > of_wave * kLoneShare);
+    if (lone) {
+      share = of_wave;
+      worker = blockIdx.x * kDecodeWaves + wave;
+    }
+    whole = lone;
+    at = worker * share;
     until = min(total, at + share);
     if (at >= total) return;
-    cut = __any(longest > (int)min((uint32_t)kWhole, share + kJoinUnits - kOutputUnits));
     // the lane that has the row of the first unit, then the row
     const int unit = (int)(at / (uint32_t)outputs);
     int who = __ffsll((unsigned long long)__ballot(sum > unit)) - 1;
@@ -552,7 +564,7 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
     who = max(who, 0);  // (no lane, should lengths change while they are read)
     row = min(row0 + who, rows - 1);
     before = __builtin_amdgcn_readlane(end - units, who);
-    if (!cut) {
+    if (lone) {
       const uint32_t all = __builtin_amdgcn_readlane(units_of(lane_len), who) + kOutputUnits;
       const uint32_t skip = (at - before * outputs) % all;
       at += skip ? all - skip : 0;
@@ -563,188 +575,209 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
       }
     }
   }
-  const __amdgpu_buffer_rsrc_t rs =
-      raw_rsrc(partials, plan.dealt ? 2u * gridDim.x * (uint32_t)part_floats(a.group, DIM) * 4u : 0u);
+  // (twice, so that the strides are constants: 300 rows of up to 1000 keys 46 us, 49 at run time)
+  const auto run = [&](auto alone) __attribute__((always_inline)) {
+    constexpr bool LONE = decltype(alone)::value;
+    const __amdgpu_buffer_rsrc_t rs =
+        raw_rsrc(partials, plan.dealt ? 2u * gridDim.x * (uint32_t)part_floats(a.group, DIM) * 4u : 0u);
 
-  // the piece at `at`, which moves to the next one
-  const auto next_piece = [&]() {
-    Piece p;
-    p.row = row;
-    if (row - row0 >= 64) look_at(row);
-    p.slot = __builtin_amdgcn_readlane(lane_slot, row - row0);
-    p.len = __builtin_amdgcn_readlane(lane_len, row - row0);
-    p.steps = units_of(p.len);
-    const int all = p.steps + kOutputUnits;
-    const uint32_t rel = at - before * outputs;
-    const int output = (int)(rel / (uint32_t)all), skip = (int)(rel - (uint32_t)output * all);
-    const int take = cut ? (int)min((uint32_t)(all - skip), until - at) : all;
-    const int step0 = max(0, skip - kOutputUnits), step1 = skip + take - kOutputUnits;
-    p.none = step1 <= 0;
-    p.whole = step1 - step0 == p.steps;
-    p.begin = step0 * kUnit;
-    p.end = min(p.len, step1 * kUnit);
-    const int tile = output % plan.head_tiles;
-    p.kvh = output / plan.head_tiles;
-    p.heads = min(16, a.group - 16 * tile);
-    p.head0 = p.kvh * a.group + 16 * tile;
-    p.first = before * outputs + (uint32_t)output * all + kOutputUnits;
-    at += take;
-    if (at >= (before + all) * outputs) {
-      before += all;
-      row = min(row + 1, rows - 1);
-    }
-    return p;
-  };
+    // the piece at `at`, which moves to the next one
+    const auto next_piece = [&]() {
+      Piece p;
+      p.row = row;
+      if (row - row0 >= 64) look_at(row);
+      p.slot = __builtin_amdgcn_readlane(lane_slot, row - row0);
+      p.len = __builtin_amdgcn_readlane(lane_len, row - row0);
+      p.steps = units_of(p.len);
+      const int all = p.steps + kOutputUnits;
+      const uint32_t rel = at - before * outputs;
+      const int output = (int)(rel / (uint32_t)all), skip = (int)(rel - (uint32_t)output * all);
+      const int take = LONE || whole ? all : (int)min((uint32_t)(all - skip), until - at);
+      const int step0 = max(0, skip - kOutputUnits), step1 = skip + take - kOutputUnits;
+      p.none = step1 <= 0;
+      p.whole = step1 - step0 == p.steps;
+      p.begin = step0 * kUnit;
+      p.end = min(p.len, step1 * kUnit);
+      const int tile = output % plan.head_tiles;
+      p.kvh = output / plan.head_tiles;
+      p.heads = min(16, a.group - 16 * tile);
+      p.head0 = p.kvh * a.group + 16 * tile;
+      p.first = before * outputs + (uint32_t)output * all + kOutputUnits;
+      at += take;
+      if (at >= (before + all) * outputs) {
+        before += all;
+        row = min(row + 1, rows - 1);
+      }
+      return p;
+    };
 
-  // the loads of a wave's tiles of a piece; a ring of tiles: one is worked on
-  // while the others are loaded
-  const char *const k = (const char *)a.kv.k, *const v = (const char *)a.kv.v;
-  constexpr uint32_t kCodes = sizeof(typename Tile<DIM>::Codes);
-  const uint32_t k_lane = (lane & 15) * Kv4<DIM>::kRow + (lane >> 4) * kCodes, v_lane = lane * kCodes;
-  const char *const p_lane = (lane & 32 ? v : k) + (lane & 15) * (4 * G);
-  const int shift = a.kv.page_shift;
-  Piece piece;
-  Window<DIM> win;
-  Tile<DIM> t[kTiles];
-  int pos, loaded;  // of the piece: the next step's first key, the steps loaded
-  const auto load = [&](Tile<DIM> &t, int p) {
-    if ((loaded & 31) == 0)
-      win.look_up(a.kv.table + (int64_t)piece.slot * a.kv.max_pages, a.kv.page_stride * 2,
-                  piece.kvh * Kv4<DIM>::head_bytes(1 << shift), (piece.len - 1) >> shift, a.kv.num_pages, shift, p,
-                  lane);
-    const int64_t c0 = win.block(2 * (loaded & 31)), c1 = win.block(2 * (loaded & 31) + 1);
-    // from a block's codes to its pairs
-    const int mask = (1 << shift) - 1, ends = Kv4<DIM>::pairs_at(1 << shift);
-    const int64_t p0 = c0 + ends - (p & mask) * (Kv4<DIM>::kRow - 4 * G);
-    const int64_t p1 = c1 + ends - ((p + 16) & mask) * (Kv4<DIM>::kRow - 4 * G);
-    t.pairs = *reinterpret_cast<const typename Words<G>::type *>(p_lane + (lane & 16 ? p1 : p0));
-    t.k[0] = *reinterpret_cast<const typename Tile<DIM>::Codes *>(k + c0 + k_lane);
-    t.k[1] = *reinterpret_cast<const typename Tile<DIM>::Codes *>(k + c1 + k_lane);
-    t.v[0] = *reinterpret_cast<const typename Tile<DIM>::Codes *>(v + c0 + v_lane);
-    t.v[1] = *reinterpret_cast<const typename Tile<DIM>::Codes *>(v + c1 + v_lane);
-    ++loaded;
-  };
-  u32x4 raw[DIM / 32];
-  const auto start = [&]() {
-    piece = next_piece();
-    if (piece.none) return;
-    load_query<DIM>(raw, a, piece.row, piece.head0, piece.heads, lane);
-    pos = piece.begin + wave * kStep;
-    loaded = 0;
+    // the loads of a wave's tiles of a piece; a ring of tiles: one is worked on
+    // while the others are loaded
+    constexpr int stride = LONE ? kStep : kUnit;  // between a wave's steps
+    const char *const k = (const char *)a.kv.k, *const v = (const char *)a.kv.v;
+    constexpr uint32_t kCodes = sizeof(typename Tile<DIM>::Codes);
+    const uint32_t k_lane = (lane & 15) * Kv4<DIM>::kRow + (lane >> 4) * kCodes, v_lane = lane * kCodes;
+    const char *const p_lane = (lane & 32 ? v : k) + (lane & 15) * (4 * G);
+    const int shift = a.kv.page_shift;
+    Piece piece;
+    Window<DIM> win;
+    Tile<DIM> t[kTiles];
+    int pos, loaded;  // of the piece: the next step's first key, the steps loaded
+    const auto load = [&](Tile<DIM> &t, int p) {
+      if ((loaded & 31) == 0)
+        win.look_up(a.kv.table + (int64_t)piece.slot * a.kv.max_pages, a.kv.page_stride * 2,
+                    piece.kvh * Kv4<DIM>::head_bytes(1 << shift), (piece.len - 1) >> shift, a.kv.num_pages, shift, p,
+                    stride, lane);
+      const int64_t c0 = win.block(2 * (loaded & 31)), c1 = win.block(2 * (loaded & 31) + 1);
+      // from a block's codes to its pairs
+      const int mask = (1 << shift) - 1, ends = Kv4<DIM>::pairs_at(1 << shift);
+      const int64_t p0 = c0 + ends - (p & mask) * (Kv4<DIM>::kRow - 4 * G);
+      const int64_t p1 = c1 + ends - ((p + 16) & mask) * (Kv4<DIM>::kRow - 4 * G);
+      t.pairs = *reinterpret_cast<const typename Words<G>::type *>(p_lane + (lane & 16 ? p1 : p0));
+      t.k[0] = *reinterpret_cast<const typename Tile<DIM>::Codes *>(k + c0 + k_lane);
+      t.k[1] = *reinterpret_cast<const typename Tile<DIM>::Codes *>(k + c1 + k_lane);
+      t.v[0] = *reinterpret_cast<const typename Tile<DIM>::Codes *>(v + c0 + v_lane);
+      t.v[1] = *reinterpret_cast<const typename Tile<DIM>::Codes *>(v + c1 + v_lane);
+      ++loaded;
+    };
+    u32x4 raw[DIM / 32];
+    const auto start = [&]() {
+      piece = next_piece();
+      if (piece.none) return;
+      load_query<DIM>(raw, a, piece.row, piece.head0, piece.heads, lane);
+      pos = piece.begin + (LONE ? 0 : wave * kStep);
+      loaded = 0;
 #pragma unroll
-    for (int d = 0; d + 1 < kTiles; ++d)
-      if (pos + d * kUnit < piece.end) load(t[d], pos + d * kUnit);
-  };
-  start();
-  while (true) {
-    const int end = piece.end;
-    const bool none = piece.none;
-    if (!none) {
-      State<DIM, N> st;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        st.m[i] = -INFINITY;
-        st.l[i] = 0.f;
-      }
-#pragma unroll
-      for (int u = 0; u < G; ++u) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) st.mids[u][i] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) st.o[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
-      st.ev = kLeastExponent;
-      if (pos < end) {
-        uint16_t *weights = reinterpret_cast<uint16_t *>(&lds.o[wave][0][0]);
-        Query<DIM, N> q;
-        open_query<DT, DIM, N>(q, raw, a.scale, piece.heads, lane);
-        bool more = true;
-        const auto turn = [&](Tile<DIM> &now, Tile<DIM> &ahead, auto fresh) {
-          const int live = end - pos;  // keys of this step: more than there are but at the end
-          const bool tail = live < kStep;
-          if (live > (kTiles - 1) * kUnit) load(ahead, pos + (kTiles - 1) * kUnit);
-          if (tail) {  // (uniform) what the page holds behind the end does not count
-            asm volatile("");
-            if ((lane & 31) >= live)
-#pragma unroll
-              for (int u = 0; u < G; ++u) now.pairs[u] = 0;
-          }
-          const Pairs<DIM> pairs = spread<DIM>(now.pairs);
-          if (young) {
-            if (&now == &t[0]) __builtin_amdgcn_s_setprio(1);
-            else __builtin_amdgcn_s_setprio(0);
-          }
-          float x[2][N];
-          scores<DT, DIM, N>(x, now, pairs, q);
-          weigh<DT, DIM, N, decltype(fresh)::value>(st, x, pairs, q, weights, tail, live, lane);
-          wave_lds_sync();
-          add_values<DIM, N>(st, now.v, weights, lane);
-          wave_lds_sync();
-          pos += kUnit;
-          more = live > kUnit;
-        };
-        turn(t[0], t[kTiles - 1], std::true_type());
-        while (more) {
-#pragma unroll
-          for (int d = 1; d <= kTiles; ++d) {
-            turn(t[d % kTiles], t[(d + kTiles - 1) % kTiles], std::false_type());
-            if (!more) break;
-          }
-        }
-      }
-      // ---- join the waves ----
-      {
-        // heads g + 4 i, over 16 lanes; then head lane % 16
-        float *own = &lds.o[wave][0][0];  // [quantity][head]
-        const int h = lane & 15, g = lane >> 4;
+      for (int d = 0; d + 1 < kTiles; ++d)
+        if (pos + d * stride < piece.end) load(t[d], pos + d * stride);
+    };
+    start();
+    while (true) {
+      const int end = piece.end;
+      const bool none = piece.none;
+      if (!none) {
+        State<DIM, N> st;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float l = sum16(st.l[i]);
-          float mids[G];
+          st.m[i] = -INFINITY;
+          st.l[i] = 0.f;
+        }
 #pragma unroll
-          for (int u = 0; u < G; ++u) mids[u] = sum16(st.mids[u][i]);
-          if (h == 0) {
-            lds.m[wave][g + 4 * i] = st.m[i];
-            lds.l[wave][g + 4 * i] = l;
+        for (int u = 0; u < G; ++u) {
 #pragma unroll
-            for (int u = 0; u < G; ++u) own[16 * u + g + 4 * i] = mids[u];
+          for (int i = 0; i < N; ++i) st.mids[u][i] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) st.o[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        st.ev = kLeastExponent;
+        if (pos < end) {
+          uint16_t *weights = reinterpret_cast<uint16_t *>(&lds.o[wave][0][0]);
+          Query<DIM, N> q;
+          open_query<DT, DIM, N>(q, raw, a.scale, piece.heads, lane);
+          bool more = true;
+          const auto turn = [&](Tile<DIM> &now, Tile<DIM> &ahead, auto fresh) {
+            const int live = end - pos;  // keys of this step: more than there are but at the end
+            const bool tail = live < kStep;
+            if (live > (kTiles - 1) * stride) load(ahead, pos + (kTiles - 1) * stride);
+            if (tail) {  // (uniform) what the page holds behind the end does not count
+              asm volatile("");
+              if ((lane & 31) >= live)
+#pragma unroll
+                for (int u = 0; u < G; ++u) now.pairs[u] = 0;
+            }
+            const Pairs<DIM> pairs = spread<DIM>(now.pairs);
+            if (young) {
+              if (&now == &t[0]) __builtin_amdgcn_s_setprio(1);
+              else __builtin_amdgcn_s_setprio(0);
+            }
+            float x[2][N];
+            scores<DT, DIM, N>(x, now, pairs, q);
+            weigh<DT, DIM, N, decltype(fresh)::value>(st, x, pairs, q, weights, tail, live, lane);
+            wave_lds_sync();
+            add_values<DIM, N>(st, now.v, weights, lane);
+            wave_lds_sync();
+            pos += stride;
+            more = live > stride;
+          };
+          turn(t[0], t[kTiles - 1], std::true_type());
+          while (more) {
+#pragma unroll
+            for (int d = 1; d <= kTiles; ++d) {
+              turn(t[d % kTiles], t[(d + kTiles - 1) % kTiles], std::false_type());
+              if (!more) break;
+            }
           }
         }
-        wave_lds_sync();
-        float mids[G];
+        // ---- a wave's sums ----
+        {
+          // heads g + 4 i, over 16 lanes; then head lane % 16
+          float *own = &lds.o[wave][0][0];  // [quantity][head]
+          const int h = lane & 15, g = lane >> 4;
 #pragma unroll
-        for (int u = 0; u < G; ++u) mids[u] = own[16 * u + (h & (4 * N - 1))];
-        wave_lds_sync();
-        if (h < piece.heads) {
+          for (int i = 0; i < N; ++i) {
+            const float l = sum16(st.l[i]);
+            float mids[G];
 #pragma unroll
-          for (int u = 0; u < G; ++u)
+            for (int u = 0; u < G; ++u) mids[u] = sum16(st.mids[u][i]);
+            if (h == 0) {
+              lds.m[wave][g + 4 * i] = st.m[i];
+              lds.l[wave][g + 4 * i] = l;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              f32x4 y;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) y[j] = ldexpf(st.o[u][j][i], (j & 1 ? 20 : 24) - kTop + st.ev) + mids[u];
-              *reinterpret_cast<f32x4 *>(&lds.o[wave][h][64 * u + 16 * g + 4 * i]) = y;
+              for (int u = 0; u < G; ++u) own[16 * u + g + 4 * i] = mids[u];
             }
+          }
+          wave_lds_sync();
+          float mids[G];
+#pragma unroll
+          for (int u = 0; u < G; ++u) mids[u] = own[16 * u + (h & (4 * N - 1))];
+          const float inv = piece.len > 0 ? 1.f / lds.l[wave][h & (4 * N - 1)] : 0.f;
+          wave_lds_sync();
+          if (h < piece.heads) {
+            uint16_t *const out = a.y + piece.row * a.y_token + (int64_t)(piece.head0 + h) * a.y_head;
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int c = 64 * u + 16 * g + 4 * i;
+                f32x4 y;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = ldexpf(st.o[u][j][i], (j & 1 ? 20 : 24) - kTop + st.ev) + mids[u];
+                if (LONE) *reinterpret_cast<u32x2 *>(out + c) = piece.len > 0 ? pack_row<DT>(y, inv) : u32x2{0, 0};
+                else *reinterpret_cast<f32x4 *>(&lds.o[wave][h][c]) = y;
+              }
+          }
         }
       }
-    }
-    const Piece done = piece;
-    const bool more = at < until;
-    if (more) start();  // (its loads pass while the waves are joined)
-    if (!none) {
-      int part = 0, parts = 1;
-      DealtParts place = {0};
-      if (!done.whole) {
-        place.first = (int)min(done.first / share, gridDim.x - 1);
-        part = (int)blockIdx.x - place.first;
-        parts = (int)((done.first + done.steps - 1) / share) - place.first + 1;
+      if (LONE) {
+        if (at >= until) break;
+        start();
+        continue;
       }
-      join_parts<DT, DIM>(a, lds, counters + place.first, rs, place, done.row, done.head0, done.heads, part, parts,
-                          done.len > 0);
+      const Piece done = piece;
+      const bool more = at < until;
+      if (more) start();  // (its loads pass while the waves are joined)
+      if (!none) {
+        int part = 0, parts = 1;
+        DealtParts place = {0};
+        if (!done.whole) {
+          place.first = (int)min(done.first / share, gridDim.x - 1);
+          part = (int)blockIdx.x - place.first;
+          parts = (int)((done.first + done.steps - 1) / share) - place.first + 1;
+        }
+        join_parts<DT, DIM>(a, lds, counters + place.first, rs, place, done.row, done.head0, done.heads, part, parts,
+                            done.len > 0);
+      }
+      if (!more) break;
+      __syncthreads();  // the join's reads of lds are done
     }
-    if (!more) break;
-    __syncthreads();  // the join's reads of lds are done
+  };
+  if constexpr (MANY) {
+    if (lone) {
+      run(std::true_type());
+      return;
+    }
   }
+  run(std::false_type());
 }
 
 }  // namespace
@@ -754,10 +787,11 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
 // the others; more rows than that, whose lengths take too long to look up in
 // every workgroup, are a workgroup for each output.  So are outputs that the card
 // holds at once where none has more than `whole` units, which grows with their
-// number, since the shares do.  Dealt and not, us: 64 rows of up to 4096 37.4 and
-// 44, rows of 131072 and 100001 59 and 1014, one of 777 9 and 10.8, 300 of up to
-// 3000 109 and 115; but 64 of up to 700 16.8 and 11.7, 64 of up to 1500 20.8 and
-// 18.3, 30 of up to 400 10.8 and 8.3, one of 512 9.2 and 8.8.
+// number, since the shares do.  Dealt and not, us: 64 rows of up to 4096 37 and 44,
+// rows of 131072 and 100001 59 and 1014, one of 777 9 and 10.8, 300 of up to 1000
+// 46 and 49, 2000 of up to 300 120 and 182, 4000 of up to 200 181 and 324; but 64 of
+// up to 700 16.8 and 11.7, 64 of up to 1500 20.8 and 18.3, 30 of up to 400 10.8 and
+// 8.3, one of 512 9.2 and 8.8.
 Decode4Plan plan_attention_decode4(int64_t rows, int q_heads, int kv_heads, int head_dim, int64_t max_len) {
   Decode4Plan p;
   p.head_tiles = (q_heads / kv_heads + 15) / 16;
@@ -777,27 +811,39 @@ hipError_t launch_attention_decode4(const AttentionArgs &a, const Decode4Plan &p
                                     float *partials, hipStream_t st) {
   const dim3 grid((unsigned)p.workgroups);
   const int heads = std::min(a.group, 16);
-#define PARO_DECODE4(DT, DIM)                                                                                        \
-  if (heads <= 4)                                                                                                    \
-    hipLaunchKernelGGL((decode4_attention_kernel<DT, DIM, 1>), grid, dim3(256), 0, st, a, p, counters, partials);     \
-  else if (heads <= 8)                                                                                               \
-    hipLaunchKernelGGL((decode4_attention_kernel<DT, DIM, 2>), grid, dim3(256), 0, st, a, p, counters, partials);     \
-  else                                                                                                               \
-    hipLaunchKernelGGL((decode4_attention_kernel<DT, DIM, 4>), grid, dim3(256), 0, st, a, p, counters, partials)
+  const bool many = !p.dealt || p.whole == 0;
+#define PARO_DECODE4_MANY(DT, DIM, N, MANY) \
+  hipLaunchKernelGGL((decode4_attention_kernel<DT, DIM, N, MANY>), grid, dim3(256), 0, st, a, p, counters, partials)
+#define PARO_DECODE4(DT, DIM, N)             \
+  if (many) {                                \
+    PARO_DECODE4_MANY(DT, DIM, N, true);     \
+  } else {                                   \
+    PARO_DECODE4_MANY(DT, DIM, N, false);    \
+  }
+#define PARO_DECODE4_HEADS(DT, DIM) \
+  if (heads <= 4) {                 \
+    PARO_DECODE4(DT, DIM, 1)        \
+  } else if (heads <= 8) {          \
+    PARO_DECODE4(DT, DIM, 2)        \
+  } else {                          \
+    PARO_DECODE4(DT, DIM, 4)        \
+  }
   if (a.dt == kF16) {
     if (a.head_dim == 64) {
-      PARO_DECODE4(kF16, 64);
+      PARO_DECODE4_HEADS(kF16, 64)
     } else {
-      PARO_DECODE4(kF16, 128);
+      PARO_DECODE4_HEADS(kF16, 128)
     }
   } else {
     if (a.head_dim == 64) {
-      PARO_DECODE4(kBF16, 64);
+      PARO_DECODE4_HEADS(kBF16, 64)
     } else {
-      PARO_DECODE4(kBF16, 128);
+      PARO_DECODE4_HEADS(kBF16, 128)
     }
   }
+#undef PARO_DECODE4_HEADS
 #undef PARO_DECODE4
+#undef PARO_DECODE4_MANY
   return hipGetLastError();
 }
 

@@ -80,11 +80,11 @@ def test_rows_share_the_card(rows_):
     assert torch.equal(y.view(torch.int16), decode(c, q, ints(slots)).view(torch.int16))
 
 
-@pytest.mark.parametrize("rows_,most", [(30, 400), (64, 700), (65, 900), (200, 500), (300, 900), (300, 2500), (1024, 300),
-                                        (1024, 1500), (1025, 300)])
+@pytest.mark.parametrize("rows_,most", [(30, 400), (64, 700), (65, 900), (200, 500), (300, 900), (300, 2500), (1024, 1500),
+                                        (600, 130), (1500, 100), (4096, 60), (4097, 300)])
 def test_many_rows(rows_, most):
-    """Every row of calls whose outputs are cut, are not cut, and have a workgroup each; one row is far the longest
-    where rows are many, some are empty and some name no slot."""
+    """Every row of calls whose outputs are cut, have a workgroup each, and have a wave each; one row is far the
+    longest where rows are many, some are empty and some name no slot."""
     lengths = [most] + [(i * 1237 + 5) % (most // 4) for i in range(12)] + [0]
     c = _kv4.fill(paro, lengths, 16, 2, 64, torch.float16, 9)
     slots = [(5 * i + 1) % 15 - 1 if rows_ <= 64 or i % 97 else 0 for i in range(rows_)]
