@@ -705,7 +705,8 @@ size_t paro_attention_prompt_cached_workspace_bytes(const paro_kv_cache *cache, 
  * row's (kept to 2^-35 of the row's largest), and what is rounded to fp16, for
  * either type, is the weights times the scales.  There the rows share the card by
  * their lengths, so the split, and with it the last bits of a result, depends on
- * the lengths of all rows of the call; a repeated call gives identical bits.
+ * the lengths of all rows of the call; a repeated call gives identical bits.  The
+ * workspace's size is the same for any number of rows.
  * rows <= 32768.
  */
 int paro_attention_decode(const paro_kv_cache *cache, int layer, const paro_attention_shape *shape, const void *q,

@@ -100,8 +100,9 @@ struct Decode4Plan {
   bool dealt;      // false: a workgroup per output, that is row, key-value head and head tile
   int whole;       // the same where no row has more units than this; 0: more outputs than workgroups
 };
-Decode4Plan plan_attention_decode4(int64_t rows, int q_heads, int kv_heads, int head_dim, int64_t max_len);
-size_t attention_decode4_partial_bytes(const Decode4Plan &p, int q_heads, int kv_heads, int head_dim);
+Decode4Plan plan_attention_decode4(int64_t rows, int q_heads, int kv_heads, int64_t max_len);
+// for any number of rows, so that a workspace serves fewer of them too
+size_t attention_decode4_partial_bytes(int q_heads, int kv_heads, int head_dim);
 hipError_t launch_attention_decode4(const AttentionArgs &a, const Decode4Plan &p, uint32_t *counters,
                                     float *partials, hipStream_t st);
 

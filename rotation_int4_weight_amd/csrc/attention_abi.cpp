@@ -343,12 +343,9 @@ size_t paro_attention_decode_workspace_bytes(const paro_kv_cache *c, int64_t row
   if (check_cache(c, false) || rows <= 0 || rows > paro::kMaxDecodeRows || q_heads < 1 || q_heads > kMaxHeads ||
       q_heads % c->kv_heads)
     return 0;
-  const int64_t most = (int64_t)c->max_pages * c->page_size;
   if (paro::kv4(c->dt))
-    return kCounterBytes +
-           paro::attention_decode4_partial_bytes(
-               paro::plan_attention_decode4(rows, q_heads, c->kv_heads, c->head_dim, most), q_heads, c->kv_heads,
-               c->head_dim);
+    return kCounterBytes + paro::attention_decode4_partial_bytes(q_heads, c->kv_heads, c->head_dim);
+  const int64_t most = (int64_t)c->max_pages * c->page_size;
   const paro::DecodeAttentionPlan p = paro::plan_attention_decode(rows, q_heads, c->kv_heads, most);
   return kCounterBytes + paro::attention_decode_partial_bytes(p, rows, c->kv_heads, c->head_dim);
 }
@@ -384,7 +381,7 @@ int paro_attention_decode(const paro_kv_cache *c, int layer, const paro_attentio
   hipError_t e =
       paro::kv4(c->dt)
           ? paro::launch_attention_decode4(
-                a, paro::plan_attention_decode4(rows, s->q_heads, c->kv_heads, c->head_dim, most), counters, partials,
+                a, paro::plan_attention_decode4(rows, s->q_heads, c->kv_heads, most), counters, partials,
                 (hipStream_t)stream)
           : paro::launch_attention_decode(a, paro::plan_attention_decode(rows, s->q_heads, c->kv_heads, most), counters,
                                           partials, (hipStream_t)stream);

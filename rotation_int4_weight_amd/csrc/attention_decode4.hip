@@ -792,7 +792,7 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
 // 46 and 49, 2000 of up to 300 120 and 182, 4000 of up to 200 181 and 324; but 64 of
 // up to 700 16.8 and 11.7, 64 of up to 1500 20.8 and 18.3, 30 of up to 400 10.8 and
 // 8.3, one of 512 9.2 and 8.8.
-Decode4Plan plan_attention_decode4(int64_t rows, int q_heads, int kv_heads, int head_dim, int64_t max_len) {
+Decode4Plan plan_attention_decode4(int64_t rows, int q_heads, int kv_heads, int64_t max_len) {
   Decode4Plan p;
   p.head_tiles = (q_heads / kv_heads + 15) / 16;
   const int64_t outputs = rows * kv_heads * p.head_tiles;
@@ -803,8 +803,8 @@ Decode4Plan plan_attention_decode4(int64_t rows, int q_heads, int kv_heads, int 
   return p;
 }
 
-size_t attention_decode4_partial_bytes(const Decode4Plan &p, int q_heads, int kv_heads, int head_dim) {
-  return p.dealt ? (size_t)2 * p.workgroups * part_floats(q_heads / kv_heads, head_dim) * 4 : 0;
+size_t attention_decode4_partial_bytes(int q_heads, int kv_heads, int head_dim) {
+  return (size_t)2 * 256 * kDecode4Resident * part_floats(q_heads / kv_heads, head_dim) * 4;
 }
 
 hipError_t launch_attention_decode4(const AttentionArgs &a, const Decode4Plan &p, uint32_t *counters,

@@ -29,7 +29,7 @@ def test_the_calls_take_it(dt):
     assert lib.paro_kv_workspace_bytes(ctypes.byref(c)) == lib.paro_kv_workspace_bytes(ctypes.byref(cache()))
     need = lib.paro_attention_decode_workspace_bytes
     assert need(ctypes.byref(c), 4, 8) > 2 ** 21 and need(ctypes.byref(c), 4, 7) == 0 and need(ctypes.byref(c), 0, 8) == 0
-    assert need(ctypes.byref(c), 32768, 8) == 2 ** 21 and need(ctypes.byref(c), 32769, 8) == 0  # an output each: no parts
+    assert need(ctypes.byref(c), 32768, 8) == need(ctypes.byref(c), 1, 8) and need(ctypes.byref(c), 32769, 8) == 0
 
 
 @pytest.mark.parametrize("dt", KV4)
