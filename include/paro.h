@@ -703,7 +703,9 @@ size_t paro_attention_prompt_cached_workspace_bytes(const paro_kv_cache *cache, 
  * Over a cache in four bits q and y are in the rows' type; scores are fp32 sums
  * over codes and pairs, queries are taken as fp16 times a power of two of their
  * row's (kept to 2^-35 of the row's largest), and what is rounded to fp16, for
- * either type, is the weights times the scales.  There the rows share the card by
+ * either type, is the weights times the scales, as fractions of the largest such
+ * product that a head has in 64 channels (those below 2^-20 of it fall into fp16's
+ * subnormals), however large other keys' scales are.  There the rows share the card by
  * their lengths, so the split, and with it the last bits of a result, depends on
  * the lengths of all rows of the call; a repeated call gives identical bits.  The
  * workspace's size is the same for any number of rows.

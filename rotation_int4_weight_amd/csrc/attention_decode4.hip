@@ -24,11 +24,12 @@
 //     that a lane has the pairs of its own keys only: each lane loads one key's
 //     pairs of K or of V, and swaps of lane halves and quarters spread them.  The
 //     second has the head in lane % 16; the weights change places in LDS.
-//   - Running maximum m of score * log2 e, moved when a score rose by more than
-//     2^kSlack over it, and sum of the weights, both fp32.
-//   - What is rounded to fp16 is p s 2^(kTop - ev), with 2^ev over every scale of V
-//     so far: off by 2^-11 of itself, or 2^-(25 + kTop) of the largest scale,
-//     which is far less than what a 16-bit output shows.
+//   - Running maximum m of score * log2 e, moved when one is more than kSlack over
+//     it, and sum of the weights, both fp32.
+//   - What is rounded to fp16 is p s 2^(kTop - ev), with 2^ev over the p s of a
+//     head and 64 channels so far: off by 2^-11 of itself, or by 2^-(22 + kTop) of
+//     the largest of them.  An ev over the scales alone would lose every other key to
+//     one that has a huge scale and no weight.
 // Work is dealt out in units (kUnit keys of an output, an output being a row and
 // up to 16 query heads of a key-value head), so that the 512 workgroups that the
 // card holds end together whatever the rows' lengths are.  A workgroup's four waves
@@ -82,10 +83,15 @@ constexpr int kOutputUnits = 3;
 // 9) 46 and 52.
 constexpr uint32_t kLoneShare = 2, kLoneLongest = 3;
 constexpr int kTiles = 2;                    // of a wave's ring
-constexpr float kSlack = 3.f;                // a maximum moves when a score rose by more than 2^kSlack over it
-constexpr int kTop = 12;                     // weights times scales stay under 2^(kTop + kSlack) in fp16
+// The maxima move when a weight is over 2^kSlack: with 3, 4 and 5 64 rows of up to
+// 4096 keys take 32.6, 32.2 and 32.1 us with 4 heads per key-value head, 45.6, 43.9
+// and 42.5 with 16, and two rows of 131072 and 100001 keys in fp16 are off by 2.49,
+// 2.51 and 2.54e-4 (the largest weight is 1 just after a move, and then exact).
+constexpr float kSlack = 4.f;
+constexpr int kTop = 8;                      // weights times scales are under 2^kTop in fp16 when their exponent is set,
+constexpr float kMost = 0x1p15f;             // and under this afterwards
 constexpr float kLeastMaximum = -3e38f;      // scores that fp32 does not hold weigh nothing, also among themselves
-constexpr int kLeastExponent = -126;         // of the values' scale
+constexpr int kLeastExponent = -110;         // of a weight times a scale: 2^(kTop - ev) is one fp32 number
 
 template <int N>
 struct Words {
@@ -154,8 +160,8 @@ struct State {
   f32x4 o[G][4];
   // of heads g + 4 i, over keys lane % 16 of each block: sums of weights times mid, and of weights
   float mids[G][N], l[N];
-  float m[N];  // weights are exp2(score * log2 e - m), at most 2^kSlack
-  int ev;      // 2^ev: over the scales of V
+  float m[N];      // weights are exp2(score * log2 e - m), at most 2^kSlack
+  float up[G][N];  // 2^(kTop - ev), with 2^ev over weights times scales, to kMost
 };
 
 // Weights of one u for the second product, [head][key], keys in the order in
@@ -243,35 +249,99 @@ __device__ __forceinline__ void scores(float (&x)[2][N], const Tile<DIM> &t, con
   }
 }
 
-// The maxima rise: weights, sums and outputs so far are made relative to the new
-// ones.  keeps: 16 floats of the wave's.
+// Weights of the scores x; dead keys have none.  Returns the lane's greatest
+// exponent of one.
 template <int DIM, int N>
-__device__ __forceinline__ void raise(State<DIM, N> &st, const float (&x)[2][N], const Query<DIM, N> &q, float *keeps,
+__device__ __forceinline__ float weights_of(float (&w)[2][N], const float (&x)[2][N], const Query<DIM, N> &q,
+                                            const float (&m)[N], bool end, int live, int lane) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      w[b][i] = __builtin_fmaf(x[b][i], q.factor[i], -m[i]);
+      top = fmaxf(top, w[b][i]);
+      w[b][i] = __builtin_amdgcn_exp2f(w[b][i]);
+    }
+  if (end) {
+    asm volatile("");
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[b][i] = 16 * b + (lane & 15) >= live ? 0.f : w[b][i];
+  }
+  return top;
+}
+
+// ev of 2^(kTop - ev)
+__device__ __forceinline__ int exponent_of(float up) { return kTop + 1 - __builtin_amdgcn_frexp_expf(up); }
+
+// The sums of weights times scales times factor, of heads g + 4 i.  room: 16 G
+// floats of the wave's.
+template <int DIM, int N>
+__device__ __forceinline__ void multiply(State<DIM, N> &st, const float (&factor)[DIM / 64][N], float *room, int lane) {
+  constexpr int G = DIM / 64;
+#pragma unroll
+  for (int u = 0; u < G; ++u)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((lane & 15) == 0) room[16 * u + (lane >> 4) + 4 * i] = factor[u][i];
+  wave_lds_sync();
+  float f[G];  // of head lane % 16 (other lanes' sums are not used)
+#pragma unroll
+  for (int u = 0; u < G; ++u) f[u] = room[16 * u + ((lane & 15) & (4 * N - 1))];
+  wave_lds_sync();
+#pragma unroll
+  for (int u = 0; u < G; ++u)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) st.o[u][n] *= f[u];
+}
+
+// The maxima rise: the sums so far are made relative to the new ones.  The
+// exponents of weights times scales fall by the whole part of that, as those
+// weights do; one that is then too low for the new keys is set by set_exponents.
+template <int DIM, int N>
+__device__ __forceinline__ void raise(State<DIM, N> &st, const float (&x)[2][N], const Query<DIM, N> &q, float *room,
                                       int lane) {
+  float factor[DIM / 64][N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float m = fmaxf(st.m[i], max16(fmaxf(x[0][i], x[1][i])) * q.factor[i]);
-    const float keep = m == st.m[i] ? 1.f : __builtin_amdgcn_exp2f(st.m[i] - m);
+    const float rise = m == st.m[i] ? 0.f : m - st.m[i], keep = __builtin_amdgcn_exp2f(-rise);
+    const int whole = (int)fminf(rise, 1024.f);
     st.m[i] = m;
     st.l[i] *= keep;
 #pragma unroll
-    for (int u = 0; u < DIM / 64; ++u) st.mids[u][i] *= keep;
-    if ((lane & 15) == 0) keeps[(lane >> 4) + 4 * i] = keep;
+    for (int u = 0; u < DIM / 64; ++u) {
+      st.mids[u][i] *= keep;
+      const int ev = exponent_of(st.up[u][i]), now = max(ev - whole, kLeastExponent);
+      st.up[u][i] = ldexpf(1.f, kTop - now);
+      factor[u][i] = ldexpf(keep, ev - now);
+    }
   }
-  wave_lds_sync();
-  const float keep = keeps[(lane & 15) & (4 * N - 1)];  // (other lanes' sums are not used)
-  wave_lds_sync();
+  multiply<DIM, N>(st, factor, room, lane);
+}
+
+// Exponents over the present keys' weights times scales (NaN leaves them) and, but
+// for the FRESH ones, over those so far.
+template <int DIM, int N, bool FRESH>
+__device__ __forceinline__ void set_exponents(State<DIM, N> &st, const float (&w)[2][N], const float (&vs)[2][DIM / 64],
+                                              float *room, int lane) {
+  float factor[DIM / 64][N];
 #pragma unroll
   for (int u = 0; u < DIM / 64; ++u)
 #pragma unroll
-    for (int n = 0; n < 4; ++n) st.o[u][n] *= keep;
-}
-
-// The exponent over 2^ev and the scales of V; size: the lane's greatest.
-__device__ __forceinline__ int exponent_over(int ev, float size) {
-  int e;
-  (void)frexpf(max16(size), &e);  // (the four groups of lanes have the same pairs)
-  return __builtin_amdgcn_readfirstlane(max(ev, min(e, 128)));
+    for (int i = 0; i < N; ++i) {
+      const float most = max16(fmaxf(w[0][i] * vs[0][u], w[1][i] * vs[1][u]));
+      int ev = most > 0.f ? max(__builtin_amdgcn_frexp_expf(most), kLeastExponent) : kLeastExponent;
+      if constexpr (!FRESH) {
+        const int old = exponent_of(st.up[u][i]);
+        ev = max(ev, old);
+        factor[u][i] = ldexpf(1.f, old - ev);
+      }
+      st.up[u][i] = ldexpf(1.f, kTop - ev);
+    }
+  if constexpr (!FRESH) multiply<DIM, N>(st, factor, room, lane);
 }
 
 // Weights of the scores x, into the sums and, times the scales of V, into `lds`
@@ -281,32 +351,13 @@ __device__ __forceinline__ void weigh(State<DIM, N> &st, float (&x)[2][N], const
                                       const Query<DIM, N> &q, uint16_t *lds, bool end, int live, int lane) {
   constexpr int G = DIM / 64;
   float vs[2][G], mid[2][G];
-  float size = 0.f;
 #pragma unroll
   for (int b = 0; b < 2; ++b)
 #pragma unroll
     for (int u = 0; u < G; ++u) {
-      const float scale = act_to_f32<DT>(pairs.v[b][u] & 0xffffu);
-      size = fmaxf(size, scale);
-      mid[b][u] = __builtin_fmaf(8.f, scale, act_to_f32<DT>(pairs.v[b][u] >> 16));
-      vs[b][u] = scale;
+      vs[b][u] = act_to_f32<DT>(pairs.v[b][u] & 0xffffu);
+      mid[b][u] = __builtin_fmaf(8.f, vs[b][u], act_to_f32<DT>(pairs.v[b][u] >> 16));
     }
-  if constexpr (FRESH) {
-    st.ev = exponent_over(st.ev, size);
-  } else if (__any(size >= ldexpf(1.f, st.ev))) {  // seldom
-    const int ev = exponent_over(st.ev, size);
-#pragma unroll
-    for (int u = 0; u < G; ++u)
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st.o[u][n][i] = ldexpf(st.o[u][n][i], st.ev - ev);
-    st.ev = ev;
-  }
-#pragma unroll
-  for (int b = 0; b < 2; ++b)
-#pragma unroll
-    for (int u = 0; u < G; ++u) vs[b][u] = ldexpf(vs[b][u], kTop - st.ev);
   if (q.more) {  // (uniform) a factor that one fp32 number does not hold
     asm volatile("");
 #pragma unroll
@@ -322,36 +373,40 @@ __device__ __forceinline__ void weigh(State<DIM, N> &st, float (&x)[2][N], const
       for (int i = 0; i < N; ++i) x[b][i] = 16 * b + (lane & 15) >= live ? -3e38f : x[b][i];
   }
   float w[2][N];
-  float top = -INFINITY;
-#pragma unroll
-  for (int b = 0; b < 2; ++b)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      w[b][i] = __builtin_fmaf(x[b][i], q.factor[i], -st.m[i]);
-      top = fmaxf(top, w[b][i]);
-    }
-  if (FRESH || __any(top > kSlack)) {
-    if constexpr (FRESH) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) st.m[i] = fmaxf(max16(fmaxf(x[0][i], x[1][i])) * q.factor[i], kLeastMaximum);
-    } else {
-      raise<DIM, N>(st, x, q, reinterpret_cast<float *>(lds), lane);
-    }
+  _Float16 h[2][G][N];  // 2^(kTop - ev) p s
+  // whether (for the wave) one of them is too large (NaN is not)
+  const auto round = [&]() {
+    _Float16 most = 0;
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int i = 0; i < N; ++i) w[b][i] = __builtin_fmaf(x[b][i], q.factor[i], -st.m[i]);
-  }
+      for (int u = 0; u < G; ++u)
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
+        for (int i = 0; i < N; ++i) {
+          h[b][u][i] = (_Float16)__builtin_fmaf(w[b][i] * st.up[u][i], vs[b][u], 0.f);
+          most = __builtin_fmaxf16(most, h[b][u][i]);
+        }
+    return most >= (_Float16)kMost;
+  };
+  float *const room = reinterpret_cast<float *>(lds);
+  if constexpr (FRESH) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[b][i] = __builtin_amdgcn_exp2f(w[b][i]);
-  if (end) {
-    asm volatile("");
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < N; ++i) w[b][i] = 16 * b + (lane & 15) >= live ? 0.f : w[b][i];
+    for (int i = 0; i < N; ++i) st.m[i] = fmaxf(max16(fmaxf(x[0][i], x[1][i])) * q.factor[i], kLeastMaximum);
+    (void)weights_of<DIM, N>(w, x, q, st.m, end, live, lane);
+    set_exponents<DIM, N, true>(st, w, vs, room, lane);
+    (void)round();
+  } else {
+    const float top = weights_of<DIM, N>(w, x, q, st.m, end, live, lane);
+    bool over = round();
+    if (__any(top > kSlack || over)) {  // seldom
+      raise<DIM, N>(st, x, q, room, lane);
+      (void)weights_of<DIM, N>(w, x, q, st.m, end, live, lane);
+      over = round();
+      if (__any(over)) {
+        set_exponents<DIM, N, false>(st, w, vs, room, lane);
+        (void)round();
+      }
+    }
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) st.l[i] += w[0][i] + w[1][i];
@@ -362,10 +417,9 @@ __device__ __forceinline__ void weigh(State<DIM, N> &st, float (&x)[2][N], const
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       st.mids[u][i] = __builtin_fmaf(w[0][i], mid[0][u], __builtin_fmaf(w[1][i], mid[1][u], st.mids[u][i]));
-      const uint32_t h =
-          __builtin_bit_cast(uint32_t, f16x2{(_Float16)(w[0][i] * vs[0][u]), (_Float16)(w[1][i] * vs[1][u])});
-      to[(16 * u + 4 * i) * kWeightRow] = (uint16_t)h;
-      to[(16 * u + 4 * i) * kWeightRow + 4] = (uint16_t)(h >> 16);
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        to[(16 * u + 4 * i) * kWeightRow + 4 * b] = __builtin_bit_cast(uint16_t, h[b][u][i]);
     }
 }
 
@@ -669,7 +723,10 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
 #pragma unroll
           for (int j = 0; j < 4; ++j) st.o[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-        st.ev = kLeastExponent;
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+#pragma unroll
+          for (int i = 0; i < N; ++i) st.up[u][i] = 1.f;
         if (pos < end) {
           uint16_t *weights = reinterpret_cast<uint16_t *>(&lds.o[wave][0][0]);
           Query<DIM, N> q;
@@ -711,7 +768,7 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
         // ---- a wave's sums ----
         {
           // heads g + 4 i, over 16 lanes; then head lane % 16
-          float *own = &lds.o[wave][0][0];  // [quantity][head]
+          float *own = &lds.o[wave][0][0];  // [quantity][head]: sums of mids, up
           const int h = lane & 15, g = lane >> 4;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
@@ -723,13 +780,20 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
               lds.m[wave][g + 4 * i] = st.m[i];
               lds.l[wave][g + 4 * i] = l;
 #pragma unroll
-              for (int u = 0; u < G; ++u) own[16 * u + g + 4 * i] = mids[u];
+              for (int u = 0; u < G; ++u) {
+                own[16 * u + g + 4 * i] = mids[u];
+                own[16 * (G + u) + g + 4 * i] = st.up[u][i];
+              }
             }
           }
           wave_lds_sync();
           float mids[G];
+          int ev[G];
 #pragma unroll
-          for (int u = 0; u < G; ++u) mids[u] = own[16 * u + (h & (4 * N - 1))];
+          for (int u = 0; u < G; ++u) {
+            mids[u] = own[16 * u + (h & (4 * N - 1))];
+            ev[u] = exponent_of(own[16 * (G + u) + (h & (4 * N - 1))]);
+          }
           const float inv = piece.len > 0 ? 1.f / lds.l[wave][h & (4 * N - 1)] : 0.f;
           wave_lds_sync();
           if (h < piece.heads) {
@@ -741,7 +805,7 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
                 const int c = 64 * u + 16 * g + 4 * i;
                 f32x4 y;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = ldexpf(st.o[u][j][i], (j & 1 ? 20 : 24) - kTop + st.ev) + mids[u];
+                for (int j = 0; j < 4; ++j) y[j] = ldexpf(st.o[u][j][i], (j & 1 ? 20 : 24) - kTop + ev[u]) + mids[u];
                 if (LONE) *reinterpret_cast<u32x2 *>(out + c) = piece.len > 0 ? pack_row<DT>(y, inv) : u32x2{0, 0};
                 else *reinterpret_cast<f32x4 *>(&lds.o[wave][h][c]) = y;
               }
