@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(256, 2) decode_attention_kernel(AttentionArgs 
   }
   const int64_t item = (row * a.kv_heads + kvh) * plan.head_tiles + tile;
   const int slots = plan.splits * part_floats(a.group, DIM);
-  join_parts<DT, DIM>(a, lds, counters + item, raw_rsrc(partials + item * slots, (uint32_t)(slots * 4)),
-                      PartsInOrder(), row, head0, heads, split, parts, len > 0);
+  join_parts<DT, DIM, true>(a, lds, counters + item, raw_rsrc(partials + item * slots, (uint32_t)(slots * 4)),
+                            PartsInOrder(), row, head0, heads, split, parts, len > 0);
 }
 
 }  // namespace

@@ -828,8 +828,8 @@ decode4_attention_kernel(AttentionArgs a, Decode4Plan plan, uint32_t *__restrict
           part = (int)blockIdx.x - place.first;
           parts = (int)((done.first + done.steps - 1) / share) - place.first + 1;
         }
-        join_parts<DT, DIM>(a, lds, counters + place.first, rs, place, done.row, done.head0, done.heads, part, parts,
-                            done.len > 0);
+        join_parts<DT, DIM, false>(a, lds, counters + place.first, rs, place, done.row, done.head0, done.heads, part,
+                                   parts, done.len > 0);
       }
       if (!more) break;
       __syncthreads();  // the join's reads of lds are done

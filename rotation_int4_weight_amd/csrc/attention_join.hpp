@@ -6,6 +6,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "attention.hpp"
 #include "common.hpp"
 #include "mfma.hpp"
@@ -14,11 +16,16 @@ namespace paro {
 
 constexpr int kDecodeWaves = 4;  // of a decode workgroup
 constexpr int kCoherent = 16;    // SC1: device-scope loads and stores of the parts
-// Parts that a thread has in flight together.  With 2, 4 and 8 one row of 777 keys
-// takes 8.7, 8.2 and 8.8 us over four bits, 40 rows of up to 1500 9.8, 9.6 and 10.3
-// (over 16 bits 6.9 with 4, 7.3 with 8): the code of a larger batch costs more than
-// a second round of loads; 16 spill registers.
-constexpr int kJoinBatch = 4;
+// Parts that a thread has in flight together.  Over 16 bits eight where it has more
+// than kJoinFew, four otherwise; always four and always eight take, us: one row of
+// 131072 keys with 16 heads on one key-value head 114 and 91 (by this rule 82), with
+// 8 times 16 heads 108 and 105 (105), one of 8000 with 8 times 8 heads 17.1 and
+// 15.6 (15.6), of 777 with 8 times 4 7.0 and 7.4 (7.1).  Over four bits always
+// four: the code of both costs one row of 777 8.5 instead of 8.2 us, 40 rows of up
+// to 1500 13.6 instead of 13.2, for 139 instead of 155 of one row of 131072 keys
+// with 16 heads on one key-value head and 60.6 instead of 63 with 8 times 16.
+// Sixteen in flight spill registers.
+constexpr int kJoinBatch = 4, kJoinFew = 8;  // of a thread
 
 // What the waves hand over: sums relative to 2^m, m the maximum of scores * log2 e.
 template <int DIM>
@@ -75,9 +82,10 @@ __host__ __device__ inline int part_floats(int group, int dim) { return (group <
 // Called by all threads once every wave has written its o, m and l (no barrier
 // needed in between): part `part` of `parts` of the `heads` query heads from
 // head0 of a row.  counter: this output's; rs: the slots (neither is used with
-// one part).  some: the row has a key; without one it is zero.  Storing a part,
-// counting and joining takes 2 to 3 us.
-template <int DT, int DIM, class Place>
+// one part).  some: the row has a key; without one it is zero.  MANY: outputs of
+// many parts have more of them in flight.  Storing a part, counting and joining
+// takes 2 to 3 us.
+template <int DT, int DIM, bool MANY, class Place>
 __device__ __forceinline__ void join_parts(const AttentionArgs &a, DecodeJoin<DIM> &lds, uint32_t *counter,
                                            __amdgpu_buffer_rsrc_t rs, Place place_of, int64_t row, int head0,
                                            int heads, int part, int parts, bool some) {
@@ -125,7 +133,7 @@ __device__ __forceinline__ void join_parts(const AttentionArgs &a, DecodeJoin<DI
   __syncthreads();
   if (!lds.last) return;
   // DIM / 4 threads per head leave room for `lanes` of them per output: each
-  // takes every lanes-th part, kJoinBatch loads in flight together
+  // takes every lanes-th part
   const int lanes = max(1, kHeadsPerPass / heads);
   const int sub = (int)threadIdx.x / kPerHead;
   float *const jo = &lds.o[0][0][0];  // [sub][RS], after the waves' use of o
@@ -133,20 +141,25 @@ __device__ __forceinline__ void join_parts(const AttentionArgs &a, DecodeJoin<DI
     const int h = lanes > 1 ? sub / lanes : h0 + sub, first = lanes > 1 ? sub % lanes : 0;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, sum = 0.f;
-    if (h < heads) {
-      for (int p0 = first; p0 < parts; p0 += kJoinBatch * lanes) {
-        f32x4 x[kJoinBatch];
-        u32x2 ml[kJoinBatch];
+    const auto gather = [&](auto batch) {
+      constexpr int B = decltype(batch)::value;
+      for (int p0 = first; p0 < parts; p0 += B * lanes) {
+        f32x4 x[B];
+        u32x2 ml[B];
 #pragma unroll
-        for (int u = 0; u < kJoinBatch; ++u) {
+        for (int u = 0; u < B; ++u) {
           const uint32_t at = (uint32_t)(place_of(min(p0 + u * lanes, parts - 1)) * slot_floats + h * (DIM + 4)) * 4u;
           x[u] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at + ch * 4, 0, kCoherent));
           ml[u] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, at + DIM * 4, 0, kCoherent));
         }
 #pragma unroll
-        for (int u = 0; u < kJoinBatch; ++u)
+        for (int u = 0; u < B; ++u)
           if (p0 + u * lanes < parts) add_part(o, m, sum, x[u], __uint_as_float(ml[u][0]), __uint_as_float(ml[u][1]));
       }
+    };
+    if (h < heads) {
+      if (MANY && parts > kJoinFew * lanes) gather(std::integral_constant<int, MANY ? 2 * kJoinBatch : kJoinBatch>());
+      else gather(std::integral_constant<int, kJoinBatch>());
     }
     if (lanes > 1) {  // then heads <= kHeadsPerPass / 2: this loop runs once
       __syncthreads();
