@@ -114,8 +114,6 @@ int paro_rotary_frequencies(const paro_rotary_scaling *s, int rot_dim, double *f
                !std::isfinite(s->high)))
     return fail(PARO_ERR_SHAPE, "context must be over 0 and 0 < low < high, all finite");
   const int n = rot_dim / 2;
-  double base = s->base;
-  if (s->kind == PARO_ROTARY_BASE) base *= std::pow(s->factor, (double)rot_dim / (rot_dim - 2));
   // the pair that makes `turns` turns over the context, as a real number
   const auto index = [&](double turns) {
     return rot_dim * std::log(s->context / (turns * kTurn)) / (2 * std::log(s->base));
@@ -126,8 +124,11 @@ int paro_rotary_frequencies(const paro_rotary_scaling *s, int rot_dim, double *f
     last = std::min(std::ceil(index(s->low)), rot_dim - 1.0);
   }
   for (int i = 0; i < n; ++i) {
-    double f = std::pow(base, -2.0 * i / rot_dim);
-    if (s->kind == PARO_ROTARY_LINEAR) {
+    double f = std::pow(s->base, -2.0 * i / rot_dim);
+    if (s->kind == PARO_ROTARY_BASE) {
+      // (base * factor^(rot_dim / (rot_dim - 2)))^(-2i / rot_dim), whose base may be no 64-bit number
+      f *= std::pow(s->factor, -2.0 * i / (rot_dim - 2));
+    } else if (s->kind == PARO_ROTARY_LINEAR) {
       f /= s->factor;
     } else if (ends) {
       // kept: 1 as it is, 0 divided by factor
