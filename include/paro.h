@@ -550,9 +550,10 @@ typedef struct {
  * products and sums are fp32, and y is rounded once.
  *   x, y : [tokens][heads][head_dim] dt in {F16, BF16, F32} with the strides of
  *          `shape`, 16-byte aligned; y may be x with the same strides (in
- *          place), else they must not overlap.  y's rows and heads must not
- *          overlap each other.  The q and the k heads of a fused q/k/v buffer
- *          are one call.
+ *          place), else they must not overlap: with the same strides they may be
+ *          views apart of one buffer, with others they must lie behind one
+ *          another.  y's rows and heads must not overlap each other.  The q and
+ *          the k heads of a fused q/k/v buffer are one call.
  *   positions : DEVICE int32 [tokens], any values.
  *   freqs     : DEVICE double [rot_dim / 2], 8-byte aligned: radians per
  *               position, for example from paro_rotary_frequencies.

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "paro.h"
 
 namespace paro {
@@ -21,6 +23,22 @@ inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintp
 inline bool overlap(const void *a, size_t an, const void *b, size_t bn) {
   const char *pa = (const char *)a, *pb = (const char *)b;
   return an && bn && pa < pb + bn && pb < pa + an;
+}
+
+// Whether two tensors [rows][heads][dim bytes] of the same strides (in bytes, at
+// least 0; that of a single row or head does not matter) share a byte: for each
+// distance in heads, the distances in rows that bring them closest together.
+inline bool strided_overlap(const void *a, const void *b, int64_t rows, int heads, int64_t dim, int64_t row,
+                            int64_t head) {
+  const int64_t delta = (int64_t)((uintptr_t)b - (uintptr_t)a), most = rows - 1;
+  for (int64_t h = 1 - heads; h < heads; ++h) {
+    const int64_t at = delta + (heads > 1 ? h * head : 0), near = rows > 1 && row > 0 ? -at / row : 0;
+    for (int64_t r = near - 1; r <= near + 1; ++r) {
+      const int64_t d = at + (rows > 1 ? std::max(-most, std::min(most, r)) * row : 0);
+      if (d > -dim && d < dim) return true;
+    }
+  }
+  return false;
 }
 
 inline bool act_dtype(int dt) { return dt == PARO_F16 || dt == PARO_BF16; }

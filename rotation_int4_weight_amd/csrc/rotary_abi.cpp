@@ -17,6 +17,7 @@ using paro::fail;
 using paro::hip_fail;
 using paro::ok;
 using paro::overlap;
+using paro::strided_overlap;
 
 constexpr int64_t kMaxRows = int64_t(1) << 21;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
@@ -73,9 +74,10 @@ int paro_rotary(const paro_rotary_shape *s, const void *x, paro_dtype dt, const 
     return fail(PARO_ERR_ALIGN, "positions must be 4-byte aligned, freqs 8-byte aligned");
   const size_t size = dt == PARO_F32 ? 4 : 2;
   const size_t xb = extent(s, tokens, s->x_token, s->x_head, size), yb = extent(s, tokens, s->y_token, s->y_head, size);
-  const bool in_place = x == y && (tokens == 1 || s->x_token == s->y_token) && (s->heads == 1 || s->x_head == s->y_head);
-  if (!in_place && overlap(x, xb, y, yb))
-    return fail(PARO_ERR_SHAPE, "y overlaps x: only the same tensor with the same strides may be both");
+  const bool alike = (tokens == 1 || s->x_token == s->y_token) && (s->heads == 1 || s->x_head == s->y_head);
+  if (!(alike && x == y) && overlap(x, xb, y, yb) &&
+      !(alike && !strided_overlap(x, y, tokens, s->heads, s->head_dim * size, s->y_token * size, s->y_head * size)))
+    return fail(PARO_ERR_SHAPE, "y overlaps x: only the same tensor, or views apart of one, with the same strides");
   if (overlap(y, yb, positions, (size_t)tokens * 4) || overlap(y, yb, freqs, (size_t)s->rot_dim * 4))
     return fail(PARO_ERR_SHAPE, "y overlaps positions or freqs");
   paro::RotaryArgs a = {};
