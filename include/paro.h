@@ -743,8 +743,10 @@ int paro_kv_append(const paro_kv_cache *cache, int layer, const void *k, int64_t
  * the codes stand for, low + scale * code rounded to fp32 and then to out_dt.
  * Rows whose position the slot does not hold (or that it has no valid page for)
  * are set to zero; rows outside every entry are left as they were.  k and v
- * must overlap neither each other, the cache nor the lists, and their rows and
- * heads not one another.  k or v may be NULL (not written).
+ * must overlap neither each other (with the same strides they may be views apart
+ * of one buffer, and with the same token stride their heads may lie side by side
+ * in its rows), the cache nor the lists, and their rows and heads not one another.
+ * k or v may be NULL (not written).
  */
 int paro_kv_read(const paro_kv_cache *cache, int layer, void *k, int64_t k_token, int64_t k_head, void *v,
                  int64_t v_token, int64_t v_head, paro_dtype out_dt, const int32_t *slots, const int64_t *cu,

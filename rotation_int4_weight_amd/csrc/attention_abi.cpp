@@ -21,6 +21,7 @@ using paro::hip_fail;
 using paro::kCounterBytes;
 using paro::ok;
 using paro::overlap;
+using paro::strided_overlap;
 
 constexpr int64_t kMaxRows = int64_t(1) << 21;
 constexpr int kMaxHeads = 256;
@@ -454,8 +455,10 @@ int paro_kv_read(const paro_kv_cache *c, int layer, void *k, int64_t k_token, in
   const size_t kb = k ? extent(tokens, c->kv_heads, c->head_dim, k_token, k_head, size) : 0,
                vb = v ? extent(tokens, c->kv_heads, c->head_dim, v_token, v_head, size) : 0;
   if (overlaps_cache(c, k, kb) || overlaps_cache(c, v, vb)) return fail(PARO_ERR_SHAPE, "k or v overlaps the cache");
-  if (overlap(k, kb, v, vb)) {
-    // views of one buffer: K's and V's heads side by side in every row of the same stride
+  const bool alike = (tokens == 1 || k_token == v_token) && (c->kv_heads == 1 || k_head == v_head);
+  if (overlap(k, kb, v, vb) &&
+      !(alike && !strided_overlap(k, v, tokens, c->kv_heads, c->head_dim * size, k_token * size, k_head * size))) {
+    // with other head strides: K's and V's heads side by side in every row of the same stride
     const uint64_t step = (uint64_t)k_token * size, kr = extent(1, c->kv_heads, c->head_dim, 0, k_head, size),
                    vr = extent(1, c->kv_heads, c->head_dim, 0, v_head, size);
     const uintptr_t a = (uintptr_t)k, b = (uintptr_t)v;

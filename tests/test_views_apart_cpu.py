@@ -8,6 +8,8 @@ import pytest
 paro = pytest.importorskip("rotation_int4_weight_amd")
 pytest.importorskip("torch")
 from rotation_int4_weight_amd import _lib  # noqa: E402
+from test_attention_abi_cpu import K, cache  # noqa: E402
+from test_kv4_abi_cpu import read  # noqa: E402
 from test_rotary_cpu import SHAPE, X, rotary, shape  # noqa: E402
 
 SIZE = {0: 2, 1: 2, 2: 4}
@@ -67,3 +69,36 @@ def test_rotary_at_the_largest_strides():
         n = 1 if kw["heads"] == 3 else 4
         assert rotary(shape(head_dim=16, rot_dim=2, **kw), tokens=n, y=X + 32, freqs=X + 32) == SHAPE
         assert "freqs" in paro.paro_last_error()
+
+
+def test_read_tells_overlaps_from_views_apart():
+    """K and V of one buffer; `first` at K is what is refused where they are no overlap."""
+    seen = set()
+    rng = random.Random(2)
+    while len(seen) < 3 or rng.random() > 0.0005:
+        rows, heads, dim, dt = rng.randint(1, 4), rng.randint(1, 4), 64, rng.randint(0, 1)
+        token, head, delta = (64 * rng.randint(0, 12) + 8 * rng.randint(-1, 1) for _ in range(3))
+        delta *= rng.choice((-1, 1))
+        if min(token, head) < 0 or not apart(rows, heads, token, head, dim):
+            continue
+        out = rng.choice((dt, 2))
+        v = K + SIZE[out] * delta
+        c = cache(dt=dt + 16 * rng.randint(0, 1), head_dim=dim, kv_heads=heads)
+        assert read(c, k=K, kt=token, kh=head, v=v, vt=token, vh=head, out=out, n=1, tokens=rows, first=K) == SHAPE
+        mine, other = elements(0, rows, heads, dim, token, head), elements(delta, rows, heads, dim, token, head)
+        clash, message = bool(mine & other), paro.paro_last_error()
+        assert ("k and v overlap" in message) == clash, (rows, heads, token, head, delta, message)
+        assert clash or "first" in message
+        seen.add((clash, max(mine) >= min(other) and max(other) >= min(mine)))
+
+
+def test_read_of_a_single_row_or_head():
+    """Their strides do not matter."""
+    c = cache(kv_heads=2)
+    assert read(c, k=K, kt=1024, kh=256, v=K + 2 * 128, vt=512, vh=256, tokens=1, first=K) == SHAPE
+    assert "first" in paro.paro_last_error()
+    assert read(c, k=K, kt=1024, kh=256, v=K + 2 * 128, vt=512, vh=256, tokens=2, first=K) == SHAPE
+    assert "k and v overlap" in paro.paro_last_error()
+    c = cache(kv_heads=1)
+    assert read(c, k=K, kt=512, kh=0, v=K + 2 * 128, vt=512, vh=1024, tokens=3, first=K) == SHAPE
+    assert "first" in paro.paro_last_error()
