@@ -113,3 +113,18 @@ def test_scales_and_scores_against_each_other(dim, n, falling):
     # a score falls by log 2 a level
     q = torch.full((1, 4, dim), 1.0, dtype=torch.bfloat16, device="cuda")
     check(c, q, decode(c, q, ints([0]), scale=0.6931471805599453 * 8 / dim), scale=0.6931471805599453 * 8 / dim)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [1, 4, 7, 8, 16, 17, 40])
+def test_ordinary_values(group, dim, dtype):
+    """Rows cut between workgroups, a workgroup for each output, a wave for each, one long row: within the bound that
+    weights what each key can add."""
+    for lengths, slots, kv_heads in (([3000, 700], [0, 1], 2), ([600, 33], [1, 0], 2), ([250, 128, 129, 33], [0, 1, 2, 3] * 200, 2),
+                                     ([2600, 90, 300], [0] + [1, 2] * 150, 2), ([20011], [0], 1)):
+        c = _kv4.fill(paro, lengths, 16, kv_heads, dim, dtype, group)
+        q = rows((len(slots), kv_heads * group, dim), dtype, 5, 1.5)
+        y = decode(c, q, ints(slots))
+        for r in {0, 1, len(slots) // 2, len(slots) - 1} & set(range(len(slots))):
+            _kv4_bounds.check(y[r], q[r], *_kv4_bounds.held(c, 0, slots[r]), _kv4.default_scale(dim))
