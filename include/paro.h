@@ -582,7 +582,8 @@ int paro_rotary(const paro_rotary_shape *shape, const void *x, paro_dtype dt, co
  *   RAMP   by the pair's index: kept up to the pair that makes `high` turns
  *          over the trained context, divided by factor from the one that makes
  *          `low`, with a linear share between (its ends rounded outwards to
- *          whole pairs); *magnitude is 0.1 ln(factor) + 1.
+ *          whole pairs, the first at least 0: pair 0 is kept); *magnitude is
+ *          0.1 ln(factor) + 1.
  * magnitude (may be NULL) is 1 but for RAMP.  context is used by BANDS and RAMP,
  * low and high too (0 < low < high; usually 1 and 4, and 1 and 32).
  * base > 1, factor >= 1, rot_dim even and in 2..512 (BASE: from 4).
@@ -740,7 +741,10 @@ int paro_kv_append(const paro_kv_cache *cache, int layer, const void *k, int64_t
  * paro_kv_append has them.  cu: DEVICE int64 [n + 1], or NULL for one row per
  * entry (tokens == n); entries are clamped as there.  n <= 16384.  From a cache
  * in 16 bits the values are copied, from one in four bits they are those that
- * the codes stand for, low + scale * code rounded to fp32 and then to out_dt.
+ * the codes stand for, low + scale * code rounded to fp32 and then to out_dt (an
+ * infinity where a group spans so much of the type's range that its top code lies
+ * past it).  paro_attention_decode takes them without these roundings: keys and
+ * values read back in 16 bits differ from its own by up to half a step of the type.
  * Rows whose position the slot does not hold (or that it has no valid page for)
  * are set to zero; rows outside every entry are left as they were.  k and v
  * must overlap neither each other (with the same strides they may be views apart

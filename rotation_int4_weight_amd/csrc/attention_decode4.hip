@@ -36,15 +36,18 @@
 // share an output and join their sums; where there are many short ones each wave
 // takes outputs of its own, with nothing to join.  See kOutputUnits, kLoneShare and
 // plan_attention_decode4.
-// What bounds it: where rows are long the bytes, 9/8 per key and channel (9/32 of
-// the 16-bit cache's): two rows of 131072 and 100001 keys (8 heads of 128
-// channels, 32 query heads, 266 MB) take 59 us, 4.5 TB/s, 64 rows of up to 4096
-// (141 MB) 36.9 us.  In its steady state the card takes in 5.2 to 5.6 TB/s (a copy
-// moves 4.8 to 5.0); about 6 us are the start and the join.  One row of 777 keys, 8
-// outputs over 56 workgroups of one step each, 8.2 us: slot and length 1.2, table
-// 1.0, queries and first keys 0.7, the step 1.3, a part stored and counted 1.3,
-// the parts joined 1.6, the rest a launch.
-// Both sides of the choices, us:
+// What bounds it, with 8 key-value heads of 128 channels and 32 query heads: where
+// rows are long the bytes, 9/8 per key and channel (9/32 of the 16-bit cache's).
+// Two rows of 131072 and 100001 keys (266 MB) take 66 us, 64 rows of up to 4096 (141
+// MB) 40, with caches in turn whose bytes together are past the last-level cache's
+// 256 MB: 4.8 TB/s, as a copy, and about 10 us of start, join and uneven ends.  On
+// the same cache again, which that cache then holds in part, 52 to 59 and 33 to 36.
+// With 8, 16 heads per key-value head the 64 rows take 35, 44 us where 4 take 32:
+// the vector instructions of the weights.  One row of 777 keys, 8 outputs over 56
+// workgroups of one step each, 8.2 us: slot and length 1.2, table 1.0, queries and
+// first keys 0.7, the step 1.3, a part stored and counted 1.3, the parts joined 1.6,
+// the rest a launch.  One row of 131072 36 us: 64 parts an output.
+// Both sides of the choices, us, on the same cache again, when each was made:
 //   - two workgroups per CU and one: 37 and 52 (64 rows), 59 and 77 (two rows);
 //     three: 43 and 67, the registers of two tiles and the sums no longer fit.
 //   - a ring of two tiles and of three: 37.4 and 37.6, 59.2 and 60.4.

@@ -19,11 +19,19 @@
 //     by the sign of t - (floor(t / scale) + 1/2) scale.
 //   - So are groups whose scale is near the ends of fp32, moved to its middle by
 //     a power of two first, or subnormal (there 15 may be the limit).
-// What bounds it: 4096 rows of 8 heads of 128 channels are written in 11.0 us
-// (21.5 MB) and read back as 16 bits in 11.4 (21.5 MB): about 5 us are launch and
-// look-ups (64 rows: 4.3 and 4.0 us), the rest 190 vector instructions per 512
-// channels written (all stores left out: 9.0 us), and the bytes of those read
-// (95537 rows: 124 us, 4.9 TB/s, what a copy reaches).
+// What bounds it, in rows of 8 heads of 128 channels (a copy moves 4.8 to 5.0 TB/s):
+//   - 64 rows are written in 4.1 us and read in 3.7, launch and look-ups.
+//   - 4096 are written in 10.8 us (21.5 MB, 4.3 us at a copy's rate).  The waves,
+//     four on a SIMD, wait half of their cycles, for entry, slot, length and page in
+//     turn and then for pieces that are loaded one ahead; vector instructions take
+//     27 % of the cycles.  V's 16-bit words reach memory as 7.3 MB for the 4.7 that
+//     are held.
+//   - 4096 are read as 16 bits in 7.8 us (21.5 MB; 9.7 with buffers in turn past the
+//     last-level cache), as fp32 in 11.9 (38 MB).
+//   - 95537 are read as 16 bits in 125 us: 501 MB, 4.0 TB/s, a quarter over a copy.
+//     The waves wait 80 % of their cycles, and 147 MB are fetched for the 110 that
+//     the rows hold: four waves read V's words of four positions, two bytes at a
+//     time.  A cache in 16 bits (783 MB) is read in 145 us, 5.4 TB/s.
 
 #include <math.h>
 

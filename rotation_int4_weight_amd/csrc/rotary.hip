@@ -12,10 +12,13 @@
 //     fp32 value is off by 2^-26 of a quarter turn; the quarters are put back by
 //     exchanging sine and cosine.  fp32 angles would be off by 2^-24 of the
 //     angle itself, 0.06 radians at position 2^20.
-// What bounds it: bytes, read and written once.  4096 tokens of 40 heads of 128
-// channels (84 MB in 16 bits) take 16.3 us in the kernel, 5.2 TB/s, 2048 tokens of
-// 32 heads in fp32 (67 MB) 11.1; a copy of 1 GiB moves 4.8 to 5.0.  One token 2.6
-// us, a launch; 778 far ones of 14 heads of 64 channels 3.2.
+// What bounds it: bytes, read and written once (counters: 42.2 and 41.9 MB of 41.9).
+// 4096 tokens of 40 heads of 128 channels (84 MB in 16 bits) take 20.9 us with
+// buffers in turn past the last-level cache, 4.0 TB/s, and 14.5 in the same ones
+// again, 2048 tokens of 32 heads in fp32 (67 MB) 16.0 and 12.2; a copy of 1 GiB moves
+// 4.8 to 5.0.  One token 2.6 us, a launch; 778 far ones of 14 heads of 64 channels
+// 3.2.  Units are as wide as the pairs' number allows: 2000 tokens of 24 heads of 128
+// channels (24.6 MB), 128, 124 and 126 of them turned, take 6.3, 9.1 and 11.4.
 #include <math.h>
 
 #include <algorithm>
