@@ -48,35 +48,35 @@ def pages(codes, pairs, page, dtype, key):
     return torch.cat([out.to(torch.uint8), p], -1).view(m, heads, page, dim * 9 // 16)
 
 
-def want(lev, v):
-    """y (kv_heads, dim) of a row that sees all keys, in 64 bits; v of rows_of."""
-    return sh.expected(lev, v, 1)[0]
-
-
-def wrong(got, lev, v, centred=True):
-    """got (rows, q_heads, dim) of rows over the same keys: where it is off by more than it may be.
+def expected(lev, v, q_heads, dtype, centred=True):
+    """(y, limit) (1, q_heads, dim) of a row that sees all keys, in 64 bits; v of rows_of.
 
     Scores are exact products of the level with scale * log2 e, a weight is off by less than 2^-18 of itself (_shares.py),
     and weight times scale, a power of two but for that, rounds to it; the codes' sums are whole numbers of it.  As there
     2^-12 covers moved maxima and joins for both sums, n 2^-24 the sum of the weights, one rounding y.  Plain: each
     key's 8 weight * scale are added exactly and taken off to 2^-18."""
-    y = want(lev, v)
-    y = y.repeat_interleave(got.shape[1] // y.shape[0], 0)[None]
-    n = lev.shape[0]
-    limit = y * (sh.HALF_STEP[got.dtype] + 2.0 ** -12 + (n + 64) * 2.0 ** -24)
-    limit = limit + (2.0 ** -25 if got.dtype == torch.float16 else 0.0)
+    w, n = 2.0 ** lev.to(v.device).double(), lev.shape[0]
+    y = (w[:, None, None] * v.double()).sum(0) / w.sum()
+    y = y.repeat_interleave(q_heads // v.shape[1], 0)[None]
+    limit = y * (sh.HALF_STEP[dtype] + 2.0 ** -12 + (n + 64) * 2.0 ** -24)
+    limit = limit + (2.0 ** -25 if dtype == torch.float16 else 0.0)
     if not centred:
-        limit = limit + 8 * n * 2.0 ** (sh.TOP - 18) / float((2.0 ** lev.double()).sum())
-    return ~((got.double() - y.to(got.device)).abs() <= limit.to(got.device))
+        limit = limit + 8 * n * 2.0 ** (sh.TOP - 18) / w.sum()
+    return y, limit
+
+
+def wrong(got, y, limit):
+    """Where got (rows, q_heads, dim) of rows over the same keys is off by more than it may be."""
+    return ~((got.double() - y).abs() <= limit)
 
 
 def check(got, lev, v, centred=True):
-    bad = wrong(got, lev, v, centred)
+    y, limit = expected(lev, v, got.shape[1], got.dtype, centred)
+    bad = wrong(got, y, limit)
     if bool(bad.any()):
         at = tuple(torch.nonzero(bad)[0].tolist())
-        y = want(lev, v).repeat_interleave(got.shape[1] // v.shape[1], 0)
         raise AssertionError(f"{int(bad.sum())} values of {bad.numel()} wrong, first at (row, head, channel) {at}: "
-                             f"{float(got[at]):.6g}, {float(y[at[1:]]):.6g} expected")
+                             f"{float(got[at]):.6g}, {float(y[0][at[1:]]):.6g} expected")
 
 
 def _constant(text, name):

@@ -11,10 +11,17 @@ import _shares4 as s4  # noqa: E402
 TYPES = (torch.float16, torch.bfloat16)
 
 
-def outputs(lev, v, counts, dtype):
-    """What a kernel gives that counts key j counts[j] times: (1, kv_heads, dim)."""
-    w = 2.0 ** lev.double() * counts
-    return ((w[:, None, None] * v.double()).sum(0) / w.sum()).to(dtype)[None]
+class Outputs:
+    """What a kernel gives that counts some keys more or less often than once: (1, kv_heads, dim)."""
+
+    def __init__(self, lev, v, dtype):
+        self.w, self.dtype = 2.0 ** lev.double(), dtype
+        self.terms = self.w[:, None, None] * v.double()
+        self.sums = self.terms.sum(0), self.w.sum()
+
+    def __call__(self, keys=slice(0, 0), more=0):
+        y = (self.sums[0] + more * self.terms[keys].sum(0)) / (self.sums[1] + more * self.w[keys].sum())
+        return y.to(self.dtype)[None]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -28,22 +35,18 @@ def test_a_lost_or_doubled_key_is_noticed(n, dim, centred, pattern, dtype):
         _, _, v = s4.rows_of(lev, 1, dim, which, centred=centred)
         seen = (v > 0).any(-1)[:, 0]
         total += seen
-        ones = torch.ones(n, dtype=torch.float64)
-        assert not s4.wrong(outputs(lev, v, ones, dtype), lev, v, centred).any()
-        assert s4.wrong(torch.zeros_like(outputs(lev, v, ones, dtype)), lev, v, centred).any()
+        out, right = Outputs(lev, v, dtype), s4.expected(lev, v, 1, dtype, centred)
+        assert not s4.wrong(out(), *right).any()
+        assert s4.wrong(torch.zeros_like(out()), *right).any()
         keys = torch.nonzero(seen).flatten().tolist()
         for j in {keys[0], keys[-1], keys[len(keys) // 2], keys[len(keys) // 3]}:
-            for times in (0.0, 2.0):
-                counts = ones.clone()
-                counts[j] = times
-                assert s4.wrong(outputs(lev, v, counts, dtype), lev, v, centred).any(), (j, times)
+            for more in (-1, 1):
+                assert s4.wrong(out([j], more), *right).any(), (j, more)
         for length in (32, 128, 384):  # a wave's step, a workgroup's, a part
             for first in range(0, n, max(length, n // 5 // length * length)):
-                counts = ones.clone()
-                counts[first:first + length] = 0.0
                 # (a window's own keys may lack as much as the sum of the weights does: 3 of a channel's 16 beside one of
                 # 4096 in 24106; another window's do not)
-                if length < n and s4.wrong(outputs(lev, v, counts, dtype), lev, v, centred).any():
+                if length < n and s4.wrong(out(slice(first, first + length), -1), *right).any():
                     noticed.add((length, first))
     assert bool((total == 1).all())  # one head's windows cover every key once
     assert noticed == {(length, first) for length in (32, 128, 384) if length < n
